@@ -13,7 +13,9 @@ FlashKDA README digest): q, k, g bf16 [B, T, H, 128]; v bf16 [B, T, H, 128];
 beta bf16 [B, T, H] (logits); out bf16 [B, T, H, 128] written in place;
 A_log fp32 [H]; dt_bias fp32 [H, 128]; lower_bound in [-5, 0]; states bf16 or
 fp32 [B|N, H, 128, 128] with equal dtypes; cu_seqlens int64 [N+1] with B = 1.
-Returns None. There is no CPU fallback: if libkda.so is missing or fails to
+Returns None. Beside it: ``fwd_slots`` (KDA on a cache's slots) and ``cache_*``, the
+gated linear recurrence ``glr_*`` and layer norm ``layernorm_*``, in the same manner.
+There is no CPU fallback: if libkda.so is missing or fails to
 load, every call raises.
 """
 from __future__ import annotations
@@ -25,7 +27,10 @@ from typing import Optional
 import torch
 
 __all__ = ["fwd", "fwd_recurrent", "workspace_size", "workspace_min", "record_bytes", "lib", "KDAError", "status_string", "LIB_PATH",
-           "profile_start", "profile_stop"]
+           "profile_start", "profile_stop",
+           "fwd_slots", "cache_copy", "cache_fork", "cache_free", "cache_compact",
+           "glr_fwd", "glr_bwd", "glr_step", "glr_carry_shape", "glr_workspace_size",
+           "layernorm_fwd", "layernorm_bwd", "layernorm_workspace_size"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -83,6 +88,7 @@ def _setup(L):
     L.kda_profile_kernel_count.argtypes = []
     L.kda_profile_kernel_name.restype = ctypes.c_char_p
     L.kda_profile_kernel_name.argtypes = [I]
+    _ops._setup(L)
     return L
 
 
@@ -264,3 +270,8 @@ def profile_stop() -> dict:
     if rc != 0:
         raise KDAError(rc, status_string(rc))
     return {L.kda_profile_kernel_name(i).decode(): (ms[i], cnt[i]) for i in range(n)}
+
+
+from . import _ops  # noqa: E402  (its wrappers use the helpers above)
+from ._ops import (cache_compact, cache_copy, cache_fork, cache_free, fwd_slots, glr_bwd, glr_carry_shape,  # noqa: E402
+                   glr_fwd, glr_step, glr_workspace_size, layernorm_bwd, layernorm_fwd, layernorm_workspace_size)

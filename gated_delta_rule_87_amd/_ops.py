@@ -1,0 +1,345 @@
+"""Python binding of the operators beside kda_fwd: caches of states in slots, the gated
+linear recurrence, layer norm (include/kda.h). Argument marshalling only, as in the
+package's __init__: outputs are the caller's tensors, written in place; contiguous GPU
+tensors of one device; work goes to that device's current stream."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+
+import gated_delta_rule_87_amd as _kda
+
+P, I64, I, SZ, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_DTYPES = {torch.bfloat16: 1, torch.float32: 2, torch.float16: 3}
+_NULL = contextlib.nullcontext()
+
+
+def _setup(L):
+    """Declare the C signatures of the operators on a loaded libkda.so."""
+    def sig(name, restype, *args):
+        f = getattr(L, name)
+        f.restype, f.argtypes = restype, list(args)
+    sig("kda_cache_workspace_size", SZ, I64)
+    sig("kda_cache_copy", I, P, I64, I64, SZ, P, P, I64, P)
+    sig("kda_cache_fork", I, P, I64, I64, SZ, P, P, P, I64, P)
+    sig("kda_cache_free", I, P, I64, P, I64, P)
+    sig("kda_cache_compact", I, P, I64, I64, SZ, P, P, P, I64, P, SZ, P)
+    sig("kda_fwd_slots", I, P, P, P, P, P, F, P, P, P, F, P, I, I64, P, P, P, I64, I64, I64, I64, I64, I64,
+        ctypes.c_uint32, P)
+    sig("kda_glr_carry_rows", I64, I64, I64)
+    sig("kda_glr_workspace_size", SZ, I64, I64, I64, I64)
+    sig("kda_glr_fwd", I, P, P, P, I, P, I, P, I, P, P, I64, I64, I64, I64, P, SZ, P)
+    sig("kda_glr_bwd", I, P, P, P, I, P, P, I, P, I, P, P, P, I, P, I64, I64, I64, I64, P, SZ, P)
+    sig("kda_glr_step", I, P, P, P, I, P, I, I64, P, P, I64, I64, P)
+    sig("kda_layernorm_workspace_size", SZ, I64, I64)
+    sig("kda_layernorm_fwd", I, P, P, P, F, P, I, P, P, I64, I64, P)
+    sig("kda_layernorm_bwd", I, P, P, P, P, P, P, I, P, P, I64, I64, P, SZ, P)
+
+
+def _on(device):
+    """The device of the call's tensors as the current one (its context only where it is another)."""
+    return _NULL if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _done(rc: int) -> None:
+    if rc != 0:
+        raise _kda.KDAError(rc, _kda.status_string(rc))
+
+
+def _gpu(name, t, dim=None) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    return t.device
+
+
+def _dtype(name, t) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bf16, fp32 or fp16, got {t.dtype}")
+    return code
+
+
+def _space(workspace, need: int, device):
+    """The caller's workspace, or one from the caching allocator."""
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def _bytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+# ---- caches of states -------------------------------------------------------------
+
+
+def _pool(pool):
+    dev = _gpu("pool", pool)
+    if pool.dim() < 2:
+        raise ValueError("pool must be [layers, slots, ...]")
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    if pool.numel() == 0:
+        raise ValueError("pool must hold a layer, a slot and an element of state")
+    L, S = pool.shape[:2]
+    return dev, L, S, _bytes(pool) // (L * S)
+
+
+def _slots(name, t, dev, n=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D tensor")
+    _kda._check(name, t, torch.int32, (t.numel() if n is None else n,), dev)
+    return t.numel()
+
+
+def cache_copy(pool, src, dst) -> None:
+    """In every layer of ``pool`` [layers, slots, ...] slot ``dst[i]`` becomes a copy of slot
+    ``src[i]`` (int32 [n] on the device; kda_cache_copy)."""
+    dev, L, S, size = _pool(pool)
+    n = _slots("src", src, dev)
+    _slots("dst", dst, dev, n)
+    with _on(dev):
+        _done(_kda.lib().kda_cache_copy(pool.data_ptr(), L, S, size, src.data_ptr(), dst.data_ptr(), n,
+                                        _kda._stream_ptr(dev)))
+
+
+def cache_fork(pool, used, src, dst) -> None:
+    """New slots: request i copies the used slot ``src[i]``, or begins at zeros where it is
+    -1, into the lowest free slot, whose number is written to ``dst[i]`` (-1 where there is
+    none) and whose flag in ``used`` (int32 [slots]) is set (kda_cache_fork)."""
+    dev, L, S, size = _pool(pool)
+    _slots("used", used, dev, S)
+    n = _slots("src", src, dev)
+    _slots("dst", dst, dev, n)
+    with _on(dev):
+        _done(_kda.lib().kda_cache_fork(pool.data_ptr(), L, S, size, used.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                        n, _kda._stream_ptr(dev)))
+
+
+def cache_free(used, slots) -> None:
+    """Clears the flags of ``slots`` in ``used``; numbers outside the cache are passed over
+    (kda_cache_free)."""
+    dev = _gpu("used", used, 1)
+    S = _slots("used", used, dev)
+    n = _slots("slots", slots, dev)
+    with _on(dev):
+        _done(_kda.lib().kda_cache_free(used.data_ptr(), S, slots.data_ptr(), n, _kda._stream_ptr(dev)))
+
+
+def cache_compact(pool, used, remap, table=None, workspace: Optional[torch.Tensor] = None) -> None:
+    """Moves the used slots of ``pool`` to its front; writes each slot's new number (-1: it
+    was free) to ``remap`` (int32 [slots]), rewrites ``used``, and puts new numbers for the
+    slots in ``table`` (int32 [n] or None) in place (kda_cache_compact)."""
+    dev, L, S, size = _pool(pool)
+    _slots("used", used, dev, S)
+    _slots("remap", remap, dev, S)
+    n = 0 if table is None else _slots("table", table, dev)
+    lib = _kda.lib()
+    with _on(dev):
+        ws = _space(workspace, lib.kda_cache_workspace_size(S), dev)
+        _done(lib.kda_cache_compact(pool.data_ptr(), L, S, size, used.data_ptr(), remap.data_ptr(), _kda._ptr(table), n,
+                                    ws.data_ptr(), _bytes(ws), _kda._stream_ptr(dev)))
+
+
+def fwd_slots(q, k, v, g, beta, scale: float, out, A_log, dt_bias, lower_bound: float, state, in_slots, out_slots,
+              cu_seqlens=None, use_gate_in_kernel: bool = True, use_qk_l2norm_in_kernel: bool = True,
+              use_beta_sigmoid_in_kernel: bool = True, safe_gate: bool = True) -> None:
+    """fwd_recurrent with the states in a cache's layer ``state`` [slots, H, V, K]: sequence n
+    starts from slot ``in_slots[n]`` (zeros for a number outside the cache) and leaves its
+    state in slot ``out_slots[n]`` (kda_fwd_slots)."""
+    flags = _kda._flags(use_gate_in_kernel, use_qk_l2norm_in_kernel, use_beta_sigmoid_in_kernel, safe_gate)
+    B, T, H, K, V, N = _kda._prepare(q, k, v, g, beta, out, A_log, dt_bias, None, None, cu_seqlens,
+                                     gate_fused=use_gate_in_kernel)
+    dev = q.device
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a 4-D tensor [slots, H, V, K]")
+    S = state.shape[0]
+    _kda._check("state", state, state.dtype, (S, H, V, K), dev)
+    n = N if cu_seqlens is not None else B
+    _slots("in_slots", in_slots, dev, n)
+    _slots("out_slots", out_slots, dev, n)
+    ptr = _kda._ptr
+    with _on(dev):
+        _done(_kda.lib().kda_fwd_slots(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), float(scale), ptr(out), ptr(A_log),
+                                       ptr(dt_bias), float(lower_bound), ptr(state), _kda._state_code(state), S,
+                                       ptr(in_slots), ptr(out_slots), ptr(cu_seqlens), N, B, T, H, K, V, flags,
+                                       _kda._stream_ptr(dev)))
+
+
+# ---- gated linear recurrence --------------------------------------------------------
+
+
+def _glr_sizes(x, cu_seqlens, dev):
+    B, T, D = x.shape
+    N = 0
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("cu_seqlens requires B == 1")
+        if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be int64 [N+1] with N >= 1")
+        _kda._check("cu_seqlens", cu_seqlens, torch.int64, tuple(cu_seqlens.shape), dev)
+        N = cu_seqlens.numel() - 1
+    return B, T, D, N
+
+
+def _state(name, t, shape, dev) -> int:
+    if t is not None:
+        _kda._check(name, t, t.dtype, shape, dev)
+    return _kda._state_code(t)
+
+
+def glr_carry_shape(B: int, T: int, D: int) -> tuple:
+    """Shape of the fp32 ``carry`` that glr_fwd saves for glr_bwd."""
+    return int(_kda.lib().kda_glr_carry_rows(int(B), int(T))), int(D)
+
+
+def glr_workspace_size(B: int, T: int, D: int, N: int = 0) -> int:
+    """Bytes of workspace glr_fwd and glr_bwd need (N = number of sequences with cu_seqlens, else 0)."""
+    return int(_kda.lib().kda_glr_workspace_size(int(B), int(T), int(D), int(N)))
+
+
+def glr_fwd(x, g, y, initial_state=None, final_state=None, cu_seqlens=None, carry=None,
+            workspace: Optional[torch.Tensor] = None) -> None:
+    """Gated linear recurrence ``h_t = exp(g_t) h_{t-1} + x_t`` per channel, ``y_t = h_t``;
+    writes ``y`` (and ``final_state``, and ``carry`` for the backward pass) in place.
+
+    x, g, y [B, T, D] of one dtype (bf16, fp32 or fp16); states bf16/fp32 [B|N, D]; carry
+    fp32 of glr_carry_shape (kda_glr_fwd)."""
+    dev = _gpu("x", x, 3)
+    B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
+    dt = _dtype("x", x)
+    _kda._check("g", g, x.dtype, x.shape, dev)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
+    n = N if cu_seqlens is not None else B
+    ic = _state("initial_state", initial_state, (n, D), dev)
+    fc = _state("final_state", final_state, (n, D), dev)
+    if ic and fc and ic != fc:
+        raise ValueError("initial_state and final_state must have the same dtype")
+    lib = _kda.lib()
+    if carry is not None:
+        _kda._check("carry", carry, torch.float32, (lib.kda_glr_carry_rows(B, T), D), dev)
+    ptr = _kda._ptr
+    with _on(dev):
+        ws = _space(workspace, lib.kda_glr_workspace_size(B, T, D, N), dev)
+        _done(lib.kda_glr_fwd(ptr(x), ptr(g), ptr(y), dt, ptr(initial_state), ic, ptr(final_state), fc, ptr(carry),
+                              ptr(cu_seqlens), N, B, T, D, ptr(ws), _bytes(ws), _kda._stream_ptr(dev)))
+
+
+def glr_bwd(x, g, dy, carry, dx, dg, initial_state=None, d_final=None, d_initial=None, cu_seqlens=None,
+            workspace: Optional[torch.Tensor] = None) -> None:
+    """Backward pass of glr_fwd: writes ``dx``, ``dg`` (like x) and ``d_initial`` ([B|N, D] or
+    None) from ``dy`` and ``d_final`` (None: zero). ``carry`` is what glr_fwd saved for the
+    same x, g, initial_state and cu_seqlens (kda_glr_bwd)."""
+    dev = _gpu("x", x, 3)
+    B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
+    dt = _dtype("x", x)
+    for name, t in (("x", x), ("g", g), ("dy", dy), ("dx", dx), ("dg", dg)):
+        _kda._check(name, t, x.dtype, x.shape, dev)
+    lib = _kda.lib()
+    _kda._check("carry", carry, torch.float32, (lib.kda_glr_carry_rows(B, T), D), dev)
+    n = N if cu_seqlens is not None else B
+    ic = _state("initial_state", initial_state, (n, D), dev)
+    fc = _state("d_final", d_final, (n, D), dev)
+    dc = _state("d_initial", d_initial, (n, D), dev)
+    ptr = _kda._ptr
+    with _on(dev):
+        ws = _space(workspace, lib.kda_glr_workspace_size(B, T, D, N), dev)
+        _done(lib.kda_glr_bwd(ptr(x), ptr(g), ptr(dy), dt, ptr(carry), ptr(initial_state), ic, ptr(d_final), fc, ptr(dx),
+                              ptr(dg), ptr(d_initial), dc, ptr(cu_seqlens), N, B, T, D, ptr(ws), _bytes(ws),
+                              _kda._stream_ptr(dev)))
+
+
+def glr_step(x, g, y, state, in_slots, out_slots) -> None:
+    """One token of the recurrence for each of N sequences, x, g, y [N, D]: the states are
+    read from slots ``in_slots`` and left in slots ``out_slots`` (int32 [N]) of a cache's
+    layer ``state`` [slots, D] (kda_glr_step)."""
+    dev = _gpu("x", x, 2)
+    N, D = x.shape
+    dt = _dtype("x", x)
+    for name, t in (("x", x), ("g", g), ("y", y)):
+        _kda._check(name, t, x.dtype, x.shape, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be a 2-D tensor [slots, D]")
+    _kda._check("state", state, state.dtype, (state.shape[0], D), dev)
+    _slots("in_slots", in_slots, dev, N)
+    _slots("out_slots", out_slots, dev, N)
+    with _on(dev):
+        _done(_kda.lib().kda_glr_step(x.data_ptr(), g.data_ptr(), y.data_ptr(), dt, state.data_ptr(),
+                                      _kda._state_code(state), state.shape[0], in_slots.data_ptr(),
+                                      out_slots.data_ptr(), N, D, _kda._stream_ptr(dev)))
+
+
+# ---- layer norm -----------------------------------------------------------------------
+
+
+def _rows(x):
+    dev = _gpu("x", x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., D] with D >= 1")
+    D = x.shape[-1]
+    return dev, x.numel() // D, D, _dtype("x", x)
+
+
+def _vector(name, t, n, dev):
+    if t is not None:
+        if not isinstance(t, torch.Tensor) or t.numel() != n:
+            raise ValueError(f"{name} must hold {n} elements")
+        _kda._check(name, t, torch.float32, t.shape, dev)
+
+
+def layernorm_workspace_size(M: int, D: int) -> int:
+    """Bytes of workspace layernorm_bwd needs for the weight's and the bias's gradient."""
+    return int(_kda.lib().kda_layernorm_workspace_size(int(M), int(D)))
+
+
+def layernorm_fwd(x, weight, bias, eps: float, y, mean=None, rstd=None) -> None:
+    """Layer norm over the last dimension of ``x`` [..., D] (bf16, fp32 or fp16) into ``y``
+    (which may be x); weight and bias fp32 [D] or None; each row's mean and 1 / sqrt(variance
+    + eps) into ``mean`` and ``rstd`` (fp32, one per row) where given (kda_layernorm_fwd)."""
+    dev, M, D, dt = _rows(x)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
+    _vector("weight", weight, D, dev)
+    _vector("bias", bias, D, dev)
+    _vector("mean", mean, M, dev)
+    _vector("rstd", rstd, M, dev)
+    ptr = _kda._ptr
+    with _on(dev):
+        _done(_kda.lib().kda_layernorm_fwd(ptr(x), ptr(weight), ptr(bias), float(eps), ptr(y), dt, ptr(mean), ptr(rstd),
+                                           M, D, _kda._stream_ptr(dev)))
+
+
+def layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight=None, d_bias=None,
+                  workspace: Optional[torch.Tensor] = None) -> None:
+    """Backward pass of layernorm_fwd from its ``mean`` and ``rstd``: ``dx`` like x (it may be
+    dy or x, or None), ``d_weight`` and ``d_bias`` fp32 [D] or None (kda_layernorm_bwd)."""
+    dev, M, D, dt = _rows(x)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("dy", dy, x.dtype, x.shape, dev)
+    if dx is not None:
+        _kda._check("dx", dx, x.dtype, x.shape, dev)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are required")
+    for name, t, n in (("weight", weight, D), ("mean", mean, M), ("rstd", rstd, M), ("d_weight", d_weight, D),
+                       ("d_bias", d_bias, D)):
+        _vector(name, t, n, dev)
+    lib = _kda.lib()
+    ptr = _kda._ptr
+    with _on(dev):
+        ws = None
+        if d_weight is not None or d_bias is not None:
+            ws = _space(workspace, lib.kda_layernorm_workspace_size(M, D), dev)
+        _done(lib.kda_layernorm_bwd(ptr(dy), ptr(x), ptr(weight), ptr(mean), ptr(rstd), ptr(dx), dt, ptr(d_weight),
+                                    ptr(d_bias), M, D, ptr(ws), 0 if ws is None else _bytes(ws), _kda._stream_ptr(dev)))

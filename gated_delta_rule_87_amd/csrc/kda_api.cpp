@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/kda.h"
+#include "kda_api_util.h"
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -26,9 +27,11 @@ static_assert(kda::FUSE_GATE == KDA_FUSE_GATE && kda::FUSE_QK_L2NORM == KDA_FUSE
                   kda::FUSE_BETA_SIGMOID == KDA_FUSE_BETA_SIGMOID && kda::GATE_UNBOUNDED == KDA_GATE_UNBOUNDED,
               "switch values");
 
-constexpr size_t ALIGN = 256;
-
-inline size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
+using kda::ALIGN;
+using kda::align_up;
+using kda::aligned;
+using kda::env_flag;
+using kda::validate_cu_on_host;
 
 struct Layout {
   int64_t max_chunks = 0;
@@ -97,8 +100,6 @@ bool make_layout(int64_t B, int64_t T, int64_t H, int64_t N, bool varlen, Layout
   L.total = off;
   return true;
 }
-
-inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Fixed-length calls given less workspace than the full layout run in windows of chunk
 // columns: launch pair w covers chunks jb = w * nc_win .. jb + nc_win - 1 of every row
@@ -196,11 +197,6 @@ inline bool short_call(int64_t T, int64_t N, bool varlen) {
   return varlen ? T <= REC_MAX_AVG * N : T <= REC_MAX_T;
 }
 
-bool env_flag(const char* name) {
-  const char* s = std::getenv(name);
-  return s && s[0] == '1';
-}
-
 // Shared argument checks of both entry points.
 int check_common(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale,
                  const void* out, const float* A_log, const float* dt_bias, float lower_bound,
@@ -236,23 +232,6 @@ int check_common(const void* q, const void* k, const void* v, const void* g, con
   if (final_state && !aligned(final_state, 16)) return KDA_ERR_ALIGN;
   if (cu_seqlens && !aligned(cu_seqlens, 8)) return KDA_ERR_ALIGN;
   return KDA_OK;
-}
-
-// Copies the boundaries to the host in pieces through a stack buffer (no allocation).
-int validate_cu_on_host(const int64_t* cu, int64_t N, int64_t T, hipStream_t stream) {
-  if (hipStreamSynchronize(stream) != hipSuccess) return KDA_ERR_HIP;
-  constexpr int64_t PIECE = 512;
-  int64_t h[PIECE];
-  int64_t prev = 0;
-  for (int64_t i0 = 0; i0 <= N; i0 += PIECE) {
-    const int64_t n = (N + 1 - i0) < PIECE ? (N + 1 - i0) : PIECE;
-    if (hipMemcpy(h, cu + i0, sizeof(int64_t) * (size_t)n, hipMemcpyDeviceToHost) != hipSuccess) return KDA_ERR_HIP;
-    for (int64_t i = 0; i < n; ++i) {
-      if (i0 + i == 0 ? h[i] != 0 : h[i] < prev) return KDA_ERR_VALUE;
-      prev = h[i];
-    }
-  }
-  return prev == T ? KDA_OK : KDA_ERR_VALUE;
 }
 
 kda::FwdParams make_params(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -561,15 +540,44 @@ int kda_fwd_recurrent_ex(const void* q, const void* k, const void* v, const void
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
+int kda_fwd_slots(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale, void* out,
+                  const float* A_log, const float* dt_bias, float lower_bound, void* state, int state_dtype, int64_t S,
+                  const int32_t* in_slots, const int32_t* out_slots, const int64_t* cu_seqlens, int64_t N, int64_t B,
+                  int64_t T, int64_t H, int64_t K, int64_t V, uint32_t flags, void* stream) {
+  if (flags & KDA_PATH_CHUNKED) return KDA_ERR_VALUE;
+  if (!state || !in_slots || !out_slots) return KDA_ERR_NULL;
+  if (state_dtype != KDA_STATE_BF16 && state_dtype != KDA_STATE_FP32) return KDA_ERR_DTYPE;
+  int rc = check_common(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, state, state_dtype, state,
+                        state_dtype, cu_seqlens, N, B, T, H, K, V, flags);
+  if (rc != KDA_OK) return rc;
+  if (S < 1 || S > kda::MAX_SLOTS) return KDA_ERR_SHAPE;
+  if (!aligned(in_slots, 4) || !aligned(out_slots, 4)) return KDA_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool varlen = cu_seqlens != nullptr;
+  if (varlen && env_flag("KDA_VALIDATE")) {
+    rc = validate_cu_on_host(cu_seqlens, N, T, st);
+    if (rc != KDA_OK) return rc;
+  }
+  kda::FwdParams p = make_params(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, state, state_dtype, state,
+                                 state_dtype, H, flags);
+  p.map.T = (int32_t)T;
+  p.map.nseq = (int32_t)(varlen ? N : B);
+  p.in_slots = in_slots;
+  p.out_slots = out_slots;
+  p.n_slots = (int32_t)S;
+  const hipError_t e = kda::launch_recurrent(p, cu_seqlens, st);
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
 const char* kda_status_string(int status) {
   switch (status) {
     case KDA_OK: return "KDA_OK: success";
     case KDA_ERR_NULL: return "KDA_ERR_NULL: a required pointer is NULL";
-    case KDA_ERR_SHAPE: return "KDA_ERR_SHAPE: unsupported or inconsistent sizes (K = V = 128, B = 1 with cu_seqlens)";
-    case KDA_ERR_DTYPE: return "KDA_ERR_DTYPE: unknown state dtype or initial/final state dtypes differ";
-    case KDA_ERR_VALUE: return "KDA_ERR_VALUE: lower_bound outside [-5, 0], non-finite scale, or bad cu_seqlens";
+    case KDA_ERR_SHAPE: return "KDA_ERR_SHAPE: unsupported or inconsistent sizes (KDA: K = V = 128; B = 1 with cu_seqlens)";
+    case KDA_ERR_DTYPE: return "KDA_ERR_DTYPE: unknown dtype or initial/final state dtypes differ";
+    case KDA_ERR_VALUE: return "KDA_ERR_VALUE: lower_bound outside [-5, 0], non-finite scale, bad eps, unknown flags, or bad cu_seqlens";
     case KDA_ERR_ALIGN: return "KDA_ERR_ALIGN: pointer not aligned (16 bytes; workspace 256 bytes)";
-    case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE: workspace missing or smaller than kda_fwd_workspace_size";
+    case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE: workspace missing or smaller than the call needs";
     case KDA_ERR_HIP: return "KDA_ERR_HIP: HIP runtime or kernel launch error";
     case KDA_ERR_CAPACITY:
       return "KDA_ERR_CAPACITY: the call needs more workspace than kda_fwd_noalloc's fixed array (256 MiB) holds";

@@ -1,0 +1,132 @@
+// kda_elem.h -- loads and stores of a few neighbouring elements of bf16, fp32 or fp16
+// tensors as fp32, for the kernels that take all three (kda_glr*.hip, kda_layernorm.hip).
+#pragma once
+
+#include "kda_device.h"
+
+namespace kda {
+
+// element types (KDA_BF16, KDA_FP32, KDA_FP16 of the public header; the first two are also
+// the state codes)
+constexpr int BF16 = 1, FP32 = 2, FP16 = 3;
+constexpr int elem_size(int dt) { return dt == FP32 ? 4 : 2; }
+
+template <int BYTES>
+struct RawOf;
+template <>
+struct RawOf<2> { using type = uint16_t; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+template <>
+struct RawOf<8> { using type = u32x2; };
+template <>
+struct RawOf<16> { using type = u32x4; };
+
+template <int DT>
+__device__ __forceinline__ float elem_to_f32(uint16_t h) {
+  if constexpr (DT == BF16) return bf16_to_f32(h);
+  else return (float)__builtin_bit_cast(_Float16, h);
+}
+
+// N neighbouring elements of type DT as they lie in memory (at most 16 bytes, aligned to
+// their size)
+template <int DT, int N>
+struct Pack {
+  using Raw = typename RawOf<N * elem_size(DT)>::type;
+  Raw r;
+
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    r = *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p) + i * elem_size(DT));
+  }
+  __device__ __forceinline__ void clear() { r = Raw{}; }
+
+  __device__ __forceinline__ void unpack(float* f) const {
+    if constexpr (DT == FP32) {
+      if constexpr (N == 1) f[0] = __uint_as_float(r);
+      else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = __uint_as_float(r[i]);
+      }
+    } else if constexpr (N == 1) {
+      f[0] = elem_to_f32<DT>(r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        uint32_t w;
+        if constexpr (N == 2) w = r;
+        else w = r[i];
+        if constexpr (DT == BF16) {
+          f[2 * i] = bf16_lo(w);
+          f[2 * i + 1] = bf16_hi(w);
+        } else {
+          const f32x2 v = unpack_f16x2(w);
+          f[2 * i] = v.x;
+          f[2 * i + 1] = v.y;
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void pack(const float* f) {
+    if constexpr (DT == FP32) {
+      if constexpr (N == 1) r = __float_as_uint(f[0]);
+      else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[i]);
+      }
+    } else if constexpr (N == 1) {
+      r = DT == BF16 ? to_bf16(f[0]) : to_f16(f[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const uint32_t w = DT == BF16 ? pack_bf16x2(f[2 * i], f[2 * i + 1]) : pack_f16x2(f[2 * i], f[2 * i + 1]);
+        if constexpr (N == 2) r = w;
+        else r[i] = w;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(void* p, size_t i) const {
+    *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + i * elem_size(DT)) = r;
+  }
+};
+
+template <int DT, int N>
+__device__ __forceinline__ void load_f32(const void* p, size_t i, float* f) {
+  constexpr int M = N * elem_size(DT) > 16 ? 16 / elem_size(DT) : N;
+#pragma unroll
+  for (int j = 0; j < N; j += M) {
+    Pack<DT, M> q;
+    q.load(p, i + j);
+    q.unpack(f + j);
+  }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void store_f32(void* p, size_t i, const float* f) {
+  constexpr int M = N * elem_size(DT) > 16 ? 16 / elem_size(DT) : N;
+#pragma unroll
+  for (int j = 0; j < N; j += M) {
+    Pack<DT, M> q;
+    q.pack(f + j);
+    q.store(p, i + j);
+  }
+}
+
+// N elements of a state of dtype code sdt (0: zeros, BF16, FP32); the same branch in every lane
+template <int N>
+__device__ __forceinline__ void load_state(const void* p, int sdt, size_t i, float* f) {
+  if (sdt == FP32) load_f32<FP32, N>(p, i, f);
+  else if (sdt == BF16) load_f32<BF16, N>(p, i, f);
+  else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = 0.0f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_state(void* p, int sdt, size_t i, const float* f) {
+  if (sdt == FP32) store_f32<FP32, N>(p, i, f);
+  else if (sdt == BF16) store_f32<BF16, N>(p, i, f);
+}
+
+}  // namespace kda

@@ -71,6 +71,11 @@ struct FwdParams {
   ChunkMap map;
   uint8_t* rec;            // chunk records: [max_chunks][H][REC_BYTES]
   ChainSeg seg;
+  // token-recurrent kernel only: states in slots of a cache (state n in row in_slots[n] of
+  // init_state, left in row out_slots[n] of final_state); without them state n is row n
+  const int32_t* in_slots = nullptr;
+  const int32_t* out_slots = nullptr;
+  int32_t n_slots = 0;
 };
 
 hipError_t launch_sched(const int64_t* cu_seqlens, int32_t N, int32_t T, int32_t max_chunks,

@@ -82,6 +82,9 @@ __device__ __forceinline__ f32x4 unpack4_bf16(u32x2 w) {
   return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
 }
 
+// SLOTS: the states lie in slots of a cache; a slot number outside it reads zeros and is
+// not written.
+template <bool SLOTS>
 __global__ __launch_bounds__(256) void kda_recurrent_kernel(FwdParams p, const int64_t* cu) {
   __shared__ f32x4 su[4][2][4];   // [wave][half][i/4]: u of row 32w + 2i + half
   const int H = p.H;
@@ -103,12 +106,21 @@ __global__ __launch_bounds__(256) void kda_recurrent_kernel(FwdParams p, const i
 
   // S[i]: row 32w + 2i + half, channels 4pl..4pl+3
   f32x4 S[16];
-  const size_t st_off = ((size_t)(n * H + h) * VD + 32 * w + half) * KD + 4 * pl;   // + 2i rows
-  if (p.init_dtype == 2) {
+  const size_t lane_off = (size_t)(32 * w + half) * KD + 4 * pl;   // + 2i rows
+  int in_row = n, out_row = n, init_dtype = p.init_dtype, final_dtype = p.final_dtype;
+  if (SLOTS) {
+    in_row = p.in_slots[n];
+    out_row = p.out_slots[n];
+    if (in_row < 0 || in_row >= p.n_slots) init_dtype = 0;
+    if (out_row < 0 || out_row >= p.n_slots) final_dtype = 0;
+  }
+  // (without slots nseq * H is below 2^23; with them slots * H is not bounded by the grid)
+  const size_t st_off = ((size_t)in_row * H + h) * (VD * KD) + lane_off;
+  if (init_dtype == 2) {
     const float* src = static_cast<const float*>(p.init_state) + st_off;
 #pragma unroll
     for (int i = 0; i < 16; ++i) S[i] = *reinterpret_cast<const f32x4*>(src + (size_t)2 * i * KD);
-  } else if (p.init_dtype == 1) {
+  } else if (init_dtype == 1) {
     const uint16_t* src = static_cast<const uint16_t*>(p.init_state) + st_off;
 #pragma unroll
     for (int i = 0; i < 16; ++i) S[i] = unpack4_bf16(*reinterpret_cast<const u32x2*>(src + (size_t)2 * i * KD));
@@ -172,12 +184,13 @@ __global__ __launch_bounds__(256) void kda_recurrent_kernel(FwdParams p, const i
     for (int i = 0; i < 16; ++i) S[i] -= uu[i >> 2][i & 3] * kh;
   }
 
-  if (p.final_dtype == 2) {
-    float* dst = static_cast<float*>(p.final_state) + st_off;
+  const size_t fin_off = SLOTS ? ((size_t)out_row * H + h) * (VD * KD) + lane_off : st_off;
+  if (final_dtype == 2) {
+    float* dst = static_cast<float*>(p.final_state) + fin_off;
 #pragma unroll
     for (int i = 0; i < 16; ++i) *reinterpret_cast<f32x4*>(dst + (size_t)2 * i * KD) = S[i];
-  } else if (p.final_dtype == 1) {
-    uint16_t* dst = static_cast<uint16_t*>(p.final_state) + st_off;
+  } else if (final_dtype == 1) {
+    uint16_t* dst = static_cast<uint16_t*>(p.final_state) + fin_off;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       *reinterpret_cast<u32x2*>(dst + (size_t)2 * i * KD) = u32x2{pack_bf16x2(S[i].x, S[i].y), pack_bf16x2(S[i].z, S[i].w)};
@@ -189,7 +202,10 @@ __global__ __launch_bounds__(256) void kda_recurrent_kernel(FwdParams p, const i
 hipError_t launch_recurrent(const FwdParams& p, const int64_t* cu_seqlens, hipStream_t stream) {
   const int64_t blocks = (int64_t)p.map.nseq * p.H;
   if (blocks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(kda_recurrent_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p, cu_seqlens);
+  if (p.in_slots)
+    hipLaunchKernelGGL(kda_recurrent_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, p, cu_seqlens);
+  else
+    hipLaunchKernelGGL(kda_recurrent_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, p, cu_seqlens);
   return hipGetLastError();
 }
 

@@ -1,6 +1,8 @@
 /*
  * kda.h -- C ABI of the MI355X (gfx950) Kimi Delta Attention forward library
- * (libkda.so).
+ * (libkda.so), and of the operators beside it that a recurrent layer trains and
+ * serves with: the gated linear recurrence (kda_glr_*), layer norm
+ * (kda_layernorm_*), and caches of states in slots (kda_cache_*, kda_fwd_slots).
  *
  * The operation (per sequence n and head h, state S of V x K, K contiguous):
  *   q^, k^ = L2-normalised q, k over K (x / sqrt(sum x^2 + 1e-6))
@@ -53,14 +55,16 @@ enum kda_status {
     KDA_OK = 0,
     KDA_ERR_NULL = 1,      /* a required pointer is NULL                           */
     KDA_ERR_SHAPE = 2,     /* K != 128, V != 128, H < 1, T < 0, B < 1, B != 1 with
-                              cu_seqlens, N < 1 with cu_seqlens, size overflow      */
-    KDA_ERR_DTYPE = 3,     /* unknown state dtype code, or initial and final state
-                              given with different dtypes                           */
+                              cu_seqlens, N < 1 with cu_seqlens, D, S, L, M or n
+                              out of range, size overflow                           */
+    KDA_ERR_DTYPE = 3,     /* unknown dtype or state dtype code, or initial and final
+                              state given with different dtypes                     */
     KDA_ERR_VALUE = 4,     /* lower_bound outside [-5, 0] or not finite (safe gate),
-                              scale not finite, unknown flag bits, bad cu_seqlens
-                              contents (KDA_VALIDATE=1 only)                        */
+                              scale not finite, eps negative or not finite, unknown
+                              flag bits, bad cu_seqlens contents (KDA_VALIDATE=1)   */
     KDA_ERR_ALIGN = 5,     /* a pointer is not 16-byte aligned                      */
-    KDA_ERR_WORKSPACE = 6, /* workspace NULL or smaller than kda_fwd_workspace_min */
+    KDA_ERR_WORKSPACE = 6, /* workspace NULL or too small (kda_fwd_workspace_min, or the
+                              operator's own kda_*_workspace_size)                  */
     KDA_ERR_HIP = 7,       /* a HIP runtime call or kernel launch failed            */
     KDA_ERR_CAPACITY = 8   /* kda_fwd_noalloc: the call needs more workspace than
                               its fixed device array holds (KDA_NOALLOC_CAPACITY)   */
@@ -256,6 +260,165 @@ int kda_fwd_noalloc(const void *q, const void *k, const void *v, const void *g, 
                     int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, uint32_t flags,
                     void *stream);
 size_t kda_noalloc_capacity(void);
+
+/* ---- states in the slots of a cache ----------------------------------------
+ *
+ * A cache ("pool") holds the states of many sequences in S slots of equal size,
+ * for L layers: contiguous [L, S, slot]. The slots' contents are the states that
+ * kda_fwd, kda_fwd_recurrent and kda_glr_fwd take and return (for KDA a slot is
+ * [H, V, K], for the gated linear recurrence [D]); slot s of a sequence is the
+ * same in every layer. Slot numbers are int32 on the device; used[s] is nonzero
+ * where slot s is held. Everything runs on the device and in stream order, so
+ * the calls can be captured into a graph.
+ *
+ * Rules of every kda_cache_* call: S <= 2^24, L >= 1, slot_bytes >= 1; pool is
+ * aligned to 16 bytes, used, src, dst, slots, remap and table to 4; the arrays do
+ * not overlap each other. n may be 0 (nothing is done; the index arrays may then
+ * be NULL). A slot number outside [0, S) is never followed: what it means is
+ * said at each call.
+ *
+ * kda_cache_copy: in every layer, slot dst[i] becomes a copy of slot src[i],
+ *   0 <= i < n. Pairs with a number outside [0, S) or with src[i] == dst[i] do
+ *   nothing. No slot may be the target of two pairs, or the target of one and the
+ *   source of another: the slots concerned then hold unspecified bytes of the
+ *   slots involved (no other slot is touched).
+ *
+ * kda_cache_fork: a new slot for each of n requests. Request i is a used slot
+ *   src[i] in [0, S) to copy (several may name the same), or -1 for a slot of
+ *   zeros. The requests, in their order, take the free slots in ascending order:
+ *   dst[i] is the new slot, its contents are written in every layer and its used
+ *   flag becomes 1. dst[i] = -1, and nothing else, where src[i] is neither -1 nor
+ *   a slot that was used before the call, and where no free slot is left.
+ *
+ * kda_cache_free: used[slots[i]] = 0 for every slots[i] in [0, S); others are
+ *   passed over, and naming a slot twice is naming it once.
+ *
+ * kda_cache_compact: moves states to the front, so that the n_used used slots are
+ *   slots 0 .. n_used - 1. The free slots below n_used, in ascending order, take
+ *   the contents of the used slots from n_used on, in ascending order; all other
+ *   slots keep their place. remap[s] (int32 [S], OUTPUT) is the new number of
+ *   slot s, or -1 where it was free; used is rewritten (1 below n_used, 0 from
+ *   there on). table (int32 [n] or NULL) holds slot numbers that are replaced by
+ *   their new ones, -1 for free slots and numbers outside [0, S). workspace:
+ *   kda_cache_workspace_size(S) bytes, 256-byte aligned.
+ */
+size_t kda_cache_workspace_size(int64_t S);
+int kda_cache_copy(void *pool, int64_t L, int64_t S, size_t slot_bytes, const int32_t *src, const int32_t *dst,
+                   int64_t n, void *stream);
+int kda_cache_fork(void *pool, int64_t L, int64_t S, size_t slot_bytes, int32_t *used, const int32_t *src,
+                   int32_t *dst, int64_t n, void *stream);
+int kda_cache_free(int32_t *used, int64_t S, const int32_t *slots, int64_t n, void *stream);
+int kda_cache_compact(void *pool, int64_t L, int64_t S, size_t slot_bytes, int32_t *used, int32_t *remap,
+                      int32_t *table, int64_t n, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_fwd_slots -- kda_fwd_recurrent_ex with the states in the slots of a cache's
+ * layer: state is [S, H, V, K] (one layer of a pool), sequence n starts from slot
+ * in_slots[n] (a number outside [0, S): from zeros) and leaves its state in slot
+ * out_slots[n] (outside [0, S): not written), for empty sequences too. in_slots
+ * and out_slots are int32 of the number of sequences (N, or B without
+ * cu_seqlens) and may be the same array. Several sequences may start from one
+ * slot; no slot may be left a state by two sequences, or by one sequence while
+ * another starts from it. state_dtype is KDA_STATE_BF16 or KDA_STATE_FP32,
+ * 1 <= S <= 2^24. Every other argument and rule is kda_fwd_recurrent_ex's.
+ */
+int kda_fwd_slots(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                  float scale, void *out, const float *A_log, const float *dt_bias, float lower_bound,
+                  void *state, int state_dtype, int64_t S, const int32_t *in_slots, const int32_t *out_slots,
+                  const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t H, int64_t K,
+                  int64_t V, uint32_t flags, void *stream);
+
+/* Element types of the operators below (the state codes' values, and fp16). */
+enum kda_dtype {
+    KDA_BF16 = 1,
+    KDA_FP32 = 2,
+    KDA_FP16 = 3
+};
+
+/* ---- gated linear recurrence -----------------------------------------------
+ *
+ * Per sequence and channel, from the state h of before its first token:
+ *     h_t = exp(g_t) h_{t-1} + x_t,      y_t = h_t
+ * g is the log-decay, as kda_fwd takes it with KDA_FUSE_GATE clear (not clamped
+ * here): g <= 0 forgets, -inf starts over from x_t. The backward pass, with dy_t
+ * and the final state's gradient d_final added at the last token:
+ *     G_t = dy_t + exp(g_{t+1}) G_{t+1}
+ *     dx_t = G_t,   dg_t = G_t exp(g_t) h_{t-1},   d_initial = exp(g_first) G_first
+ * States and sums are fp32 throughout; every output is rounded once.
+ *
+ *   x, g, y, dy, dx, dg   [B, T, D] in `dtype` (KDA_BF16, KDA_FP32 or KDA_FP16).
+ *                         T may be 0 (they hold no element and may be NULL).
+ *   D                     channels, 1 <= D <= 2^24, any number (whole multiples
+ *                         of 16 bytes are fastest)
+ *   initial_state, final_state, their dtypes, cu_seqlens, N, B, T
+ *                         as for kda_fwd, with states [B|N, D]. Tokens of a packed
+ *                         batch that no sequence covers are neither read nor written.
+ *   carry                 fp32 [kda_glr_carry_rows(B, T), D]: the state that enters
+ *                         every 128th of the B * T packed tokens. kda_glr_fwd writes
+ *                         it where it is not NULL; kda_glr_bwd needs the one of the
+ *                         same x, g, initial_state and boundaries. Its contents
+ *                         where a sequence begins are unspecified.
+ *   d_final, d_final_dtype, d_initial, d_initial_dtype
+ *                         gradient of final_state (NULL/KDA_STATE_NONE: zero) and
+ *                         of initial_state (NULL/KDA_STATE_NONE: not written),
+ *                         [B|N, D] bf16/fp32 each. An empty sequence's d_initial is
+ *                         its d_final. May not alias each other.
+ *   workspace             caller-owned, kda_glr_workspace_size(B, T, D, N) bytes
+ *                         (N = 0 without cu_seqlens) for either direction, 256-byte
+ *                         aligned; contents need no initialisation and are clobbered
+ * Outputs do not overlap inputs, except that final_state may be initial_state.
+ * Results do not depend on timing: the same call gives the same bits. cu_seqlens'
+ * contents are the caller's precondition, as for kda_fwd (KDA_VALIDATE=1 checks).
+ */
+int64_t kda_glr_carry_rows(int64_t B, int64_t T);
+size_t kda_glr_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N);
+int kda_glr_fwd(const void *x, const void *g, void *y, int dtype, const void *initial_state, int initial_dtype,
+                void *final_state, int final_dtype, float *carry, const int64_t *cu_seqlens, int64_t N, int64_t B,
+                int64_t T, int64_t D, void *workspace, size_t workspace_bytes, void *stream);
+int kda_glr_bwd(const void *x, const void *g, const void *dy, int dtype, const float *carry,
+                const void *initial_state, int initial_dtype, const void *d_final, int d_final_dtype, void *dx,
+                void *dg, void *d_initial, int d_initial_dtype, const int64_t *cu_seqlens, int64_t N, int64_t B,
+                int64_t T, int64_t D, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_glr_step -- one token for each of N sequences, the states in the slots of a
+ * cache's layer [S, D] (bf16/fp32): y[n] = exp(g[n]) state[in_slots[n]] + x[n], left
+ * in slot out_slots[n]. x, g, y are [N, D] in `dtype`; the rules for slots are
+ * kda_fwd_slots'. N >= 0.
+ */
+int kda_glr_step(const void *x, const void *g, void *y, int dtype, void *state, int state_dtype, int64_t S,
+                 const int32_t *in_slots, const int32_t *out_slots, int64_t N, int64_t D, void *stream);
+
+/* ---- layer norm --------------------------------------------------------------
+ *
+ * Per row of D elements, with the row's mean m and r = 1 / sqrt(variance + eps)
+ * (variance over D, not D - 1):
+ *     y = (x - m) r weight + bias
+ *     a = dy weight,  c1 = mean(a),  c2 = mean(a (x - m) r)
+ *     dx = r (a - c1 - (x - m) r c2)
+ *     d_weight = sum over rows of dy (x - m) r,   d_bias = sum over rows of dy
+ * Statistics and sums are fp32; every output is rounded once.
+ *
+ *   x, y, dy, dx      [M, D] in `dtype` (KDA_BF16, KDA_FP32 or KDA_FP16), M >= 0,
+ *                     1 <= D <= 2^24. A row per token (D the model's width), or per
+ *                     token and head (D = 128 and M = B * T * H on kda_fwd's out).
+ *   weight, bias      fp32 [D], or NULL (ones, zeros)
+ *   eps               finite, >= 0
+ *   mean, rstd        fp32 [M]: written by kda_layernorm_fwd where not NULL, read
+ *                     by kda_layernorm_bwd (needed there where M > 0)
+ *   d_weight, d_bias  fp32 [D] or NULL, overwritten (zeros where M = 0). Their sums
+ *                     have an order of their own that no timing changes.
+ *   dx                may be NULL (only the weight's and bias's gradients are wanted)
+ *   workspace         caller-owned, kda_layernorm_workspace_size(M, D) bytes,
+ *                     256-byte aligned, needed where d_weight or d_bias is given
+ * y may be x, and dx may be dy or x; other outputs do not overlap inputs.
+ */
+size_t kda_layernorm_workspace_size(int64_t M, int64_t D);
+int kda_layernorm_fwd(const void *x, const float *weight, const float *bias, float eps, void *y, int dtype,
+                      float *mean, float *rstd, int64_t M, int64_t D, void *stream);
+int kda_layernorm_bwd(const void *dy, const void *x, const float *weight, const float *mean, const float *rstd,
+                      void *dx, int dtype, float *d_weight, float *d_bias, int64_t M, int64_t D, void *workspace,
+                      size_t workspace_bytes, void *stream);
 
 /* kda_status_string -- static description of a status code (never NULL). */
 const char *kda_status_string(int status);
