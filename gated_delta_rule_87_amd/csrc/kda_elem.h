@@ -91,6 +91,22 @@ struct Pack {
   }
 };
 
+// elements c .. c + M - 1 of a pack: one 32-bit word of it, or its only element
+template <int DT, int N, int M>
+__device__ __forceinline__ void unpack_word(const Pack<DT, N>& q, int c, float* f) {
+  Pack<DT, M> one;
+  if constexpr (N == M) one.r = q.r;
+  else one.r = q.r[c / M];
+  one.unpack(f);
+}
+template <int DT, int N, int M>
+__device__ __forceinline__ void pack_word(Pack<DT, N>& q, int c, const float* f) {
+  Pack<DT, M> one;
+  one.pack(f);
+  if constexpr (N == M) q.r = one.r;
+  else q.r[c / M] = one.r;
+}
+
 template <int DT, int N>
 __device__ __forceinline__ void load_f32(const void* p, size_t i, float* f) {
   constexpr int M = N * elem_size(DT) > 16 ? 16 / elem_size(DT) : N;

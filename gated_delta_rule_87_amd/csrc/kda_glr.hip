@@ -1,4 +1,30 @@
-// kda_glr.hip -- gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per channel (gfx950).
+// kda_glr.hip -- gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per channel, forward
+// and backward (gfx950).
+//
+// The B * T packed tokens are cut into tiles of GLR_TILE tokens by 256 bytes of channels (64
+// elements where D is no whole number of 16-byte vectors), one workgroup each. A tile acts on
+// the state that enters it as an affine map h -> A h + L, with A = prod exp(g): the workgroup
+// loads its tile once into registers, reduces it to (A, L) per channel, publishes that,
+// obtains the state that enters it from the tiles before, and runs through its registers a
+// second time for the outputs. So every element is read once and written once, also for few
+// channels on long sequences, where one lane per channel would leave most of the GPU idle.
+//
+// Inside a tile, 256 / LR groups of lanes hold R consecutive tokens each; their maps are
+// composed through shared memory. A sequence's first token sets the state instead of
+// continuing it: A = RESET (-1; an exp is never negative) marks a map that does not depend on
+// the state before, which is then not multiplied by zero but left out (it may be NaN).
+//
+// Between tiles: per tile and channel a word for (A, L) and one for the state that leaves the
+// tile, both EMPTY (all ones) until published; a value that is NaN is stored as one NaN whose
+// bits are not EMPTY. A tile waits until one of the WINDOW tiles before it has published its
+// state and all between that one and itself their maps, and applies those in the tokens'
+// order. Every published state is (A, L) applied to the state before, whoever computes it, so
+// the bits do not depend on how far a tile looked back. Words are single relaxed atomics of
+// device scope: no fences, no flags beside the data.
+//
+// Every wait ends: a workgroup takes its tile's number from a counter of its channels when it
+// starts, so all tiles that it waits for belong to workgroups that have started before it and
+// which themselves wait only for earlier ones; the first waits for none.
 #include <type_traits>
 
 #include "kda_elem.h"
@@ -7,95 +33,602 @@
 namespace kda {
 namespace {
 
-struct Span { int64_t b, e; };
+constexpr float RESET = -1.0f;
+constexpr uint32_t EMPTY = 0xffffffffu;
+constexpr int WINDOW = 8;
+constexpr int TICK_STRIDE = 16;   // a counter per 64 bytes
 
-// tokens of sequence n among the packed ones, kept inside [0, tokens]
-__device__ __forceinline__ Span glr_span(const GlrParams& p, int n) {
-  if (!p.cu) return {(int64_t)n * p.T, (int64_t)(n + 1) * p.T};
-  int64_t a = p.cu[n], b = p.cu[n + 1];
-  a = a < 0 ? 0 : (a > p.T ? p.T : a);
-  b = b < a ? a : (b > p.T ? p.T : b);
-  return {a, b};
+template <int DT, int VEC>
+struct Geom {
+  static constexpr int LR = VEC > 1 ? 16 : 64;    // lanes across a row
+  static constexpr int CH = LR * VEC;             // channels of a tile
+  static constexpr int GRP = 256 / LR;            // groups of lanes along the tokens
+  static constexpr int R = GLR_TILE / GRP;        // tokens of a lane
+};
+
+__device__ __forceinline__ float decay(float g) { return fast_exp2(g * LOG2E); }
+// the map (A, L) on a state
+__device__ __forceinline__ float apply(float A, float L, float h) { return A < 0.0f ? L : fmaf(A, h, L); }
+// (A, L) followed by (a, l)
+__device__ __forceinline__ void compose(float& A, float& L, float a, float l) {
+  L = apply(a, l, L);
+  A = a < 0.0f || A < 0.0f ? RESET : A * a;
 }
 
-// One lane per channel, token by token.
-template <int DT>
-__global__ __launch_bounds__(64) void kda_glr_fwd_kernel(GlrParams p) {
-  const int n = blockIdx.y, d = blockIdx.x * 64 + threadIdx.x;
-  if (d >= p.D) return;
-  const Span s = glr_span(p, n);
+__device__ __forceinline__ uint32_t word_of(float f) { return f != f ? 0x7fc00000u : __float_as_uint(f); }
+template <typename T>
+__device__ __forceinline__ void publish(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T observe(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+struct TileWs {
+  uint64_t* maps;     // [tiles][D] (L, A) of each tile, by the order of processing
+  uint32_t* states;   // [tiles][D] state leaving each tile
+  uint32_t* ticks;    // [channel tiles * TICK_STRIDE]
+  float* stage;       // [nseq][D] initial states, where final_state overwrites them
+  int32_t tiles, cols;
+};
+
+// Publishes the tile's map, waits for the state that enters it and publishes the one that
+// leaves it; k: the tile's place in the order of processing.
+__device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, size_t d, float A, float L) {
+  uint64_t* maps = w.maps + d;
+  uint32_t* states = w.states + d;
+  const bool more = k + 1 < w.tiles;
+  if (more) publish(maps + (size_t)k * D, ((uint64_t)word_of(L) << 32) | __float_as_uint(A));
+  if (more && (A < 0.0f || k == 0)) publish(states + (size_t)k * D, word_of(apply(A, L, 0.0f)));
   float h = 0.0f;
-  const int64_t in_row = p.in_slots ? p.in_slots[n] : n;
-  if (!p.in_slots || (in_row >= 0 && in_row < p.n_slots)) load_state<1>(p.init, p.init_dtype, (size_t)in_row * p.D + d, &h);
-  for (int64_t t = s.b; t < s.e; ++t) {
-    float g, x;
-    load_f32<DT, 1>(p.g, (size_t)t * p.D + d, &g);
-    load_f32<DT, 1>(p.x, (size_t)t * p.D + d, &x);
-    if (p.carry && t % GLR_TILE == 0) p.carry[(size_t)(t / GLR_TILE) * p.D + d] = h;
-    h = fmaf(expf(g), h, x);
-    store_f32<DT, 1>(p.y, (size_t)t * p.D + d, &h);
+  for (bool found = k == 0; !found;) {
+    // state of the tile i places before (the one before the first tile: zero)
+    const uint32_t s1 = observe(states + (size_t)(k - 1) * D);
+    if (s1 != EMPTY) {
+      h = __uint_as_float(s1);
+      break;
+    }
+    uint32_t s[WINDOW];
+    uint64_t m[WINDOW];
+#pragma unroll
+    for (int i = 1; i < WINDOW; ++i) {
+      m[i] = k - i >= 0 ? observe(maps + (size_t)(k - i) * D) : ~0ull;
+      s[i] = k - i - 1 >= 0 ? observe(states + (size_t)(k - i - 1) * D) : k - i - 1 == -1 ? 0u : EMPTY;
+    }
+    int at = 0;   // the nearest published state with all maps after it: i = at
+    bool whole = true;
+#pragma unroll
+    for (int i = 1; i < WINDOW; ++i) {
+      whole = whole && m[i] != ~0ull;
+      if (whole && at == 0 && s[i] != EMPTY) at = i;
+    }
+    if (at > 0) {
+#pragma unroll
+      for (int i = WINDOW - 1; i >= 1; --i) {
+        if (i == at) h = __uint_as_float(s[i]);
+        if (i <= at) h = apply(__uint_as_float((uint32_t)m[i]), __uint_as_float((uint32_t)(m[i] >> 32)), h);
+      }
+      found = true;
+    } else {
+      __builtin_amdgcn_s_sleep(2);
+    }
   }
-  const int64_t out_row = p.out_slots ? p.out_slots[n] : n;
-  if (!p.out_slots || (out_row >= 0 && out_row < p.n_slots)) store_state<1>(p.fin, p.fin_dtype, (size_t)out_row * p.D + d, &h);
+  if (more && !(A < 0.0f) && k != 0) publish(states + (size_t)k * D, word_of(apply(A, L, h)));
+  return h;
 }
 
-// One lane per channel: per tile of GLR_TILE tokens the states before each token are
-// computed again from the saved one into shared memory, then the tokens are taken backwards.
-template <int DT>
-__global__ __launch_bounds__(64) void kda_glr_bwd_kernel(GlrParams p) {
-  __shared__ float hs[GLR_TILE][64];
-  const int n = blockIdx.y, lane = threadIdx.x, d = blockIdx.x * 64 + lane;
+// ---- which sequence a token belongs to -------------------------------------------
+
+struct Place {
+  int n;              // sequence, -1: none
+  bool first, last;   // token of it
+};
+
+__device__ __forceinline__ int64_t bound_of(const int64_t* cu, int i, int T) {
+  const int64_t v = cu[i];
+  return v < 0 ? 0 : v > T ? T : v;
+}
+
+// largest n in [lo, hi] with cu[n] <= t, or lo
+__device__ __forceinline__ int find_seq(const int64_t* cu, int lo, int hi, int t) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ Place place_of(const GlrParams& p, const int64_t* cu, int lo, int hi, int t) {
+  if (t >= p.tokens) return {-1, false, false};
+  if (!cu) {
+    const int n = (int)((uint32_t)t / (uint32_t)p.T), r = t - n * p.T;
+    return {n, r == 0, r == p.T - 1};
+  }
+  const int n = find_seq(cu, lo, hi, t);
+  const int64_t b = bound_of(cu, n, p.T), e = bound_of(cu, n + 1, p.T);
+  if (t < b || t >= e) return {-1, false, false};
+  return {n, t == b, t == e - 1};
+}
+
+// The sequences that a tile's tokens belong to, in shared memory: masks of tokens in a
+// sequence, first of one and last of one; numbers of the sequences of all tokens.
+struct TilePlaces {
+  uint64_t in[GLR_TILE / 64], first[GLR_TILE / 64], last[GLR_TILE / 64];
+  int n[GLR_TILE];
+};
+
+__device__ __forceinline__ void find_places(const GlrParams& p, const int64_t* cu, int t_base, TilePlaces& s) {
+  const int tid = threadIdx.x;
+  int lo = 0, hi = 0;
+  if (cu) {   // the same search in every lane
+    lo = find_seq(cu, 0, p.nseq - 1, t_base);
+    hi = find_seq(cu, lo, p.nseq - 1, t_base + GLR_TILE - 1);
+  }
+  if (tid < GLR_TILE) {
+    const Place q = place_of(p, cu, lo, hi, t_base + tid);
+    s.n[tid] = q.n;
+    const uint64_t in = __ballot(q.n >= 0), first = __ballot(q.first), last = __ballot(q.last);
+    if ((tid & 63) == 0) {
+      s.in[tid >> 6] = in;
+      s.first[tid >> 6] = first;
+      s.last[tid >> 6] = last;
+    }
+  }
+}
+
+// ---- before the tiles: the words EMPTY, the counters zero; states of empty sequences ----
+
+__global__ __launch_bounds__(256) void kda_glr_prep_kernel(GlrParams p, TileWs w, const void* from, int from_dtype) {
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  const int64_t words = (int64_t)w.tiles * p.D;   // maps and states lie one after the other
+  const u32x4 ones = {EMPTY, EMPTY, EMPTY, EMPTY};
+  for (int64_t i = i0; i < (3 * words + 3) / 4; i += step) reinterpret_cast<u32x4*>(w.maps)[i] = ones;
+  for (int64_t i = i0; i < (int64_t)w.cols * TICK_STRIDE; i += step) w.ticks[i] = 0;
+  if (!w.stage && !p.cu && p.T > 0) return;
+  for (int64_t i = i0; i < (int64_t)p.nseq * p.D; i += step) {
+    const int n = (int)(i / p.D);
+    float h;
+    load_state<1>(from, from_dtype, i, &h);
+    if (w.stage) w.stage[i] = h;
+    if (p.cu ? bound_of(p.cu, n, p.T) >= bound_of(p.cu, n + 1, p.T) : p.T == 0) store_state<1>(p.fin, p.fin_dtype, i, &h);
+  }
+}
+
+// ---- forward -----------------------------------------------------------------------
+
+template <int DT, int VEC>
+__global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, const int64_t* __restrict__ cu, TileWs w) {
+  using G = Geom<DT, VEC>;
+  constexpr int R = G::R;
+  __shared__ float sA[G::GRP][G::CH], sL[G::GRP][G::CH];
+  __shared__ TilePlaces places;
+  __shared__ int s_tile;
+  const int tid = threadIdx.x, lr = tid % G::LR, grp = tid / G::LR;
+  const int col = blockIdx.x % w.cols;
+  if (tid == 0)
+    s_tile = (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const int tile = __builtin_amdgcn_readfirstlane(s_tile);
+  const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
+  const int d = col * G::CH + lr * VEC;
+  const bool d_ok = d < p.D;   // (a vector lies inside or outside: VEC divides D)
+
+  Pack<DT, VEC> g[R], x[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    g[r].clear();
+    x[r].clear();
+    if (d_ok && t0 + r < p.tokens) {
+      const size_t i = (size_t)(t0 + r) * p.D + d;
+      g[r].load(p.g, i);
+      x[r].load(p.x, i);
+    }
+  }
+  find_places(p, cu, t_base, places);
+  __syncthreads();
+  const int word = grp * R / 64, bit = grp * R % 64;
+  const uint32_t all = (uint32_t)((1ull << R) - 1);
+  const uint32_t in = (uint32_t)(places.in[word] >> bit) & all, first = (uint32_t)(places.first[word] >> bit) & all,
+                 last = (uint32_t)(places.last[word] >> bit) & all;
+  const bool plain = in == all && first == 0;
+
+  auto reduce = [&](auto plain_c, float* A, float* L) {
+    constexpr bool PLAIN = decltype(plain_c)::value;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, L[v] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!PLAIN && !(in >> r & 1)) continue;
+      float gf[VEC], xf[VEC];
+      g[r].unpack(gf);
+      x[r].unpack(xf);
+      if (!PLAIN && (first >> r & 1)) {
+        float h0[VEC] = {};
+        if (d_ok) load_state<VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, h0);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          L[v] = fmaf(decay(gf[v]), h0[v], xf[v]);
+          A[v] = RESET;
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const float a = decay(gf[v]);
+          L[v] = fmaf(a, L[v], xf[v]);
+          A[v] = PLAIN ? A[v] * a : (A[v] < 0.0f ? RESET : A[v] * a);
+        }
+      }
+    }
+  };
+  {
+    float A[VEC], L[VEC];
+    if (__all(plain)) reduce(std::true_type{}, A, L);
+    else reduce(std::false_type{}, A, L);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      sA[grp][lr * VEC + v] = A[v];
+      sL[grp][lr * VEC + v] = L[v];
+    }
+  }
+  __syncthreads();
+  if (tid < G::CH && col * G::CH + tid < p.D) {   // a lane per channel
+    const size_t dc = (size_t)col * G::CH + tid;
+    float A[G::GRP], L[G::GRP], TA = 1.0f, TL = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G::GRP; ++i) {
+      A[i] = sA[i][tid];
+      L[i] = sL[i][tid];
+      compose(TA, TL, A[i], L[i]);
+    }
+    float h = pass_state(w, tile, p.D, dc, TA, TL);
+    if (p.carry) p.carry[(size_t)tile * p.D + dc] = h;
+#pragma unroll
+    for (int i = 0; i < G::GRP; ++i) {   // the state that enters each group
+      sL[i][tid] = h;
+      h = apply(A[i], L[i], h);
+    }
+  }
+  __syncthreads();
+  if (!d_ok) return;
+  float h[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) h[v] = sL[grp][lr * VEC + v];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (!(in >> r & 1)) continue;
+    float gf[VEC], xf[VEC];
+    g[r].unpack(gf);
+    x[r].unpack(xf);
+    if (first >> r & 1) load_state<VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, h);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
+    Pack<DT, VEC> y;
+    y.pack(h);
+    y.store(p.y, (size_t)(t0 + r) * p.D + d);
+    if (last >> r & 1) store_state<VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, h);
+  }
+}
+
+// ---- backward ------------------------------------------------------------------------
+//
+// E is the gradient that reaches the state behind a token from the tokens after it:
+// G_t = dy_t + E, dx_t = G_t, then E = exp(g_t) G_t is passed to the token before, and
+// dg_t = E h_{t-1}. E runs through the tiles from the last to the first as h does from the
+// first to the last, with maps of the same A; the state that enters a tile was saved by the
+// forward pass, so only E is passed between tiles here. Words of two channels (one in fp32)
+// are worked on one after the other, their dx and dg written over x and g in the registers:
+// of the states before each token only R times two are held at once (all channels' would take
+// 64 more registers and a third of the waves).
+template <int DT, int VEC>
+__global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, const int64_t* __restrict__ cu, TileWs w) {
+  using G = Geom<DT, VEC>;
+  constexpr int R = G::R;
+  constexpr int NV = VEC > 1 && DT != FP32 ? 2 : 1;   // channels of a word
+  __shared__ float sA[G::GRP][G::CH], sL[G::GRP][G::CH], sB[G::GRP][G::CH], sM[G::GRP][G::CH];
+  __shared__ TilePlaces places;
+  __shared__ int s_tile;
+  const int tid = threadIdx.x, lr = tid % G::LR, grp = tid / G::LR;
+  const int col = blockIdx.x % w.cols;
+  if (tid == 0)
+    s_tile = (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const int k = __builtin_amdgcn_readfirstlane(s_tile), tile = w.tiles - 1 - k;
+  const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
+  const int d = col * G::CH + lr * VEC;
+  const bool d_ok = d < p.D;
+
+  Pack<DT, VEC> g[R], x[R], dy[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    g[r].clear();
+    x[r].clear();
+    dy[r].clear();
+    if (d_ok && t0 + r < p.tokens) {
+      const size_t i = (size_t)(t0 + r) * p.D + d;
+      g[r].load(p.g, i);
+      x[r].load(p.x, i);
+      dy[r].load(p.dy, i);
+    }
+  }
+  find_places(p, cu, t_base, places);
+  __syncthreads();
+  const int word = grp * R / 64, bit = grp * R % 64;
+  const uint32_t all = (uint32_t)((1ull << R) - 1);
+  const uint32_t in = (uint32_t)(places.in[word] >> bit) & all, first = (uint32_t)(places.first[word] >> bit) & all,
+                 last = (uint32_t)(places.last[word] >> bit) & all;
+  const bool plain = in == all && first == 0 && last == 0;
+  auto row = [&](int r) { return (size_t)places.n[grp * R + r] * p.D + d; };
+
+  auto reduce = [&](auto plain_c) {
+    constexpr bool PLAIN = decltype(plain_c)::value;
+#pragma unroll
+    for (int c = 0; c < VEC; c += NV) {
+      float a[R][NV], A[NV], L[NV], B[NV], M[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) A[v] = B[v] = 1.0f, L[v] = M[v] = 0.0f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float xf[NV];
+        unpack_word<DT, VEC, NV>(g[r], c, a[r]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) a[r][v] = decay(a[r][v]);
+        if (!PLAIN && !(in >> r & 1)) continue;
+        unpack_word<DT, VEC, NV>(x[r], c, xf);
+        if (!PLAIN && (first >> r & 1)) {
+          if (d_ok) load_state<NV>(p.init, p.init_dtype, row(r) + c, L);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) A[v] = RESET;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          L[v] = fmaf(a[r][v], L[v], xf[v]);
+          A[v] = PLAIN ? A[v] * a[r][v] : (A[v] < 0.0f ? RESET : A[v] * a[r][v]);
+        }
+      }
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) {
+        if (!PLAIN && !(in >> r & 1)) continue;
+        float df[NV];
+        unpack_word<DT, VEC, NV>(dy[r], c, df);
+        if (!PLAIN && (last >> r & 1)) {
+          if (d_ok) load_state<NV>(p.dfin, p.dfin_dtype, row(r) + c, M);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) B[v] = RESET;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          M[v] = a[r][v] * (df[v] + M[v]);
+          B[v] = PLAIN ? B[v] * a[r][v] : (B[v] < 0.0f ? RESET : B[v] * a[r][v]);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int ch = lr * VEC + c + v;
+        sA[grp][ch] = A[v];
+        sL[grp][ch] = L[v];
+        sB[grp][ch] = B[v];
+        sM[grp][ch] = M[v];
+      }
+    }
+  };
+  if (__all(plain)) reduce(std::true_type{});
+  else reduce(std::false_type{});
+  __syncthreads();
+  if (tid < G::CH && col * G::CH + tid < p.D) {
+    const size_t dc = (size_t)col * G::CH + tid;
+    float TB = 1.0f, TM = 0.0f;
+#pragma unroll
+    for (int i = G::GRP - 1; i >= 0; --i) compose(TB, TM, sB[i][tid], sM[i][tid]);
+    float h = p.carry[(size_t)tile * p.D + dc];
+    float E = pass_state(w, k, p.D, dc, TB, TM);
+#pragma unroll
+    for (int i = 0; i < G::GRP; ++i) {
+      const float A = sA[i][tid], L = sL[i][tid];
+      sL[i][tid] = h;
+      h = apply(A, L, h);
+    }
+#pragma unroll
+    for (int i = G::GRP - 1; i >= 0; --i) {
+      const float B = sB[i][tid], M = sM[i][tid];
+      sM[i][tid] = E;
+      E = apply(B, M, E);
+    }
+  }
+  __syncthreads();
+  if (!d_ok) return;
+
+  auto outputs = [&](auto plain_c) {
+    constexpr bool PLAIN = decltype(plain_c)::value;
+#pragma unroll
+    for (int c = 0; c < VEC; c += NV) {
+      float a[R][NV], before[R][NV], h[NV], E[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        h[v] = sL[grp][lr * VEC + c + v];
+        E[v] = sM[grp][lr * VEC + c + v];
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float xf[NV];
+        unpack_word<DT, VEC, NV>(g[r], c, a[r]);
+        unpack_word<DT, VEC, NV>(x[r], c, xf);
+        if (!PLAIN && (first >> r & 1)) load_state<NV>(p.init, p.init_dtype, row(r) + c, h);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          a[r][v] = decay(a[r][v]);
+          before[r][v] = h[v];
+          if (PLAIN || (in >> r & 1)) h[v] = fmaf(a[r][v], h[v], xf[v]);
+        }
+      }
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) {
+        if (!PLAIN && !(in >> r & 1)) continue;
+        float df[NV], dg[NV];
+        unpack_word<DT, VEC, NV>(dy[r], c, df);
+        if (!PLAIN && (last >> r & 1)) load_state<NV>(p.dfin, p.dfin_dtype, row(r) + c, E);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          df[v] += E[v];
+          E[v] = a[r][v] * df[v];
+          dg[v] = E[v] * before[r][v];
+        }
+        pack_word<DT, VEC, NV>(x[r], c, df);
+        pack_word<DT, VEC, NV>(g[r], c, dg);
+        if (!PLAIN && (first >> r & 1)) store_state<NV>(p.fin, p.fin_dtype, row(r) + c, E);
+      }
+    }
+  };
+  if (__all(plain)) outputs(std::true_type{});
+  else outputs(std::false_type{});
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (!(in >> r & 1)) continue;
+    const size_t i = (size_t)(t0 + r) * p.D + d;
+    x[r].store(p.dx, i);
+    g[r].store(p.dg, i);
+  }
+}
+
+// ---- few tokens per sequence -----------------------------------------------------------
+
+// One lane per VEC channels of a sequence, token by token, from and to rows of the states or
+// slots of a cache.
+template <int DT, int VEC, bool SLOTS>
+__global__ __launch_bounds__(64) void kda_glr_tokens_kernel(GlrParams p, int cols) {
+  const int n = blockIdx.x / cols, d = ((blockIdx.x - n * cols) * 64 + threadIdx.x) * VEC;
   if (d >= p.D) return;
-  const Span s = glr_span(p, n);
-  float e = 0.0f, h0 = 0.0f;
-  load_state<1>(p.dfin, p.dfin_dtype, (size_t)n * p.D + d, &e);
-  load_state<1>(p.init, p.init_dtype, (size_t)n * p.D + d, &h0);
-  for (int64_t hi = s.e; hi > s.b;) {
-    const int64_t c = (hi - 1) / GLR_TILE, lo = c * GLR_TILE > s.b ? c * GLR_TILE : s.b;
-    float h = lo == s.b ? h0 : p.carry[(size_t)c * p.D + d];
-    for (int64_t t = lo; t < hi; ++t) {
-      float g, x;
-      load_f32<DT, 1>(p.g, (size_t)t * p.D + d, &g);
-      load_f32<DT, 1>(p.x, (size_t)t * p.D + d, &x);
-      hs[t - lo][lane] = h;
-      h = fmaf(expf(g), h, x);
-    }
-    for (int64_t t = hi - 1; t >= lo; --t) {
-      float g, dy;
-      load_f32<DT, 1>(p.g, (size_t)t * p.D + d, &g);
-      load_f32<DT, 1>(p.dy, (size_t)t * p.D + d, &dy);
-      const float G = dy + e;
-      e = expf(g) * G;
-      const float dg = e * hs[t - lo][lane];
-      store_f32<DT, 1>(p.dx, (size_t)t * p.D + d, &G);
-      store_f32<DT, 1>(p.dg, (size_t)t * p.D + d, &dg);
-    }
-    hi = lo;
+  int64_t b = (int64_t)n * p.T, e = b + p.T;
+  if (p.cu) {
+    b = bound_of(p.cu, n, p.T);
+    e = bound_of(p.cu, n + 1, p.T);
   }
-  store_state<1>(p.fin, p.fin_dtype, (size_t)n * p.D + d, &e);
+  int in_row = n, out_row = n, in_dtype = p.init_dtype, out_dtype = p.fin_dtype;
+  if (SLOTS) {
+    in_row = p.in_slots[n];
+    out_row = p.out_slots[n];
+    if (in_row < 0 || in_row >= p.n_slots) in_dtype = 0;
+    if (out_row < 0 || out_row >= p.n_slots) out_dtype = 0;
+  }
+  float h[VEC];
+  load_state<VEC>(p.init, in_dtype, (size_t)in_row * p.D + d, h);
+  for (int64_t t = b; t < e; ++t) {
+    const size_t i = (size_t)t * p.D + d;
+    Pack<DT, VEC> g, x, y;
+    g.load(p.g, i);
+    x.load(p.x, i);
+    float gf[VEC], xf[VEC];
+    g.unpack(gf);
+    x.unpack(xf);
+    if (p.carry && t % GLR_TILE == 0) store_f32<FP32, VEC>(p.carry, (size_t)(t / GLR_TILE) * p.D + d, h);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
+    y.pack(h);
+    y.store(p.y, i);
+  }
+  store_state<VEC>(p.fin, out_dtype, (size_t)out_row * p.D + d, h);
 }
 
+// f(element type, vector length) for the widest vectors that rows of D elements allow
 template <typename F>
-hipError_t by_dtype(int dt, F f) {
-  if (dt == BF16) f(std::integral_constant<int, BF16>{});
-  else if (dt == FP32) f(std::integral_constant<int, FP32>{});
-  else f(std::integral_constant<int, FP16>{});
+hipError_t by_type(int dt, int32_t D, F f) {
+  const bool wide = D % (16 / elem_size(dt)) == 0;
+  using std::integral_constant;
+  if (dt == BF16) {
+    if (wide) f(integral_constant<int, BF16>{}, integral_constant<int, 8>{});
+    else f(integral_constant<int, BF16>{}, integral_constant<int, 1>{});
+  } else if (dt == FP16) {
+    if (wide) f(integral_constant<int, FP16>{}, integral_constant<int, 8>{});
+    else f(integral_constant<int, FP16>{}, integral_constant<int, 1>{});
+  } else {
+    if (wide) f(integral_constant<int, FP32>{}, integral_constant<int, 4>{});
+    else f(integral_constant<int, FP32>{}, integral_constant<int, 1>{});
+  }
   return hipGetLastError();
 }
 
+int32_t tile_count(int64_t tokens) { return (int32_t)((tokens + GLR_TILE - 1) / GLR_TILE); }
+int32_t tile_cols(int dt, int32_t D) {
+  const int v = 16 / elem_size(dt);
+  const int ch = D % v == 0 ? 16 * v : 64;
+  return (D + ch - 1) / ch;
+}
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+TileWs tile_ws(const GlrParams& p, void* workspace, bool stage) {
+  TileWs w{};
+  uint8_t* b = static_cast<uint8_t*>(workspace);
+  w.tiles = tile_count(p.tokens);
+  w.cols = tile_cols(p.dtype, p.D);
+  const size_t words = (size_t)w.tiles * p.D;
+  w.maps = reinterpret_cast<uint64_t*>(b);
+  w.states = reinterpret_cast<uint32_t*>(b + words * 8);
+  w.ticks = reinterpret_cast<uint32_t*>(b + up256(words * 12 + 16));
+  if (stage) w.stage = reinterpret_cast<float*>(b + up256(words * 12 + 16) + up256((size_t)((p.D + 63) / 64) * TICK_STRIDE * 4));
+  return w;
+}
+
+hipError_t launch_prep(const GlrParams& p, const TileWs& w, const void* from, int from_dtype, hipStream_t stream) {
+  const int64_t fill = (3 * (int64_t)w.tiles * p.D + 3) / 4, rows = w.stage || p.cu || p.T == 0 ? (int64_t)p.nseq * p.D : 0;
+  const int64_t blocks = ((fill > rows ? fill : rows) + 255) / 256;
+  hipLaunchKernelGGL(kda_glr_prep_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream, p, w, from,
+                     from_dtype);
+  return hipGetLastError();
+}
+
+// Few tokens per sequence: rows of at most 16 tokens, packed batches of at most 2 on average
+// (as kda_fwd's own rule; the lengths stay on the device).
+bool few_tokens(const GlrParams& p) { return p.cu ? p.T <= 2 * (int64_t)p.nseq : p.T <= 16; }
+
 }  // namespace
 
-hipError_t launch_glr_fwd(const GlrParams& p, hipStream_t stream) {
+size_t glr_workspace(int64_t tokens, int64_t D, int64_t nseq) {
+  const size_t words = (size_t)tile_count(tokens) * (size_t)D;
+  return up256(words * 12 + 16) + up256((size_t)((D + 63) / 64) * TICK_STRIDE * 4) + up256((size_t)nseq * D * 4);
+}
+
+bool glr_fits(int64_t tokens, int64_t D, int64_t nseq) {
+  const int64_t cols = (D + 63) / 64, most = (int64_t)1 << 24;   // workgroups of a launch
+  return cols * ((tokens + GLR_TILE - 1) / GLR_TILE) < most && cols * nseq < most;
+}
+
+hipError_t launch_glr_fwd(const GlrParams& p, void* workspace, hipStream_t stream) {
   if (p.nseq <= 0) return hipSuccess;
-  return by_dtype(p.dtype, [&](auto dt) {
-    hipLaunchKernelGGL(kda_glr_fwd_kernel<dt.value>, dim3((p.D + 63) / 64, p.nseq), dim3(64), 0, stream, p);
+  if (p.in_slots || few_tokens(p)) {
+    return by_type(p.dtype, p.D, [&](auto dt, auto vec) {
+      const int cols = (p.D + 64 * vec.value - 1) / (64 * vec.value);
+      const dim3 grid((unsigned)cols * (unsigned)p.nseq);
+      if (p.in_slots)
+        hipLaunchKernelGGL((kda_glr_tokens_kernel<dt.value, vec.value, true>), grid, dim3(64), 0, stream, p, cols);
+      else
+        hipLaunchKernelGGL((kda_glr_tokens_kernel<dt.value, vec.value, false>), grid, dim3(64), 0, stream, p, cols);
+    });
+  }
+  // a sequence's final state may be written while another workgroup still reads its initial one
+  const bool stage = p.init && p.init == p.fin;
+  const TileWs w = tile_ws(p, workspace, stage);
+  hipError_t e = launch_prep(p, w, p.init, p.init_dtype, stream);
+  if (e != hipSuccess) return e;
+  GlrParams q = p;
+  if (stage) {
+    q.init = w.stage;
+    q.init_dtype = FP32;
+  }
+  return by_type(p.dtype, p.D, [&](auto dt, auto vec) {
+    hipLaunchKernelGGL((kda_glr_fwd_tile_kernel<dt.value, vec.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
+                       0, stream, q, q.cu, w);
   });
 }
 
-hipError_t launch_glr_bwd(const GlrParams& p, hipStream_t stream) {
+hipError_t launch_glr_bwd(const GlrParams& p, void* workspace, hipStream_t stream) {
   if (p.nseq <= 0) return hipSuccess;
-  return by_dtype(p.dtype, [&](auto dt) {
-    hipLaunchKernelGGL(kda_glr_bwd_kernel<dt.value>, dim3((p.D + 63) / 64, p.nseq), dim3(64), 0, stream, p);
+  const TileWs w = tile_ws(p, workspace, false);
+  const hipError_t e = launch_prep(p, w, p.dfin, p.dfin_dtype, stream);
+  if (e != hipSuccess || w.tiles == 0) return e;
+  return by_type(p.dtype, p.D, [&](auto dt, auto vec) {
+    hipLaunchKernelGGL((kda_glr_bwd_tile_kernel<dt.value, vec.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
+                       0, stream, p, p.cu, w);
   });
 }
 

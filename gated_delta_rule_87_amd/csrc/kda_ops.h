@@ -35,8 +35,10 @@ struct GlrParams {
   int32_t n_slots;
 };
 
-hipError_t launch_glr_fwd(const GlrParams& p, hipStream_t stream);
-hipError_t launch_glr_bwd(const GlrParams& p, hipStream_t stream);
+size_t glr_workspace(int64_t tokens, int64_t D, int64_t nseq);
+bool glr_fits(int64_t tokens, int64_t D, int64_t nseq);   // within what a launch can hold
+hipError_t launch_glr_fwd(const GlrParams& p, void* workspace, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrParams& p, void* workspace, hipStream_t stream);
 
 // ---- layer norm (kda_layernorm.hip) ----
 struct NormParams {

@@ -41,7 +41,7 @@ int check_glr(const void* a, const void* b, const void* c, int dtype, const int6
   if (B < 1 || T < 0 || D < 1 || D > MAX_D) return KDA_ERR_SHAPE;
   if (cu && (B != 1 || N < 1)) return KDA_ERR_SHAPE;
   if (T > INT32_MAX / 2 || B > INT32_MAX / 2 || B * T >= (int64_t)INT32_MAX / 2) return KDA_ERR_SHAPE;
-  if ((cu ? N : B) >= 65536) return KDA_ERR_SHAPE;
+  if ((cu ? N : B) > INT32_MAX / 2 || !kda::glr_fits(B * T, D, cu ? N : B)) return KDA_ERR_SHAPE;
   if (bad_dtype(dtype)) return KDA_ERR_DTYPE;
   return KDA_OK;
 }
@@ -82,8 +82,8 @@ int64_t kda_glr_carry_rows(int64_t B, int64_t T) {
 }
 
 size_t kda_glr_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N) {
-  (void)B, (void)T, (void)D, (void)N;
-  return 0;
+  if (B < 1 || T < 0 || D < 1 || N < 0 || D > MAX_D || T > INT32_MAX || B > INT32_MAX || N > INT32_MAX) return 0;
+  return kda::glr_workspace(B * T, D, N > 0 ? N : B);
 }
 
 int kda_glr_fwd(const void* x, const void* g, void* y, int dtype, const void* initial_state, int initial_dtype,
@@ -95,11 +95,8 @@ int kda_glr_fwd(const void* x, const void* g, void* y, int dtype, const void* in
   if (rc != KDA_OK) return rc;
   if (initial_state && final_state && initial_dtype != final_dtype) return KDA_ERR_DTYPE;
   if (any_unaligned({x, g, y, initial_state, final_state, carry}, 16) || any_unaligned({cu_seqlens}, 8)) return KDA_ERR_ALIGN;
-  const size_t need = kda_glr_workspace_size(B, T, D, cu_seqlens ? N : 0);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
-    if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
-  }
+  if (!workspace || workspace_bytes < kda_glr_workspace_size(B, T, D, cu_seqlens ? N : 0)) return KDA_ERR_WORKSPACE;
+  if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (cu_seqlens && kda::env_flag("KDA_VALIDATE")) {
     rc = kda::validate_cu_on_host(cu_seqlens, N, T, st);
@@ -110,7 +107,7 @@ int kda_glr_fwd(const void* x, const void* g, void* y, int dtype, const void* in
   p.fin = final_state;
   p.fin_dtype = final_dtype;
   p.carry = carry;
-  return status(kda::launch_glr_fwd(p, st));
+  return status(kda::launch_glr_fwd(p, workspace, st));
 }
 
 int kda_glr_bwd(const void* x, const void* g, const void* dy, int dtype, const float* carry, const void* initial_state,
@@ -123,13 +120,11 @@ int kda_glr_bwd(const void* x, const void* g, const void* dy, int dtype, const f
   if (rc == KDA_OK) rc = check_state(d_final, d_final_dtype);
   if (rc == KDA_OK) rc = check_state(d_initial, d_initial_dtype);
   if (rc != KDA_OK) return rc;
+  if (d_initial && (d_initial == d_final || d_initial == initial_state)) return KDA_ERR_VALUE;
   if (any_unaligned({x, g, dy, carry, initial_state, d_final, dx, dg, d_initial}, 16) || any_unaligned({cu_seqlens}, 8))
     return KDA_ERR_ALIGN;
-  const size_t need = kda_glr_workspace_size(B, T, D, cu_seqlens ? N : 0);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
-    if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
-  }
+  if (!workspace || workspace_bytes < kda_glr_workspace_size(B, T, D, cu_seqlens ? N : 0)) return KDA_ERR_WORKSPACE;
+  if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (cu_seqlens && kda::env_flag("KDA_VALIDATE")) {
     rc = kda::validate_cu_on_host(cu_seqlens, N, T, st);
@@ -144,12 +139,12 @@ int kda_glr_bwd(const void* x, const void* g, const void* dy, int dtype, const f
   p.dfin = d_final;
   p.dfin_dtype = d_final_dtype;
   p.carry = const_cast<float*>(carry);
-  return status(kda::launch_glr_bwd(p, st));
+  return status(kda::launch_glr_bwd(p, workspace, st));
 }
 
 int kda_glr_step(const void* x, const void* g, void* y, int dtype, void* state, int state_dtype, int64_t S,
                  const int32_t* in_slots, const int32_t* out_slots, int64_t N, int64_t D, void* stream) {
-  if (N < 0 || N >= 65536 || D < 1 || D > MAX_D || S < 1 || S > MAX_SLOTS) return KDA_ERR_SHAPE;
+  if (N < 0 || N > INT32_MAX || D < 1 || D > MAX_D || S < 1 || S > MAX_SLOTS || !kda::glr_fits(0, D, N)) return KDA_ERR_SHAPE;
   if (!state || (N != 0 && (!x || !g || !y || !in_slots || !out_slots))) return KDA_ERR_NULL;
   if (bad_dtype(dtype) || (state_dtype != KDA_STATE_BF16 && state_dtype != KDA_STATE_FP32)) return KDA_ERR_DTYPE;
   if (any_unaligned({x, g, y, state}, 16) || any_unaligned({in_slots, out_slots}, 4)) return KDA_ERR_ALIGN;
@@ -160,7 +155,7 @@ int kda_glr_step(const void* x, const void* g, void* y, int dtype, void* state, 
   p.in_slots = in_slots;
   p.out_slots = out_slots;
   p.n_slots = (int32_t)S;
-  return status(kda::launch_glr_fwd(p, static_cast<hipStream_t>(stream)));
+  return status(kda::launch_glr_fwd(p, nullptr, static_cast<hipStream_t>(stream)));
 }
 
 size_t kda_layernorm_workspace_size(int64_t M, int64_t D) {

@@ -352,7 +352,8 @@ enum kda_dtype {
  *                         of 16 bytes are fastest)
  *   initial_state, final_state, their dtypes, cu_seqlens, N, B, T
  *                         as for kda_fwd, with states [B|N, D]. Tokens of a packed
- *                         batch that no sequence covers are neither read nor written.
+ *                         batch that no sequence covers are not used, and their
+ *                         outputs are left as they were.
  *   carry                 fp32 [kda_glr_carry_rows(B, T), D]: the state that enters
  *                         every 128th of the B * T packed tokens. kda_glr_fwd writes
  *                         it where it is not NULL; kda_glr_bwd needs the one of the
@@ -362,7 +363,8 @@ enum kda_dtype {
  *                         gradient of final_state (NULL/KDA_STATE_NONE: zero) and
  *                         of initial_state (NULL/KDA_STATE_NONE: not written),
  *                         [B|N, D] bf16/fp32 each. An empty sequence's d_initial is
- *                         its d_final. May not alias each other.
+ *                         its d_final. d_initial may be neither d_final nor
+ *                         initial_state (KDA_ERR_VALUE).
  *   workspace             caller-owned, kda_glr_workspace_size(B, T, D, N) bytes
  *                         (N = 0 without cu_seqlens) for either direction, 256-byte
  *                         aligned; contents need no initialisation and are clobbered

@@ -7,10 +7,16 @@ plus 2u|g| from rounding the exponent, a product or a fused multiply-add by u of
 sum, and taking the tokens in groups whose affine maps are composed adds at most four more
 roundings a token: STEP(g) = (8 + 2|g|) u of the sum of absolute terms, carried along by the
 recurrence itself. Rounding the result to its type adds half a step of it.
+
+An exp(g) below the smallest normal fp32 number (g < -87.3) may come out as zero: it is then
+off by less than TINY = 2^-126, so the state before, of absolute sum s, adds less than TINY s
+(and to dg, which multiplies by h_{t-1}, TINY s |h_{t-1}|: s and h can each be above one, so
+the smallest normal number alone does not cover it).
 """
 import torch
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126
 
 
 def half_step(dtype):
@@ -39,8 +45,9 @@ def glr(x, g, sp, h0=None, dy=None, d_final=None):
         for t in range(b, t1):
             v["before"][t], e["before"][t] = h, err
             h = a[t] * h + x[t]
+            lost = TINY * s
             s = a[t] * s + x[t].abs()
-            err = a[t] * err + step[t] * s
+            err = a[t] * err + step[t] * s + lost
             v["y"][t], e["y"][t] = h, err
         v["final"][i], e["final"][i] = h, err
     if dy is None:
@@ -56,8 +63,9 @@ def glr(x, g, sp, h0=None, dy=None, d_final=None):
             G, s = dy[t] + E, s + dy[t].abs()
             err = err + U * s
             v["dx"][t], e["dx"][t] = G, err
+            lost = TINY * s
             E, s = a[t] * G, a[t] * s
-            err = a[t] * err + step[t] * s
+            err = a[t] * err + step[t] * s + lost
             v["dg"][t] = E * v["before"][t]
             e["dg"][t] = err * v["before"][t].abs() + (E.abs() + err) * e["before"][t] + 2 * U * v["dg"][t].abs()
         v["d_initial"][i], e["d_initial"][i] = E, err

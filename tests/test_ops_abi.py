@@ -52,8 +52,8 @@ def test_glr_refusals(name, d):
         assert go(**{k: None}) == ENULL, k
         assert go(**{k: d[k] + 2}) == EALIGN, k
     for bad in (dict(B=0), dict(T=-1), dict(D=0), dict(D=(1 << 24) + 1), dict(cu=fake(7), N=2), dict(cu=fake(7), N=0, B=1),
-                dict(B=1 << 20, T=1 << 20), dict(B=1 << 62, T=4), dict(T=1 << 62), dict(B=70000, T=1),
-                dict(cu=fake(7), N=70000, B=1)):
+                dict(B=1 << 20, T=1 << 20), dict(B=1 << 62, T=4), dict(T=1 << 62), dict(B=1 << 24, T=1),
+                dict(cu=fake(7), N=1 << 24, B=1), dict(T=1 << 29, D=1 << 20)):
         assert go(**bad) == ESHAPE, bad
     assert go(dtype=0) == EDTYPE and go(dtype=4) == EDTYPE and go(dtype=-1) == EDTYPE
     for p, c in ([("h0", "h0d"), ("hT", "hTd")] if third == "y" else [("h0", "h0d"), ("df", "dfd"), ("d0", "d0d")]):
@@ -61,12 +61,13 @@ def test_glr_refusals(name, d):
         assert go(**{p: None, c: 2}) == ENULL
         assert go(**{p: fake(8) + 4, c: 2}) == EALIGN
     assert go(cu=fake(7) + 4, N=2, B=1) == EALIGN
+    if third == "dy":
+        assert go(df=fake(8), dfd=2, d0=fake(8), d0d=2) == EVALUE and go(h0=fake(8), h0d=2, d0=fake(8), d0d=2) == EVALUE
     if third == "y":
         assert go(h0=fake(8), h0d=1, hT=fake(8), hTd=2) == EDTYPE
         assert go(carry=fake(8) + 4) == EALIGN
     need = kda.glr_workspace_size(2, 100, 64)
-    if need:
-        assert go(ws=None) == EWS and go(wsb=need - 1) == EWS and go(ws=fake(9) + 16) == EALIGN
+    assert need > 0 and go(ws=None) == EWS and go(wsb=need - 1) == EWS and go(ws=fake(9) + 16) == EALIGN
     # no tokens: the token tensors may be NULL, the checks after them still hold
     null = {k: None for k in ("x", "g", third) + (("carry", "dx", "dg") if third == "dy" else ())}
     assert go(T=0, D=0, **null) == ESHAPE and go(T=0, dtype=9, **null) == EDTYPE
@@ -88,7 +89,7 @@ def test_glr_step_refusals():
     for k in ("x", "g", "y", "state", "src", "dst"):
         assert go(**{k: None}) == ENULL, k
         assert go(**{k: STEP[k] + 2}) == EALIGN, k
-    for bad in (dict(N=-1), dict(N=65536), dict(D=0), dict(S=0), dict(S=(1 << 24) + 1)):
+    for bad in (dict(N=-1), dict(N=1 << 24), dict(N=1 << 40), dict(D=0), dict(S=0), dict(S=(1 << 24) + 1)):
         assert go(**bad) == ESHAPE, bad
     assert go(dtype=5) == EDTYPE and go(sd=0) == EDTYPE and go(sd=3) == EDTYPE
 
