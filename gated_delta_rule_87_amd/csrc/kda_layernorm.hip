@@ -1,4 +1,17 @@
 // kda_layernorm.hip -- layer norm of rows, forward and backward (gfx950).
+//
+// Both directions are bound by memory: the forward pass reads x and writes y, the backward
+// pass reads dy and x and writes dx. A row is loaded once into the registers of LANES lanes
+// (8 of a wave for the shortest rows, a workgroup of 1024 for the widest), 16 bytes a lane and
+// vector; statistics are two sums over those registers (the mean, then the squares of the
+// centred values: no cancellation for rows far from zero). Workgroups take rows in strides and
+// keep the weight, and in the backward pass the sums of dy xhat and dy of their columns, in
+// registers from row to row; each writes its sums once to the workspace, and a second kernel
+// adds those in a fixed order.
+//
+// Rows need not be whole numbers of vectors nor aligned to them: vectors are loaded at any
+// address (the hardware splits what crosses a line), a row's last elements one by one. Rows of
+// more than 16384 elements do not fit the registers of a workgroup and are read three times.
 #include <type_traits>
 
 #include "kda_elem.h"
@@ -7,129 +20,534 @@
 namespace kda {
 namespace {
 
-__device__ __forceinline__ float block_sum(float v, float* buf) {   // 256 threads
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return buf[0] + buf[1] + buf[2] + buf[3];
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float swap16_add(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float swap32_add(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+// Sum over groups of 8, 16 or 64 lanes, the same bits in every lane.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+  x = dpp_add<0xB1>(x);    // lane ^ 1
+  x = dpp_add<0x1B>(x);    // lane ^ 3
+  x = dpp_add<0x141>(x);   // lane ^ 7
+  if constexpr (LANES >= 16) x = dpp_add<0x140>(x);   // lane ^ 15
+  if constexpr (LANES >= 64) x = swap32_add(swap16_add(x));
+  return x;
 }
 
-// One workgroup per row, the row read three times.
+// Sums of K values over LANES lanes. Rows of several waves go through buf, one barrier a call:
+// consecutive calls take different halves of it.
+template <int LANES, int K>
+__device__ __forceinline__ void row_sums(float* v, float (*buf)[K], int half) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = lanes_sum<(LANES > 64 ? 64 : LANES)>(v[k]);
+  if constexpr (LANES > 64) {
+    constexpr int W = LANES / 64;
+    float (*b)[K] = buf + half * W;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) b[threadIdx.x >> 6][k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float s = b[0][k];
+#pragma unroll
+      for (int w = 1; w < W; ++w) s += b[w][k];
+      v[k] = s;
+    }
+  }
+}
+
+// c elements (at most VEC) from element i on, zeros behind them; any alignment
+template <int DT, int VEC>
+__device__ __forceinline__ void load_part(Pack<DT, VEC>& q, const void* p, size_t i, int c) {
+  if (c >= VEC) {
+    __builtin_memcpy(&q.r, static_cast<const uint8_t*>(p) + i * elem_size(DT), sizeof(q.r));
+  } else {
+    float f[VEC] = {};
+#pragma unroll
+    for (int e = 0; e < VEC - 1; ++e)
+      if (e < c) load_f32<DT, 1>(p, i + e, f + e);
+    q.pack(f);
+  }
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void store_part(const Pack<DT, VEC>& q, void* p, size_t i, int c) {
+  if (c >= VEC) {
+    __builtin_memcpy(static_cast<uint8_t*>(p) + i * elem_size(DT), &q.r, sizeof(q.r));
+  } else {
+    float f[VEC];
+    q.unpack(f);
+#pragma unroll
+    for (int e = 0; e < VEC - 1; ++e)
+      if (e < c) store_f32<DT, 1>(p, i + e, f + e);
+  }
+}
+// c fp32 parameters of columns i on, or a constant
+template <int VEC>
+__device__ __forceinline__ void load_param(const float* p, int i, int c, float none, float* f) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) f[e] = e < c ? (p ? p[i + e] : none) : 0.0f;
+}
+
 template <int DT>
-__global__ __launch_bounds__(256) void kda_layernorm_fwd_kernel(NormParams p) {
-  __shared__ float buf[4];
-  const int tid = threadIdx.x;
+constexpr int vec_of() { return 16 / elem_size(DT); }
+constexpr int wg_of(int lanes) { return lanes > 256 ? lanes : 256; }
+
+// ---- forward ----------------------------------------------------------------------
+
+// A lane holds NV vectors of a row, U rows at a time.
+template <int DT, int LANES, int NV, int U>
+__global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormParams p) {
+  constexpr int VEC = vec_of<DT>(), G = wg_of(LANES) / LANES;
+  __shared__ float buf[LANES > 64 ? 2 * LANES / 64 : 1][U];
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  const float inv = 1.0f / p.D;
+  float w[NV][VEC], b[NV][VEC];
+  int c[NV];   // elements of this lane's vectors
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * LANES + lane) * VEC;
+    c[i] = p.D - col < 0 ? 0 : p.D - col > VEC ? VEC : p.D - col;
+    load_param<VEC>(p.weight, col, c[i], 1.0f, w[i]);
+    load_param<VEC>(p.bias, col, c[i], 0.0f, b[i]);
+  }
+  for (int64_t m0 = (int64_t)blockIdx.x * G * U; m0 < p.M; m0 += (int64_t)gridDim.x * G * U) {
+    Pack<DT, VEC> x[U][NV];
+    float s[U], q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * G + grp;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        x[u][i].clear();
+        if (m < p.M && c[i] > 0) load_part(x[u][i], p.x, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[VEC];
+        x[u][i].unpack(f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[u] += f[e];
+      }
+    }
+    row_sums<LANES, U>(s, buf, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] /= p.D;   // a division: the mean of a row of one value is that value, its centred values zero
+      q[u] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[VEC];
+        x[u][i].unpack(f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = e < c[i] ? f[e] - s[u] : 0.0f;
+          q[u] = fmaf(d, d, q[u]);
+        }
+      }
+    }
+    row_sums<LANES, U>(q, buf, 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * G + grp;
+      const float mean = s[u], rstd = 1.0f / sqrtf(q[u] * inv + p.eps);
+      if (m >= p.M) continue;
+      if (lane == 0) {
+        if (p.mean) p.mean[m] = mean;
+        if (p.rstd) p.rstd[m] = rstd;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[VEC];
+        x[u][i].unpack(f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[i][e], b[i][e]);
+        Pack<DT, VEC> y;
+        y.pack(f);
+        if (c[i] > 0) store_part(y, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+      }
+    }
+  }
+}
+
+// Rows of more than 16384 elements: a workgroup reads a row three times.
+template <int DT>
+__global__ __launch_bounds__(1024) void kda_layernorm_fwd_long_kernel(NormParams p) {
+  constexpr int VEC = vec_of<DT>();
+  __shared__ float buf[2 * 16][1];
+  const float inv = 1.0f / p.D;
   for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
     const size_t row = (size_t)m * p.D;
-    float s = 0.0f, q = 0.0f, v;
-    for (int d = tid; d < p.D; d += 256) {
-      load_f32<DT, 1>(p.x, row + d, &v);
-      s += v;
-    }
-    const float mean = block_sum(s, buf) / p.D;
-    for (int d = tid; d < p.D; d += 256) {
-      load_f32<DT, 1>(p.x, row + d, &v);
-      q += (v - mean) * (v - mean);
-    }
-    const float rstd = 1.0f / sqrtf(block_sum(q, buf) / p.D + p.eps);
-    if (tid == 0) {
+    float s = 0.0f, q = 0.0f;
+    auto each = [&](auto f) {
+      for (int64_t col = (int64_t)threadIdx.x * VEC; col < p.D; col += 1024 * VEC) {
+        const int c = p.D - col < VEC ? (int)(p.D - col) : VEC;
+        Pack<DT, VEC> x;
+        load_part(x, p.x, row + col, c);
+        float v[VEC];
+        x.unpack(v);
+        f((int)col, c, v);
+      }
+    };
+    each([&](int, int, const float* v) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += v[e];
+    });
+    row_sums<1024, 1>(&s, buf, 0);
+    const float mean = s / p.D;
+    each([&](int, int c, const float* v) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < c) q = fmaf(v[e] - mean, v[e] - mean, q);
+    });
+    row_sums<1024, 1>(&q, buf, 1);
+    const float rstd = 1.0f / sqrtf(q * inv + p.eps);
+    if (threadIdx.x == 0) {
       if (p.mean) p.mean[m] = mean;
       if (p.rstd) p.rstd[m] = rstd;
     }
-    for (int d = tid; d < p.D; d += 256) {
-      load_f32<DT, 1>(p.x, row + d, &v);
-      const float y = fmaf((v - mean) * rstd, p.weight ? p.weight[d] : 1.0f, p.bias ? p.bias[d] : 0.0f);
-      store_f32<DT, 1>(p.out, row + d, &y);
-    }
+    each([&](int col, int c, const float* v) {
+      float w[VEC], b[VEC];
+      load_param<VEC>(p.weight, col, c, 1.0f, w);
+      load_param<VEC>(p.bias, col, c, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+      Pack<DT, VEC> y;
+      y.pack(w);
+      store_part(y, p.out, row + col, c);
+    });
   }
 }
 
-// One workgroup per run of rows; each thread keeps the sums of its columns in its part of
-// the workspace.
-template <int DT>
-__global__ __launch_bounds__(256) void kda_layernorm_bwd_kernel(NormParams p, int parts) {
-  __shared__ float buf[4];
-  const int tid = threadIdx.x;
+// ---- backward ---------------------------------------------------------------------
+
+// Sum over the row groups of a workgroup: the groups of a wave by lane swaps, the waves'
+// through shared memory; lanes 0 .. LANES - 1 of the workgroup end with the total.
+template <int LANES>
+__device__ __forceinline__ float groups_sum(float v, float* buf) {
+  if constexpr (LANES == 8) v = v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, false));   // row_ror 8
+  if constexpr (LANES <= 16) v = swap32_add(swap16_add(v));
+  if constexpr (LANES <= 64) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    if (lane < LANES) buf[wave * LANES + lane] = v;
+    __syncthreads();
+    v = 0.0f;
+    if (threadIdx.x < LANES) v = (buf[lane] + buf[LANES + lane]) + (buf[2 * LANES + lane] + buf[3 * LANES + lane]);
+  }
+  return v;
+}
+
+template <int DT, int LANES, int NV, int U>
+__global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_bwd_kernel(NormParams p, int parts) {
+  constexpr int VEC = vec_of<DT>(), G = wg_of(LANES) / LANES;
+  __shared__ float buf[LANES > 64 ? 2 * LANES / 64 : 1][2 * U];
+  __shared__ float gbuf[LANES <= 64 ? 4 * LANES : 1];
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  const float inv = 1.0f / p.D;
+  float w[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+  int c[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * LANES + lane) * VEC;
+    c[i] = p.D - col < 0 ? 0 : p.D - col > VEC ? VEC : p.D - col;
+    load_param<VEC>(p.weight, col, c[i], 1.0f, w[i]);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) aw[i][e] = ab[i][e] = 0.0f;
+  }
+  int half = 0;
+  for (int64_t m0 = (int64_t)blockIdx.x * G * U; m0 < p.M; m0 += (int64_t)gridDim.x * G * U) {
+    Pack<DT, VEC> x[U][NV], dy[U][NV];
+    float mean[U], rstd[U], s[2 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * G + grp;
+      mean[u] = rstd[u] = 0.0f;
+      if (m < p.M) {
+        mean[u] = p.mean[m];
+        rstd[u] = p.rstd[m];
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        x[u][i].clear();
+        dy[u][i].clear();
+        if (m < p.M && c[i] > 0) {
+          const size_t at = (size_t)m * p.D + (i * LANES + lane) * VEC;
+          load_part(x[u][i], p.x, at, c[i]);
+          load_part(dy[u][i], p.dy, at, c[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float xf[VEC], df[VEC];
+        x[u][i].unpack(xf);
+        dy[u][i].unpack(df);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {   // dy and the weight are zero behind a row's end
+          const float xh = (xf[e] - mean[u]) * rstd[u], a = df[e] * w[i][e];
+          s1 += a;
+          s2 = fmaf(a, xh, s2);
+          aw[i][e] = fmaf(df[e], xh, aw[i][e]);
+          ab[i][e] += df[e];
+        }
+      }
+      s[2 * u] = s1;
+      s[2 * u + 1] = s2;
+    }
+    if (!p.out) continue;
+    row_sums<LANES, 2 * U>(s, buf, half);
+    half ^= 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * G + grp;
+      if (m >= p.M) continue;
+      const float c1 = s[2 * u] * inv, c2 = s[2 * u + 1] * inv;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float xf[VEC], df[VEC];
+        x[u][i].unpack(xf);
+        dy[u][i].unpack(df);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (xf[e] - mean[u]) * rstd[u];
+          df[e] = rstd[u] * (fmaf(df[e], w[i][e], -c1) - xh * c2);
+        }
+        Pack<DT, VEC> dx;
+        dx.pack(df);
+        if (c[i] > 0) store_part(dx, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+      }
+    }
+  }
+  if (!p.partial) return;
   float* pw = p.partial + (size_t)blockIdx.x * p.D;
   float* pb = p.partial + ((size_t)parts + blockIdx.x) * p.D;
-  if (p.partial)
-    for (int d = tid; d < p.D; d += 256) pw[d] = pb[d] = 0.0f;
-  for (int64_t m = blockIdx.x; m < p.M; m += parts) {
-    const size_t row = (size_t)m * p.D;
-    const float mean = p.mean[m], rstd = p.rstd[m];
-    float s1 = 0.0f, s2 = 0.0f, x, dy;
-    for (int d = tid; d < p.D; d += 256) {
-      load_f32<DT, 1>(p.x, row + d, &x);
-      load_f32<DT, 1>(p.dy, row + d, &dy);
-      const float a = dy * (p.weight ? p.weight[d] : 1.0f);
-      s1 += a;
-      s2 += a * (x - mean) * rstd;
-    }
-    const float c1 = block_sum(s1, buf) / p.D;
-    const float c2 = block_sum(s2, buf) / p.D;
-    for (int d = tid; d < p.D; d += 256) {
-      load_f32<DT, 1>(p.x, row + d, &x);
-      load_f32<DT, 1>(p.dy, row + d, &dy);
-      const float xh = (x - mean) * rstd, a = dy * (p.weight ? p.weight[d] : 1.0f);
-      if (p.partial) {
-        pw[d] += dy * xh;
-        pb[d] += dy;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float sw = groups_sum<LANES>(aw[i][e], gbuf), sb = groups_sum<LANES>(ab[i][e], gbuf);
+      if (grp == 0 && e < c[i]) {
+        const int col = (i * LANES + lane) * VEC + e;
+        pw[col] = sw;
+        pb[col] = sb;
       }
-      const float dx = rstd * (a - c1 - xh * c2);
-      if (p.out) store_f32<DT, 1>(p.out, row + d, &dx);
     }
   }
 }
 
-__global__ __launch_bounds__(256) void kda_layernorm_sum_kernel(NormParams p, int parts) {
-  const int d = blockIdx.x * 256 + threadIdx.x;
-  if (d >= p.D) return;
-  float w = 0.0f, b = 0.0f;
-  for (int i = 0; i < parts; ++i) {
-    w += p.partial[(size_t)i * p.D + d];
-    b += p.partial[((size_t)parts + i) * p.D + d];
+// Rows of more than 16384 elements: dx from a row read twice by a workgroup ...
+template <int DT>
+__global__ __launch_bounds__(1024) void kda_layernorm_bwd_long_kernel(NormParams p) {
+  constexpr int VEC = vec_of<DT>();
+  __shared__ float buf[2 * 16][2];
+  const float inv = 1.0f / p.D;
+  int half = 0;
+  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    const size_t row = (size_t)m * p.D;
+    const float mean = p.mean[m], rstd = p.rstd[m];
+    float s[2] = {0.0f, 0.0f};
+    auto each = [&](auto f) {
+      for (int64_t col = (int64_t)threadIdx.x * VEC; col < p.D; col += 1024 * VEC) {
+        const int c = p.D - col < VEC ? (int)(p.D - col) : VEC;
+        Pack<DT, VEC> x, dy;
+        load_part(x, p.x, row + col, c);
+        load_part(dy, p.dy, row + col, c);
+        float xf[VEC], df[VEC], w[VEC];
+        x.unpack(xf);
+        dy.unpack(df);
+        load_param<VEC>(p.weight, (int)col, c, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          xf[e] = (xf[e] - mean) * rstd;
+          df[e] *= w[e];
+        }
+        f(col, c, xf, df);
+      }
+    };
+    each([&](int64_t, int, const float* xh, const float* a) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        s[0] += a[e];
+        s[1] = fmaf(a[e], xh[e], s[1]);
+      }
+    });
+    row_sums<1024, 2>(s, buf, half);
+    half ^= 1;
+    const float c1 = s[0] * inv, c2 = s[1] * inv;
+    each([&](int64_t col, int c, const float* xh, float* a) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) a[e] = rstd * (a[e] - c1 - xh[e] * c2);
+      Pack<DT, VEC> dx;
+      dx.pack(a);
+      store_part(dx, p.out, row + col, c);
+    });
   }
-  if (p.dw) p.dw[d] = w;
-  if (p.db) p.db[d] = b;
+}
+
+// ... and before it (dx may be written over dy or x) the columns' sums: a lane per VEC columns,
+// part i the rows i, i + parts, ...
+template <int DT>
+__global__ __launch_bounds__(64) void kda_layernorm_cols_kernel(NormParams p, int parts) {
+  constexpr int VEC = vec_of<DT>();
+  const int part = blockIdx.x % parts;
+  const int64_t col = ((int64_t)(blockIdx.x / parts) * 64 + threadIdx.x) * VEC;
+  if (col >= p.D) return;
+  const int c = p.D - col < VEC ? (int)(p.D - col) : VEC;
+  float aw[VEC] = {}, ab[VEC] = {};
+  for (int64_t m = part; m < p.M; m += parts) {
+    const float mean = p.mean[m], rstd = p.rstd[m];
+    Pack<DT, VEC> x, dy;
+    load_part(x, p.x, (size_t)m * p.D + col, c);
+    load_part(dy, p.dy, (size_t)m * p.D + col, c);
+    float xf[VEC], df[VEC];
+    x.unpack(xf);
+    dy.unpack(df);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      aw[e] = fmaf(df[e], (xf[e] - mean) * rstd, aw[e]);
+      ab[e] += df[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    if (e < c) {
+      p.partial[(size_t)part * p.D + col + e] = aw[e];
+      p.partial[((size_t)parts + part) * p.D + col + e] = ab[e];
+    }
+  }
+}
+
+// The parts' sums: 16 columns of dw (blockIdx.y 0) or db by 64 runs of parts a workgroup.
+__global__ __launch_bounds__(1024) void kda_layernorm_sum_kernel(NormParams p, int parts) {
+  __shared__ float buf[64][17];
+  float* out = blockIdx.y ? p.db : p.dw;
+  if (!out) return;
+  const float* in = p.partial + (blockIdx.y ? (size_t)parts * p.D : 0);
+  const int j = threadIdx.x & 15, run = threadIdx.x >> 4, col = blockIdx.x * 16 + j;
+  float s = 0.0f;
+  if (col < p.D) {
+#pragma unroll 8
+    for (int i = run; i < parts; i += 64) s += in[(size_t)i * p.D + col];
+  }
+  buf[run][j] = s;
+  __syncthreads();
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    if (run < o) buf[run][j] += buf[run + o][j];
+    __syncthreads();
+  }
+  if (run == 0 && col < p.D) out[col] = buf[0][j];
+}
+
+using std::integral_constant;
+template <int L, int V, int U>
+struct Shape {
+  static constexpr int lanes = L, nv = V, rows = U;
+};
+
+// f(element type, shape) for the fewest lanes and vectors that hold a row; false: none does
+template <int DT, typename F>
+bool by_width(int32_t D, F f) {
+  constexpr int V = vec_of<DT>();
+  if (D <= 8 * V) f(Shape<8, 1, 4>{});
+  else if (D <= 16 * V) f(Shape<16, 1, 4>{});
+  else if (D <= 32 * V) f(Shape<16, 2, 2>{});
+  else if (D <= 64 * V) f(Shape<16, 4, 1>{});
+  else if (D <= 128 * V) f(Shape<64, 2, 2>{});
+  else if (D <= 256 * V) f(Shape<64, 4, 1>{});
+  else if (D <= 512 * V) f(Shape<256, 2, 2>{});
+  else if (D <= 1024 * V) f(Shape<256, 4, 1>{});
+  else if (D <= 2048 * V) f(Shape<1024, 2, 1>{});
+  else if constexpr (V == 4) {
+    if (D <= 4096 * V) f(Shape<1024, 4, 1>{});
+    else return false;
+  } else {
+    return false;
+  }
+  return true;
 }
 
 template <typename F>
-hipError_t by_dtype(int dt, F f) {
-  if (dt == BF16) f(std::integral_constant<int, BF16>{});
-  else if (dt == FP32) f(std::integral_constant<int, FP32>{});
-  else f(std::integral_constant<int, FP16>{});
-  return hipGetLastError();
+void by_dtype(int dt, F f) {
+  if (dt == BF16) f(integral_constant<int, BF16>{});
+  else if (dt == FP32) f(integral_constant<int, FP32>{});
+  else f(integral_constant<int, FP16>{});
 }
+
+unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
 
 }  // namespace
 
+// Workgroups of a backward pass, at most: their sums take two rows of D each in the workspace,
+// so wide rows get one workgroup per compute unit and short ones enough to fill the GPU.
 size_t layernorm_parts(int64_t M, int64_t D) {
-  (void)D;
-  return (size_t)(M < 512 ? M : 512);
+  const int64_t most = D <= 2048 ? 1024 : D <= 8192 ? 512 : 256;
+  return (size_t)(M < most ? M : most);
 }
 
 hipError_t launch_layernorm_fwd(const NormParams& p, hipStream_t stream) {
   if (p.M == 0) return hipSuccess;
-  const unsigned blocks = (unsigned)(p.M < 65536 ? p.M : 65536);
-  return by_dtype(p.dtype, [&](auto dt) {
-    hipLaunchKernelGGL(kda_layernorm_fwd_kernel<dt.value>, dim3(blocks), dim3(256), 0, stream, p);
+  by_dtype(p.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const bool done = by_width<DT>(p.D, [&](auto shape) {
+      using S = decltype(shape);
+      constexpr int wg = wg_of(S::lanes), step = wg / S::lanes * S::rows;
+      hipLaunchKernelGGL((kda_layernorm_fwd_kernel<DT, S::lanes, S::nv, S::rows>),
+                         dim3(at_most((p.M + step - 1) / step, 2048 * 256 / wg)), dim3(wg), 0, stream, p);
+    });
+    if (!done)
+      hipLaunchKernelGGL(kda_layernorm_fwd_long_kernel<DT>, dim3(at_most(p.M, 4096)), dim3(1024), 0, stream, p);
   });
+  return hipGetLastError();
 }
 
 hipError_t launch_layernorm_bwd(const NormParams& p, hipStream_t stream) {
-  const int parts = (int)layernorm_parts(p.M, p.D);
-  hipError_t e = hipSuccess;
-  if (p.M > 0)
-    e = by_dtype(p.dtype, [&](auto dt) {
-      hipLaunchKernelGGL(kda_layernorm_bwd_kernel<dt.value>, dim3(parts), dim3(256), 0, stream, p, parts);
+  int parts = (int)layernorm_parts(p.M, p.D);
+  if (p.M > 0) {
+    by_dtype(p.dtype, [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      const bool done = by_width<DT>(p.D, [&](auto shape) {
+        using S = decltype(shape);
+        constexpr int wg = wg_of(S::lanes), step = wg / S::lanes * S::rows;
+        parts = (int)at_most((p.M + step - 1) / step, parts);
+        hipLaunchKernelGGL((kda_layernorm_bwd_kernel<DT, S::lanes, S::nv, S::rows>), dim3(parts), dim3(wg), 0, stream, p, parts);
+      });
+      if (!done) {
+        if (p.partial) {
+          const int64_t cols = ((int64_t)p.D + 64 * vec_of<DT>() - 1) / (64 * vec_of<DT>());
+          parts = (int)at_most(parts, 1 + 8192 / cols);
+          hipLaunchKernelGGL(kda_layernorm_cols_kernel<DT>, dim3((unsigned)cols * parts), dim3(64), 0, stream, p, parts);
+        }
+        if (p.out)
+          hipLaunchKernelGGL(kda_layernorm_bwd_long_kernel<DT>, dim3(at_most(p.M, 4096)), dim3(1024), 0, stream, p);
+      }
     });
-  if (e == hipSuccess && (p.dw || p.db)) {
-    hipLaunchKernelGGL(kda_layernorm_sum_kernel, dim3((p.D + 255) / 256), dim3(256), 0, stream, p, parts);
-    e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  return e;
+  if (p.dw || p.db) {
+    hipLaunchKernelGGL(kda_layernorm_sum_kernel, dim3((p.D + 15) / 16, 2), dim3(1024), 0, stream, p, parts);
+    return hipGetLastError();
+  }
+  return hipSuccess;
 }
 
 }  // namespace kda
