@@ -38,6 +38,15 @@ struct Pack {
   __device__ __forceinline__ void load(const void* p, size_t i) {
     r = *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p) + i * elem_size(DT));
   }
+  // at byte `uniform` (the same in every lane) plus a lane's 32-bit offset
+  __device__ __forceinline__ void load_at(const void* p, size_t uniform, uint32_t lane) {
+    r = *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p) + uniform + lane);
+  }
+  __device__ __forceinline__ void store_at(void* p, size_t uniform, uint32_t lane) const {
+    *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + uniform + lane) = r;
+  }
+  // the compiler forgets what it has computed from these registers
+  __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void clear() { r = Raw{}; }
 
   __device__ __forceinline__ void unpack(float* f) const {

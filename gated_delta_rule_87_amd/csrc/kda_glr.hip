@@ -74,27 +74,29 @@ struct TileWs {
 };
 
 // Publishes the tile's map, waits for the state that enters it and publishes the one that
-// leaves it; k: the tile's place in the order of processing.
-__device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, size_t d, float A, float L) {
-  uint64_t* maps = w.maps + d;
-  uint32_t* states = w.states + d;
+// leaves it; k: the tile's place in the order of processing, c0 + ch: the lane's channel.
+// (Addresses are a uniform base and a 32-bit lane offset each: one register, not two.)
+__device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, int c0, uint32_t ch, float A, float L) {
+  auto map_at = [&](int i) { return w.maps + ((size_t)i * D + c0) + ch; };
+  auto state_at = [&](int i) { return w.states + ((size_t)i * D + c0) + ch; };
   const bool more = k + 1 < w.tiles;
-  if (more) publish(maps + (size_t)k * D, ((uint64_t)word_of(L) << 32) | __float_as_uint(A));
-  if (more && (A < 0.0f || k == 0)) publish(states + (size_t)k * D, word_of(apply(A, L, 0.0f)));
+  if (more) publish(map_at(k), ((uint64_t)word_of(L) << 32) | __float_as_uint(A));
+  if (more && (A < 0.0f || k == 0)) publish(state_at(k), word_of(apply(A, L, 0.0f)));
   float h = 0.0f;
   for (bool found = k == 0; !found;) {
-    // state of the tile i places before (the one before the first tile: zero)
-    const uint32_t s1 = observe(states + (size_t)(k - 1) * D);
-    if (s1 != EMPTY) {
-      h = __uint_as_float(s1);
+    int t = k;
+    asm volatile("" : "+s"(t));   // addresses are formed anew: kept over the loop they cost 30 registers
+    const uint32_t s0 = observe(state_at(t - 1));
+    if (s0 != EMPTY) {
+      h = __uint_as_float(s0);
       break;
     }
-    uint32_t s[WINDOW];
+    uint32_t s[WINDOW];   // s[i]: the state that enters tile t - i (zero for the first); m[i]: that tile's map
     uint64_t m[WINDOW];
 #pragma unroll
     for (int i = 1; i < WINDOW; ++i) {
-      m[i] = k - i >= 0 ? observe(maps + (size_t)(k - i) * D) : ~0ull;
-      s[i] = k - i - 1 >= 0 ? observe(states + (size_t)(k - i - 1) * D) : k - i - 1 == -1 ? 0u : EMPTY;
+      m[i] = t - i >= 0 ? observe(map_at(t - i)) : ~0ull;
+      s[i] = t - i > 0 ? observe(state_at(t - i - 1)) : t == i ? 0u : EMPTY;
     }
     int at = 0;   // the nearest published state with all maps after it: i = at
     bool whole = true;
@@ -114,7 +116,7 @@ __device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, s
       __builtin_amdgcn_s_sleep(2);
     }
   }
-  if (more && !(A < 0.0f) && k != 0) publish(states + (size_t)k * D, word_of(apply(A, L, h)));
+  if (more && !(A < 0.0f) && k != 0) publish(state_at(k), word_of(apply(A, L, h)));
   return h;
 }
 
@@ -215,15 +217,17 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
   const int d = col * G::CH + lr * VEC;
   const bool d_ok = d < p.D;   // (a vector lies inside or outside: VEC divides D)
 
+  // token r of a group: a uniform base and the lane's 32-bit offset (one register for all)
+  const uint32_t off = ((uint32_t)(grp * R) * p.D + lr * VEC) * elem_size(DT);
+  auto at = [&](int r) { return ((size_t)(t_base + r) * p.D + col * G::CH) * elem_size(DT); };
   Pack<DT, VEC> g[R], x[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     g[r].clear();
     x[r].clear();
     if (d_ok && t0 + r < p.tokens) {
-      const size_t i = (size_t)(t0 + r) * p.D + d;
-      g[r].load(p.g, i);
-      x[r].load(p.x, i);
+      g[r].load_at(p.g, at(r), off);
+      x[r].load_at(p.x, at(r), off);
     }
   }
   find_places(p, cu, t_base, places);
@@ -274,24 +278,25 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
   }
   __syncthreads();
   if (tid < G::CH && col * G::CH + tid < p.D) {   // a lane per channel
-    const size_t dc = (size_t)col * G::CH + tid;
-    float A[G::GRP], L[G::GRP], TA = 1.0f, TL = 0.0f;
-#pragma unroll
-    for (int i = 0; i < G::GRP; ++i) {
-      A[i] = sA[i][tid];
-      L[i] = sL[i][tid];
-      compose(TA, TL, A[i], L[i]);
-    }
-    float h = pass_state(w, tile, p.D, dc, TA, TL);
-    if (p.carry) p.carry[(size_t)tile * p.D + dc] = h;
-#pragma unroll
+    float TA = 1.0f, TL = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < G::GRP; ++i) compose(TA, TL, sA[i][tid], sL[i][tid]);
+    float h = pass_state(w, tile, p.D, col * G::CH, tid, TA, TL);
+    if (p.carry) p.carry[(size_t)tile * p.D + col * G::CH + tid] = h;
+#pragma unroll 4
     for (int i = 0; i < G::GRP; ++i) {   // the state that enters each group
+      const float A = sA[i][tid], L = sL[i][tid];
       sL[i][tid] = h;
-      h = apply(A[i], L[i], h);
+      h = apply(A, L, h);
     }
   }
   __syncthreads();
   if (!d_ok) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    g[r].opaque();
+    x[r].opaque();
+  }
   float h[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) h[v] = sL[grp][lr * VEC + v];
@@ -306,7 +311,7 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
     for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
     Pack<DT, VEC> y;
     y.pack(h);
-    y.store(p.y, (size_t)(t0 + r) * p.D + d);
+    y.store_at(p.y, at(r), off);
     if (last >> r & 1) store_state<VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, h);
   }
 }
@@ -339,6 +344,8 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   const int d = col * G::CH + lr * VEC;
   const bool d_ok = d < p.D;
 
+  const uint32_t off = ((uint32_t)(grp * R) * p.D + lr * VEC) * elem_size(DT);
+  auto at = [&](int r) { return ((size_t)(t_base + r) * p.D + col * G::CH) * elem_size(DT); };
   Pack<DT, VEC> g[R], x[R], dy[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -346,10 +353,9 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     x[r].clear();
     dy[r].clear();
     if (d_ok && t0 + r < p.tokens) {
-      const size_t i = (size_t)(t0 + r) * p.D + d;
-      g[r].load(p.g, i);
-      x[r].load(p.x, i);
-      dy[r].load(p.dy, i);
+      g[r].load_at(p.g, at(r), off);
+      x[r].load_at(p.x, at(r), off);
+      dy[r].load_at(p.dy, at(r), off);
     }
   }
   find_places(p, cu, t_base, places);
@@ -365,6 +371,7 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     constexpr bool PLAIN = decltype(plain_c)::value;
 #pragma unroll
     for (int c = 0; c < VEC; c += NV) {
+      __builtin_amdgcn_sched_barrier(0);   // one word after the other
       float a[R][NV], A[NV], L[NV], B[NV], M[NV];
 #pragma unroll
       for (int v = 0; v < NV; ++v) A[v] = B[v] = 1.0f, L[v] = M[v] = 0.0f;
@@ -419,17 +426,17 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   if (tid < G::CH && col * G::CH + tid < p.D) {
     const size_t dc = (size_t)col * G::CH + tid;
     float TB = 1.0f, TM = 0.0f;
-#pragma unroll
+#pragma unroll 4
     for (int i = G::GRP - 1; i >= 0; --i) compose(TB, TM, sB[i][tid], sM[i][tid]);
     float h = p.carry[(size_t)tile * p.D + dc];
-    float E = pass_state(w, k, p.D, dc, TB, TM);
-#pragma unroll
+    float E = pass_state(w, k, p.D, col * G::CH, tid, TB, TM);
+#pragma unroll 4
     for (int i = 0; i < G::GRP; ++i) {
       const float A = sA[i][tid], L = sL[i][tid];
       sL[i][tid] = h;
       h = apply(A, L, h);
     }
-#pragma unroll
+#pragma unroll 4
     for (int i = G::GRP - 1; i >= 0; --i) {
       const float B = sB[i][tid], M = sM[i][tid];
       sM[i][tid] = E;
@@ -438,11 +445,17 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   }
   __syncthreads();
   if (!d_ok) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {   // the exps are computed again: kept, they would take R * VEC registers
+    g[r].opaque();
+    x[r].opaque();
+    dy[r].opaque();
+  }
 
-  auto outputs = [&](auto plain_c) {
-    constexpr bool PLAIN = decltype(plain_c)::value;
+  if (__all(plain)) {
 #pragma unroll
     for (int c = 0; c < VEC; c += NV) {
+      __builtin_amdgcn_sched_barrier(0);
       float a[R][NV], before[R][NV], h[NV], E[NV];
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -454,20 +467,17 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         float xf[NV];
         unpack_word<DT, VEC, NV>(g[r], c, a[r]);
         unpack_word<DT, VEC, NV>(x[r], c, xf);
-        if (!PLAIN && (first >> r & 1)) load_state<NV>(p.init, p.init_dtype, row(r) + c, h);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           a[r][v] = decay(a[r][v]);
           before[r][v] = h[v];
-          if (PLAIN || (in >> r & 1)) h[v] = fmaf(a[r][v], h[v], xf[v]);
+          h[v] = fmaf(a[r][v], h[v], xf[v]);
         }
       }
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
-        if (!PLAIN && !(in >> r & 1)) continue;
         float df[NV], dg[NV];
         unpack_word<DT, VEC, NV>(dy[r], c, df);
-        if (!PLAIN && (last >> r & 1)) load_state<NV>(p.dfin, p.dfin_dtype, row(r) + c, E);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           df[v] += E[v];
@@ -476,18 +486,71 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         }
         pack_word<DT, VEC, NV>(x[r], c, df);
         pack_word<DT, VEC, NV>(g[r], c, dg);
-        if (!PLAIN && (first >> r & 1)) store_state<NV>(p.fin, p.fin_dtype, row(r) + c, E);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {   // each pack stays one run of registers: no copies of it
+        g[r].opaque();
+        x[r].opaque();
       }
     }
-  };
-  if (__all(plain)) outputs(std::true_type{});
-  else outputs(std::false_type{});
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (!(in >> r & 1)) continue;
-    const size_t i = (size_t)(t0 + r) * p.D + d;
-    x[r].store(p.dx, i);
-    g[r].store(p.dg, i);
+    for (int r = 0; r < R; ++r) {
+      x[r].store_at(p.dx, at(r), off);
+      g[r].store_at(p.dg, at(r), off);
+    }
+    return;
+  }
+  // A wave whose tokens begin or end a sequence reads them again (they are in the caches), a
+  // word at a time: with the packs and every case of every token in registers at once, the
+  // kernel would need 242 of them and lose a third of its waves.
+  for (int c = 0; c < VEC; c += NV) {
+    float a[R][NV], before[R][NV], h[NV], E[NV];
+    int q = grp * R;
+    uint32_t o = off + c * elem_size(DT);
+    asm volatile("" : "+v"(q), "+v"(o));   // no address is kept from word to word
+    auto row = [&](int r) { return (size_t)places.n[q + r] * p.D + d + c; };
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      h[v] = sL[grp][lr * VEC + c + v];
+      E[v] = sM[grp][lr * VEC + c + v];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!(in >> r & 1)) continue;
+      Pack<DT, NV> gq, xq;
+      gq.load_at(p.g, at(r), o);
+      xq.load_at(p.x, at(r), o);
+      float xf[NV];
+      gq.unpack(a[r]);
+      xq.unpack(xf);
+      if (first >> r & 1) load_state<NV>(p.init, p.init_dtype, row(r), h);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        a[r][v] = decay(a[r][v]);
+        before[r][v] = h[v];
+        h[v] = fmaf(a[r][v], h[v], xf[v]);
+      }
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      if (!(in >> r & 1)) continue;
+      Pack<DT, NV> q1, q2;
+      float df[NV], dg[NV];
+      q1.load_at(p.dy, at(r), o);
+      q1.unpack(df);
+      if (last >> r & 1) load_state<NV>(p.dfin, p.dfin_dtype, row(r), E);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        df[v] += E[v];
+        E[v] = a[r][v] * df[v];
+        dg[v] = E[v] * before[r][v];
+      }
+      q1.pack(df);
+      q2.pack(dg);
+      q1.store_at(p.dx, at(r), o);
+      q2.store_at(p.dg, at(r), o);
+      if (first >> r & 1) store_state<NV>(p.fin, p.fin_dtype, row(r), E);
+    }
   }
 }
 
