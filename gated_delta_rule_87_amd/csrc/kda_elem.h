@@ -45,6 +45,10 @@ struct Pack {
   __device__ __forceinline__ void store_at(void* p, size_t uniform, uint32_t lane) const {
     *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + uniform + lane) = r;
   }
+  // whole rows of outputs, not kept in the caches: the inputs stay there instead
+  __device__ __forceinline__ void stream_at(void* p, size_t uniform, uint32_t lane) const {
+    __builtin_nontemporal_store(r, reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + uniform + lane));
+  }
   // the compiler forgets what it has computed from these registers
   __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void clear() { r = Raw{}; }

@@ -311,7 +311,7 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
     for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
     Pack<DT, VEC> y;
     y.pack(h);
-    y.store_at(p.y, at(r), off);
+    y.stream_at(p.y, at(r), off);
     if (last >> r & 1) store_state<VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, h);
   }
 }
@@ -495,8 +495,8 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r].store_at(p.dx, at(r), off);
-      g[r].store_at(p.dg, at(r), off);
+      x[r].stream_at(p.dx, at(r), off);
+      g[r].stream_at(p.dg, at(r), off);
     }
     return;
   }

@@ -58,43 +58,85 @@ __device__ __forceinline__ void row_sums(float* v, float (*buf)[K], int half) {
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float s = b[0][k];
-#pragma unroll
-      for (int w = 1; w < W; ++w) s += b[w][k];
+    for (int k = 0; k < K; ++k) {   // a wave's sum in every lane, added up over 4, 8 or 16 lanes
+      float s = b[threadIdx.x % W][k];
+      s = dpp_add<0x1B>(dpp_add<0xB1>(s));
+      if constexpr (W >= 8) s = dpp_add<0x141>(s);
+      if constexpr (W == 16) s = dpp_add<0x140>(s);
       v[k] = s;
     }
   }
 }
 
-// c elements (at most VEC) from element i on, zeros behind them; any alignment
-template <int DT, int VEC>
+// c elements (0 <= c <= VEC) from element i on, zeros behind them, at any alignment: a vector,
+// or at most one load of 8, 4 and 2 bytes each (one element after the other, rows of 700 bf16
+// elements took 1.5 times as long). EXACT: rows are whole vectors, and c is VEC.
+template <bool EXACT, int DT, int VEC>
 __device__ __forceinline__ void load_part(Pack<DT, VEC>& q, const void* p, size_t i, int c) {
-  if (c >= VEC) {
-    __builtin_memcpy(&q.r, static_cast<const uint8_t*>(p) + i * elem_size(DT), sizeof(q.r));
-  } else {
-    float f[VEC] = {};
+  const uint8_t* a = static_cast<const uint8_t*>(p) + i * elem_size(DT);
+  if (EXACT || c >= VEC) {
+    __builtin_memcpy(&q.r, a, 16);
+    return;
+  }
+  if constexpr (DT == FP32) {
+    q.r = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < VEC - 1; ++e)
-      if (e < c) load_f32<DT, 1>(p, i + e, f + e);
-    q.pack(f);
+      if (e < c) q.r[e] = reinterpret_cast<const uint32_t*>(a)[e];
+    return;
+  }
+  // each piece goes straight to its registers: merging them here would wait for every row's
+  // pieces before the next row's loads are issued
+  auto w4 = [](const uint8_t* b) { uint32_t v; __builtin_memcpy(&v, b, 4); return v; };
+  auto w2 = [](const uint8_t* b) { return (uint32_t)*reinterpret_cast<const uint16_t*>(b); };
+  const int bytes = c * elem_size(DT);
+  q.r = u32x4{0u, 0u, 0u, 0u};
+  if (bytes & 8) {
+    u32x2 v;
+    __builtin_memcpy(&v, a, 8);
+    q.r.x = v.x;
+    q.r.y = v.y;
+    if (bytes & 4) {
+      q.r.z = w4(a + 8);
+      if (bytes & 2) q.r.w = w2(a + 12);
+    } else if (bytes & 2) {
+      q.r.z = w2(a + 8);
+    }
+  } else if (bytes & 4) {
+    q.r.x = w4(a);
+    if (bytes & 2) q.r.y = w2(a + 4);
+  } else if (bytes & 2) {
+    q.r.x = w2(a);
   }
 }
-template <int DT, int VEC>
+template <bool EXACT, int DT, int VEC>
 __device__ __forceinline__ void store_part(const Pack<DT, VEC>& q, void* p, size_t i, int c) {
-  if (c >= VEC) {
-    __builtin_memcpy(static_cast<uint8_t*>(p) + i * elem_size(DT), &q.r, sizeof(q.r));
-  } else {
-    float f[VEC];
-    q.unpack(f);
+  uint8_t* a = static_cast<uint8_t*>(p) + i * elem_size(DT);
+  if (EXACT || c >= VEC) {
+    using Any = u32x4 __attribute__((aligned(2)));   // any alignment
+    __builtin_nontemporal_store(q.r, reinterpret_cast<Any*>(a));
+    return;
+  }
+  if constexpr (DT == FP32) {
 #pragma unroll
     for (int e = 0; e < VEC - 1; ++e)
-      if (e < c) store_f32<DT, 1>(p, i + e, f + e);
+      if (e < c) reinterpret_cast<uint32_t*>(a)[e] = q.r[e];
+    return;
   }
+  const int bytes = c * elem_size(DT);
+  const u32x2 head = {q.r.x, q.r.y}, rest = bytes & 8 ? u32x2{q.r.z, q.r.w} : head;
+  if (bytes & 8) __builtin_memcpy(a, &head, 8);
+  a += bytes & 8;
+  if (bytes & 4) __builtin_memcpy(a, &rest, 4);
+  if (bytes & 2) *reinterpret_cast<uint16_t*>(a + (bytes & 4)) = (uint16_t)(bytes & 4 ? rest.y : rest.x);
 }
-// c fp32 parameters of columns i on, or a constant
+// c fp32 parameters of columns i on (i a multiple of VEC), or a constant
 template <int VEC>
 __device__ __forceinline__ void load_param(const float* p, int i, int c, float none, float* f) {
+  if (p && c >= VEC) {
+    load_f32<FP32, VEC>(p, i, f);
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < VEC; ++e) f[e] = e < c ? (p ? p[i + e] : none) : 0.0f;
 }
@@ -106,7 +148,7 @@ constexpr int wg_of(int lanes) { return lanes > 256 ? lanes : 256; }
 // ---- forward ----------------------------------------------------------------------
 
 // A lane holds NV vectors of a row, U rows at a time.
-template <int DT, int LANES, int NV, int U>
+template <int DT, bool EXACT, int LANES, int NV, int U>
 __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormParams p) {
   constexpr int VEC = vec_of<DT>(), G = wg_of(LANES) / LANES;
   __shared__ float buf[LANES > 64 ? 2 * LANES / 64 : 1][U];
@@ -130,7 +172,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormPar
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         x[u][i].clear();
-        if (m < p.M && c[i] > 0) load_part(x[u][i], p.x, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+        if (m < p.M && c[i] > 0) load_part<EXACT>(x[u][i], p.x, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
       }
     }
 #pragma unroll
@@ -155,7 +197,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormPar
         x[u][i].unpack(f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float d = e < c[i] ? f[e] - s[u] : 0.0f;
+          const float d = (EXACT ? c[i] > 0 : e < c[i]) ? f[e] - s[u] : 0.0f;
           q[u] = fmaf(d, d, q[u]);
         }
       }
@@ -178,7 +220,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormPar
         for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[i][e], b[i][e]);
         Pack<DT, VEC> y;
         y.pack(f);
-        if (c[i] > 0) store_part(y, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+        if (c[i] > 0) store_part<EXACT>(y, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
       }
     }
   }
@@ -197,7 +239,7 @@ __global__ __launch_bounds__(1024) void kda_layernorm_fwd_long_kernel(NormParams
       for (int64_t col = (int64_t)threadIdx.x * VEC; col < p.D; col += 1024 * VEC) {
         const int c = p.D - col < VEC ? (int)(p.D - col) : VEC;
         Pack<DT, VEC> x;
-        load_part(x, p.x, row + col, c);
+        load_part<false>(x, p.x, row + col, c);
         float v[VEC];
         x.unpack(v);
         f((int)col, c, v);
@@ -228,7 +270,7 @@ __global__ __launch_bounds__(1024) void kda_layernorm_fwd_long_kernel(NormParams
       for (int e = 0; e < VEC; ++e) w[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
       Pack<DT, VEC> y;
       y.pack(w);
-      store_part(y, p.out, row + col, c);
+      store_part<false>(y, p.out, row + col, c);
     });
   }
 }
@@ -252,7 +294,7 @@ __device__ __forceinline__ float groups_sum(float v, float* buf) {
   return v;
 }
 
-template <int DT, int LANES, int NV, int U>
+template <int DT, bool EXACT, int LANES, int NV, int U>
 __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_bwd_kernel(NormParams p, int parts) {
   constexpr int VEC = vec_of<DT>(), G = wg_of(LANES) / LANES;
   __shared__ float buf[LANES > 64 ? 2 * LANES / 64 : 1][2 * U];
@@ -287,8 +329,8 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_bwd_kernel(NormPar
         dy[u][i].clear();
         if (m < p.M && c[i] > 0) {
           const size_t at = (size_t)m * p.D + (i * LANES + lane) * VEC;
-          load_part(x[u][i], p.x, at, c[i]);
-          load_part(dy[u][i], p.dy, at, c[i]);
+          load_part<EXACT>(x[u][i], p.x, at, c[i]);
+          load_part<EXACT>(dy[u][i], p.dy, at, c[i]);
         }
       }
     }
@@ -332,7 +374,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_bwd_kernel(NormPar
         }
         Pack<DT, VEC> dx;
         dx.pack(df);
-        if (c[i] > 0) store_part(dx, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+        if (c[i] > 0) store_part<EXACT>(dx, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
       }
     }
   }
@@ -368,8 +410,8 @@ __global__ __launch_bounds__(1024) void kda_layernorm_bwd_long_kernel(NormParams
       for (int64_t col = (int64_t)threadIdx.x * VEC; col < p.D; col += 1024 * VEC) {
         const int c = p.D - col < VEC ? (int)(p.D - col) : VEC;
         Pack<DT, VEC> x, dy;
-        load_part(x, p.x, row + col, c);
-        load_part(dy, p.dy, row + col, c);
+        load_part<false>(x, p.x, row + col, c);
+        load_part<false>(dy, p.dy, row + col, c);
         float xf[VEC], df[VEC], w[VEC];
         x.unpack(xf);
         dy.unpack(df);
@@ -397,7 +439,7 @@ __global__ __launch_bounds__(1024) void kda_layernorm_bwd_long_kernel(NormParams
       for (int e = 0; e < VEC; ++e) a[e] = rstd * (a[e] - c1 - xh[e] * c2);
       Pack<DT, VEC> dx;
       dx.pack(a);
-      store_part(dx, p.out, row + col, c);
+      store_part<false>(dx, p.out, row + col, c);
     });
   }
 }
@@ -415,8 +457,8 @@ __global__ __launch_bounds__(64) void kda_layernorm_cols_kernel(NormParams p, in
   for (int64_t m = part; m < p.M; m += parts) {
     const float mean = p.mean[m], rstd = p.rstd[m];
     Pack<DT, VEC> x, dy;
-    load_part(x, p.x, (size_t)m * p.D + col, c);
-    load_part(dy, p.dy, (size_t)m * p.D + col, c);
+    load_part<false>(x, p.x, (size_t)m * p.D + col, c);
+    load_part<false>(dy, p.dy, (size_t)m * p.D + col, c);
     float xf[VEC], df[VEC];
     x.unpack(xf);
     dy.unpack(df);
@@ -458,31 +500,39 @@ __global__ __launch_bounds__(1024) void kda_layernorm_sum_kernel(NormParams p, i
 }
 
 using std::integral_constant;
-template <int L, int V, int U>
+template <bool E, int L, int V, int U>
 struct Shape {
+  static constexpr bool exact = E;
   static constexpr int lanes = L, nv = V, rows = U;
 };
 
-// f(element type, shape) for the fewest lanes and vectors that hold a row; false: none does
-template <int DT, typename F>
-bool by_width(int32_t D, F f) {
-  constexpr int V = vec_of<DT>();
-  if (D <= 8 * V) f(Shape<8, 1, 4>{});
-  else if (D <= 16 * V) f(Shape<16, 1, 4>{});
-  else if (D <= 32 * V) f(Shape<16, 2, 2>{});
-  else if (D <= 64 * V) f(Shape<16, 4, 1>{});
-  else if (D <= 128 * V) f(Shape<64, 2, 2>{});
-  else if (D <= 256 * V) f(Shape<64, 4, 1>{});
-  else if (D <= 512 * V) f(Shape<256, 2, 2>{});
-  else if (D <= 1024 * V) f(Shape<256, 4, 1>{});
-  else if (D <= 2048 * V) f(Shape<1024, 2, 1>{});
+// f(shape) for the fewest lanes, and vectors of a lane, that hold a row; false: none does. Few
+// vectors leave registers for more rows at once (8192 bf16 backward: 108 us with 256 lanes of
+// 4 vectors, a row at a time; 93 with 1024 lanes, 4 rows). Rows that are not whole vectors take
+// more registers, so fewer at once.
+template <int DT, bool BWD, bool E, typename F>
+bool by_width_of(int32_t D, F f) {
+  constexpr int V = vec_of<DT>(), MANY = E || !BWD || V == 4 ? 4 : 2;
+  if (D <= 8 * V) f(Shape<E, 8, 1, MANY>{});
+  else if (D <= 16 * V) f(Shape<E, 16, 1, MANY>{});
+  else if (D <= 32 * V) f(Shape<E, 16, 2, 2>{});
+  else if (D <= 64 * V) f(Shape<E, 64, 1, MANY>{});
+  else if (D <= 128 * V) f(Shape<E, 64, 2, 2>{});
+  else if (D <= 256 * V) f(Shape<E, 256, 1, MANY>{});
+  else if (D <= 512 * V) f(Shape<E, 256, 2, 2>{});
+  else if (D <= 1024 * V) f(Shape<E, BWD ? 1024 : 512, BWD ? 1 : 2, BWD ? MANY : 2>{});
+  else if (D <= 2048 * V) f(Shape<E, 1024, 2, BWD ? 1 : 2>{});
   else if constexpr (V == 4) {
-    if (D <= 4096 * V) f(Shape<1024, 4, 1>{});
+    if (D <= 4096 * V) f(Shape<E, 1024, 4, 1>{});
     else return false;
   } else {
     return false;
   }
   return true;
+}
+template <int DT, bool BWD, typename F>
+bool by_width(int32_t D, F f) {
+  return D % vec_of<DT>() == 0 ? by_width_of<DT, BWD, true>(D, f) : by_width_of<DT, BWD, false>(D, f);
 }
 
 template <typename F>
@@ -499,7 +549,7 @@ unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : mos
 // Workgroups of a backward pass, at most: their sums take two rows of D each in the workspace,
 // so wide rows get one workgroup per compute unit and short ones enough to fill the GPU.
 size_t layernorm_parts(int64_t M, int64_t D) {
-  const int64_t most = D <= 2048 ? 1024 : D <= 8192 ? 512 : 256;
+  const int64_t most = D <= 1024 ? 1024 : D <= 2048 ? 768 : D <= 4096 ? 512 : 256;
   return (size_t)(M < most ? M : most);
 }
 
@@ -507,10 +557,10 @@ hipError_t launch_layernorm_fwd(const NormParams& p, hipStream_t stream) {
   if (p.M == 0) return hipSuccess;
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    const bool done = by_width<DT>(p.D, [&](auto shape) {
+    const bool done = by_width<DT, false>(p.D, [&](auto shape) {
       using S = decltype(shape);
       constexpr int wg = wg_of(S::lanes), step = wg / S::lanes * S::rows;
-      hipLaunchKernelGGL((kda_layernorm_fwd_kernel<DT, S::lanes, S::nv, S::rows>),
+      hipLaunchKernelGGL((kda_layernorm_fwd_kernel<DT, S::exact, S::lanes, S::nv, S::rows>),
                          dim3(at_most((p.M + step - 1) / step, 2048 * 256 / wg)), dim3(wg), 0, stream, p);
     });
     if (!done)
@@ -524,11 +574,11 @@ hipError_t launch_layernorm_bwd(const NormParams& p, hipStream_t stream) {
   if (p.M > 0) {
     by_dtype(p.dtype, [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
-      const bool done = by_width<DT>(p.D, [&](auto shape) {
+      const bool done = by_width<DT, true>(p.D, [&](auto shape) {
         using S = decltype(shape);
         constexpr int wg = wg_of(S::lanes), step = wg / S::lanes * S::rows;
-        parts = (int)at_most((p.M + step - 1) / step, parts);
-        hipLaunchKernelGGL((kda_layernorm_bwd_kernel<DT, S::lanes, S::nv, S::rows>), dim3(parts), dim3(wg), 0, stream, p, parts);
+        parts = (int)at_most((p.M + step - 1) / step, parts < 256 * 1024 / wg ? parts : 256 * 1024 / wg);
+        hipLaunchKernelGGL((kda_layernorm_bwd_kernel<DT, S::exact, S::lanes, S::nv, S::rows>), dim3(parts), dim3(wg), 0, stream, p, parts);
       });
       if (!done) {
         if (p.partial) {
