@@ -14,13 +14,16 @@
 // continuing it: A = RESET (-1; an exp is never negative) marks a map that does not depend on
 // the state before, which is then not multiplied by zero but left out (it may be NaN).
 //
-// Between tiles: per tile and channel a word for (A, L) and one for the state that leaves the
-// tile, both EMPTY (all ones) until published; a value that is NaN is stored as one NaN whose
-// bits are not EMPTY. A tile waits until one of the WINDOW tiles before it has published its
-// state and all between that one and itself their maps, and applies those in the tokens'
-// order. Every published state is (A, L) applied to the state before, whoever computes it, so
-// the bits do not depend on how far a tile looked back. Words are single relaxed atomics of
-// device scope: no fences, no flags beside the data.
+// Between tiles: every tile publishes its map; the last of BLOCK tiles also their composition,
+// the block's map, and the state that leaves the block. A tile takes the maps of the tiles
+// before it in its block, and the state that enters the block: as published, or, looking back
+// over up to WINDOW blocks, from an earlier block's state and the maps of the blocks between.
+// (Passing a state from tile to tile over 7 of them at once, 32768 tokens of 256 channels took
+// 47 us: many tiles in flight and little data.) A block's state is always its map applied to the
+// state before it, and a tile's its block's map so far applied to that, whoever computes it, so
+// the bits do not depend on how far a tile looked back. Each word is EMPTY (all ones) until it
+// is published, as a single relaxed atomic of device scope: no fences, no flags beside the data;
+// a NaN is stored as one whose bits are not EMPTY.
 //
 // Every wait ends: a workgroup takes its tile's number from a counter of its channels when it
 // starts, so all tiles that it waits for belong to workgroups that have started before it and
@@ -35,7 +38,8 @@ namespace {
 
 constexpr float RESET = -1.0f;
 constexpr uint32_t EMPTY = 0xffffffffu;
-constexpr int WINDOW = 8;
+constexpr int BLOCK = 8;    // tiles of a block
+constexpr int WINDOW = 6;   // blocks looked back over at once
 constexpr int TICK_STRIDE = 16;   // a counter per 64 bytes
 
 template <int DT, int VEC>
@@ -66,58 +70,87 @@ __device__ __forceinline__ T observe(const T* p) {
 }
 
 struct TileWs {
-  uint64_t* maps;     // [tiles][D] (L, A) of each tile, by the order of processing
-  uint32_t* states;   // [tiles][D] state leaving each tile
-  uint32_t* ticks;    // [channel tiles * TICK_STRIDE]
-  float* stage;       // [nseq][D] initial states, where final_state overwrites them
+  uint64_t* maps;           // [tiles][D] (L, A) of each tile, by the order of processing
+  uint64_t* block_maps;     // [blocks][D] of each whole block of BLOCK tiles
+  uint32_t* block_states;   // [blocks][D] state entering each block
+  uint32_t* ticks;          // [channel tiles * TICK_STRIDE]
+  float* stage;             // [nseq][D] initial states, where final_state overwrites them
   int32_t tiles, cols;
 };
 
-// Publishes the tile's map, waits for the state that enters it and publishes the one that
-// leaves it; k: the tile's place in the order of processing, c0 + ch: the lane's channel.
-// (Addresses are a uniform base and a 32-bit lane offset each: one register, not two.)
+__device__ __forceinline__ float map_A(uint64_t m) { return __uint_as_float((uint32_t)m); }
+__device__ __forceinline__ float map_L(uint64_t m) { return __uint_as_float((uint32_t)(m >> 32)); }
+__device__ __forceinline__ uint64_t map_word(float A, float L) { return ((uint64_t)word_of(L) << 32) | __float_as_uint(A); }
+
+// 32-bit words of all maps and states
+__host__ __device__ inline int64_t glr_words(int64_t tiles, int64_t D) {
+  return (2 * tiles + 3 * ((tiles + BLOCK - 1) / BLOCK)) * D;
+}
+
+// Publishes the tile's map, waits for the state that enters it, and, for the last tile of a
+// block, publishes the block's map and the state that leaves it; k: the tile's place in the
+// order of processing, c0 + ch: the lane's channel. Addresses are formed anew at every poll (t
+// is opaque): kept over the loops they cost 30 registers.
 __device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, int c0, uint32_t ch, float A, float L) {
-  auto map_at = [&](int i) { return w.maps + ((size_t)i * D + c0) + ch; };
-  auto state_at = [&](int i) { return w.states + ((size_t)i * D + c0) + ch; };
-  const bool more = k + 1 < w.tiles;
-  if (more) publish(map_at(k), ((uint64_t)word_of(L) << 32) | __float_as_uint(A));
-  if (more && (A < 0.0f || k == 0)) publish(state_at(k), word_of(apply(A, L, 0.0f)));
-  float h = 0.0f;
-  for (bool found = k == 0; !found;) {
-    int t = k;
-    asm volatile("" : "+s"(t));   // addresses are formed anew: kept over the loop they cost 30 registers
-    const uint32_t s0 = observe(state_at(t - 1));
-    if (s0 != EMPTY) {
-      h = __uint_as_float(s0);
-      break;
-    }
-    uint32_t s[WINDOW];   // s[i]: the state that enters tile t - i (zero for the first); m[i]: that tile's map
-    uint64_t m[WINDOW];
+  auto row = [&](int i) { return (size_t)i * D + c0; };
+  const int b = k / BLOCK, j = k % BLOCK;
+  const bool more = k + 1 < w.tiles, closes = more && j == BLOCK - 1;
+  if (more && !closes) publish(w.maps + row(k) + ch, map_word(A, L));
+  uint64_t m[BLOCK - 1];   // maps of the block's tiles before this one
 #pragma unroll
-    for (int i = 1; i < WINDOW; ++i) {
-      m[i] = t - i >= 0 ? observe(map_at(t - i)) : ~0ull;
-      s[i] = t - i > 0 ? observe(state_at(t - i - 1)) : t == i ? 0u : EMPTY;
+  for (int i = 0; i < BLOCK - 1; ++i) m[i] = 0;
+  for (bool whole = j == 0; !whole;) {
+    int t = b * BLOCK;
+    asm volatile("" : "+s"(t));
+#pragma unroll
+    for (int i = 0; i < BLOCK - 1; ++i)
+      if (i < j) m[i] = observe(w.maps + row(t + i) + ch);
+    whole = true;
+#pragma unroll
+    for (int i = 0; i < BLOCK - 1; ++i) whole = whole && m[i] != ~0ull;
+    if (!whole) __builtin_amdgcn_s_sleep(1);
+  }
+  float BA = 1.0f, BL = 0.0f;   // the block's map up to this tile
+#pragma unroll
+  for (int i = 0; i < BLOCK - 1; ++i)
+    if (i < j) compose(BA, BL, map_A(m[i]), map_L(m[i]));
+  float CA = BA, CL = BL;       // and through it
+  compose(CA, CL, A, L);
+  if (closes) {
+    publish(w.block_maps + row(b) + ch, map_word(CA, CL));
+    if (CA < 0.0f || b == 0) publish(w.block_states + row(b + 1) + ch, word_of(apply(CA, CL, 0.0f)));
+  }
+  float S = 0.0f;   // the state that enters the block: not needed where a sequence begins in it before this tile
+  for (bool found = b == 0 || BA < 0.0f; !found;) {
+    int t = b;
+    asm volatile("" : "+s"(t));
+    uint32_t s[WINDOW];   // s[i]: the state that enters block b - i (zero for the first); n[i]: that block's map
+    uint64_t n[WINDOW];
+#pragma unroll
+    for (int i = 0; i < WINDOW; ++i) {
+      s[i] = t - i > 0 ? observe(w.block_states + row(t - i) + ch) : t == i ? 0u : EMPTY;
+      n[i] = i > 0 && t - i >= 0 ? observe(w.block_maps + row(t - i) + ch) : ~0ull;
     }
-    int at = 0;   // the nearest published state with all maps after it: i = at
+    int at = -1;   // the nearest published state with all maps after it: i = at
     bool whole = true;
 #pragma unroll
-    for (int i = 1; i < WINDOW; ++i) {
-      whole = whole && m[i] != ~0ull;
-      if (whole && at == 0 && s[i] != EMPTY) at = i;
+    for (int i = 0; i < WINDOW; ++i) {
+      whole = whole && (i == 0 || n[i] != ~0ull);
+      if (whole && at < 0 && s[i] != EMPTY) at = i;
     }
-    if (at > 0) {
+    if (at >= 0) {
 #pragma unroll
-      for (int i = WINDOW - 1; i >= 1; --i) {
-        if (i == at) h = __uint_as_float(s[i]);
-        if (i <= at) h = apply(__uint_as_float((uint32_t)m[i]), __uint_as_float((uint32_t)(m[i] >> 32)), h);
+      for (int i = WINDOW - 1; i >= 0; --i) {
+        if (i == at) S = __uint_as_float(s[i]);
+        if (i > 0 && i <= at) S = apply(map_A(n[i]), map_L(n[i]), S);
       }
       found = true;
     } else {
-      __builtin_amdgcn_s_sleep(2);
+      __builtin_amdgcn_s_sleep(1);
     }
   }
-  if (more && !(A < 0.0f) && k != 0) publish(state_at(k), word_of(apply(A, L, h)));
-  return h;
+  if (closes && !(CA < 0.0f) && b > 0) publish(w.block_states + row(b + 1) + ch, word_of(apply(CA, CL, S)));
+  return j == 0 ? S : apply(BA, BL, S);
 }
 
 // ---- which sequence a token belongs to -------------------------------------------
@@ -184,9 +217,9 @@ __device__ __forceinline__ void find_places(const GlrParams& p, const int64_t* c
 
 __global__ __launch_bounds__(256) void kda_glr_prep_kernel(GlrParams p, TileWs w, const void* from, int from_dtype) {
   const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  const int64_t words = (int64_t)w.tiles * p.D;   // maps and states lie one after the other
+  const int64_t words = glr_words(w.tiles, p.D);   // maps and states lie one after the other
   const u32x4 ones = {EMPTY, EMPTY, EMPTY, EMPTY};
-  for (int64_t i = i0; i < (3 * words + 3) / 4; i += step) reinterpret_cast<u32x4*>(w.maps)[i] = ones;
+  for (int64_t i = i0; i < (words + 3) / 4; i += step) reinterpret_cast<u32x4*>(w.maps)[i] = ones;
   for (int64_t i = i0; i < (int64_t)w.cols * TICK_STRIDE; i += step) w.ticks[i] = 0;
   if (!w.stage && !p.cu && p.T > 0) return;
   for (int64_t i = i0; i < (int64_t)p.nseq * p.D; i += step) {
@@ -624,16 +657,18 @@ TileWs tile_ws(const GlrParams& p, void* workspace, bool stage) {
   uint8_t* b = static_cast<uint8_t*>(workspace);
   w.tiles = tile_count(p.tokens);
   w.cols = tile_cols(p.dtype, p.D);
-  const size_t words = (size_t)w.tiles * p.D;
+  const size_t words = (size_t)glr_words(w.tiles, p.D), blocks = (size_t)((w.tiles + BLOCK - 1) / BLOCK);
   w.maps = reinterpret_cast<uint64_t*>(b);
-  w.states = reinterpret_cast<uint32_t*>(b + words * 8);
-  w.ticks = reinterpret_cast<uint32_t*>(b + up256(words * 12 + 16));
-  if (stage) w.stage = reinterpret_cast<float*>(b + up256(words * 12 + 16) + up256((size_t)((p.D + 63) / 64) * TICK_STRIDE * 4));
+  w.block_maps = w.maps + (size_t)w.tiles * p.D;
+  w.block_states = reinterpret_cast<uint32_t*>(w.block_maps + blocks * p.D);
+  const size_t ticks = up256(words * 4 + 16);   // (the fill writes whole vectors)
+  w.ticks = reinterpret_cast<uint32_t*>(b + ticks);
+  if (stage) w.stage = reinterpret_cast<float*>(b + ticks + up256((size_t)((p.D + 63) / 64) * TICK_STRIDE * 4));
   return w;
 }
 
 hipError_t launch_prep(const GlrParams& p, const TileWs& w, const void* from, int from_dtype, hipStream_t stream) {
-  const int64_t fill = (3 * (int64_t)w.tiles * p.D + 3) / 4, rows = w.stage || p.cu || p.T == 0 ? (int64_t)p.nseq * p.D : 0;
+  const int64_t fill = (glr_words(w.tiles, p.D) + 3) / 4, rows = w.stage || p.cu || p.T == 0 ? (int64_t)p.nseq * p.D : 0;
   const int64_t blocks = ((fill > rows ? fill : rows) + 255) / 256;
   hipLaunchKernelGGL(kda_glr_prep_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream, p, w, from,
                      from_dtype);
@@ -647,8 +682,7 @@ bool few_tokens(const GlrParams& p) { return p.cu ? p.T <= 2 * (int64_t)p.nseq :
 }  // namespace
 
 size_t glr_workspace(int64_t tokens, int64_t D, int64_t nseq) {
-  const size_t words = (size_t)tile_count(tokens) * (size_t)D;
-  return up256(words * 12 + 16) + up256((size_t)((D + 63) / 64) * TICK_STRIDE * 4) + up256((size_t)nseq * D * 4);
+  return up256((size_t)glr_words(tile_count(tokens), D) * 4 + 16) + up256((size_t)((D + 63) / 64) * TICK_STRIDE * 4) + up256((size_t)nseq * D * 4);
 }
 
 bool glr_fits(int64_t tokens, int64_t D, int64_t nseq) {
