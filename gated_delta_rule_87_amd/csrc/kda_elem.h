@@ -142,6 +142,76 @@ __device__ __forceinline__ void store_f32(void* p, size_t i, const float* f) {
   }
 }
 
+// c elements (0 <= c <= VEC) from element i on, or from byte a on, zeros behind them, at any
+// alignment (the hardware splits what crosses a line): a vector,
+// or at most one load of 8, 4 and 2 bytes each (one element after the other, rows of 700 bf16
+// elements took 1.5 times as long). EXACT: rows are whole vectors, and c is VEC.
+template <bool EXACT, int DT, int VEC>
+__device__ __forceinline__ void load_part(Pack<DT, VEC>& q, const uint8_t* a, int c) {
+  if (EXACT || c >= VEC) {
+    __builtin_memcpy(&q.r, a, 16);
+    return;
+  }
+  if constexpr (DT == FP32) {
+    q.r = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < VEC - 1; ++e)
+      if (e < c) q.r[e] = reinterpret_cast<const uint32_t*>(a)[e];
+    return;
+  }
+  // each piece goes straight to its registers: merging them here would wait for every row's
+  // pieces before the next row's loads are issued
+  auto w4 = [](const uint8_t* b) { uint32_t v; __builtin_memcpy(&v, b, 4); return v; };
+  auto w2 = [](const uint8_t* b) { return (uint32_t)*reinterpret_cast<const uint16_t*>(b); };
+  const int bytes = c * elem_size(DT);
+  q.r = u32x4{0u, 0u, 0u, 0u};
+  if (bytes & 8) {
+    u32x2 v;
+    __builtin_memcpy(&v, a, 8);
+    q.r.x = v.x;
+    q.r.y = v.y;
+    if (bytes & 4) {
+      q.r.z = w4(a + 8);
+      if (bytes & 2) q.r.w = w2(a + 12);
+    } else if (bytes & 2) {
+      q.r.z = w2(a + 8);
+    }
+  } else if (bytes & 4) {
+    q.r.x = w4(a);
+    if (bytes & 2) q.r.y = w2(a + 4);
+  } else if (bytes & 2) {
+    q.r.x = w2(a);
+  }
+}
+template <bool EXACT, int DT, int VEC>
+__device__ __forceinline__ void store_part(const Pack<DT, VEC>& q, uint8_t* a, int c) {
+  if (EXACT || c >= VEC) {
+    using Any = u32x4 __attribute__((aligned(2)));   // any alignment
+    __builtin_nontemporal_store(q.r, reinterpret_cast<Any*>(a));
+    return;
+  }
+  if constexpr (DT == FP32) {
+#pragma unroll
+    for (int e = 0; e < VEC - 1; ++e)
+      if (e < c) reinterpret_cast<uint32_t*>(a)[e] = q.r[e];
+    return;
+  }
+  const int bytes = c * elem_size(DT);
+  const u32x2 head = {q.r.x, q.r.y}, rest = bytes & 8 ? u32x2{q.r.z, q.r.w} : head;
+  if (bytes & 8) __builtin_memcpy(a, &head, 8);
+  a += bytes & 8;
+  if (bytes & 4) __builtin_memcpy(a, &rest, 4);
+  if (bytes & 2) *reinterpret_cast<uint16_t*>(a + (bytes & 4)) = (uint16_t)(bytes & 4 ? rest.y : rest.x);
+}
+template <bool EXACT, int DT, int VEC>
+__device__ __forceinline__ void load_part(Pack<DT, VEC>& q, const void* p, size_t i, int c) {
+  load_part<EXACT>(q, static_cast<const uint8_t*>(p) + i * elem_size(DT), c);
+}
+template <bool EXACT, int DT, int VEC>
+__device__ __forceinline__ void store_part(const Pack<DT, VEC>& q, void* p, size_t i, int c) {
+  store_part<EXACT>(q, static_cast<uint8_t*>(p) + i * elem_size(DT), c);
+}
+
 // N elements of a state of dtype code sdt (0: zeros, BF16, FP32); the same branch in every lane
 template <int N>
 __device__ __forceinline__ void load_state(const void* p, int sdt, size_t i, float* f) {
@@ -156,6 +226,28 @@ template <int N>
 __device__ __forceinline__ void store_state(void* p, int sdt, size_t i, const float* f) {
   if (sdt == FP32) store_f32<FP32, N>(p, i, f);
   else if (sdt == BF16) store_f32<BF16, N>(p, i, f);
+}
+
+// the first c of them (EXACT: all; rows of another width are not aligned to vectors)
+template <bool EXACT, int N>
+__device__ __forceinline__ void load_state_part(const void* p, int sdt, size_t i, int c, float* f) {
+  if (EXACT) {
+    load_state<N>(p, sdt, i, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < c) load_state<1>(p, sdt, i + j, f + j);
+  }
+}
+template <bool EXACT, int N>
+__device__ __forceinline__ void store_state_part(void* p, int sdt, size_t i, int c, const float* f) {
+  if (EXACT) {
+    store_state<N>(p, sdt, i, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < c) store_state<1>(p, sdt, i + j, f + j);
+  }
 }
 
 }  // namespace kda

@@ -1,15 +1,16 @@
 // kda_glr.hip -- gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per channel, forward
 // and backward (gfx950).
 //
-// The B * T packed tokens are cut into tiles of GLR_TILE tokens by 256 bytes of channels (64
-// elements where D is no whole number of 16-byte vectors), one workgroup each. A tile acts on
+// The B * T packed tokens are cut into tiles of GLR_TILE tokens by 256 bytes of channels, one
+// workgroup each. A tile acts on
 // the state that enters it as an affine map h -> A h + L, with A = prod exp(g): the workgroup
 // loads its tile once into registers, reduces it to (A, L) per channel, publishes that,
 // obtains the state that enters it from the tiles before, and runs through its registers a
 // second time for the outputs. So every element is read once and written once, also for few
 // channels on long sequences, where one lane per channel would leave most of the GPU idle.
 //
-// Inside a tile, 256 / LR groups of lanes hold R consecutive tokens each; their maps are
+// Inside a tile, 16 groups of 16 lanes hold R = 8 consecutive tokens each, 16 bytes a lane and
+// token (rows that are no whole vectors: at any address, the last elements in smaller pieces); their maps are
 // composed through shared memory. A sequence's first token sets the state instead of
 // continuing it: A = RESET (-1; an exp is never negative) marks a map that does not depend on
 // the state before, which is then not multiplied by zero but left out (it may be NaN).
@@ -42,12 +43,13 @@ constexpr int BLOCK = 8;    // tiles of a block
 constexpr int WINDOW = 6;   // blocks looked back over at once
 constexpr int TICK_STRIDE = 16;   // a counter per 64 bytes
 
-template <int DT, int VEC>
+constexpr int LR = 16;             // lanes across a row
+constexpr int GRP = 256 / LR;      // groups of lanes along the tokens
+constexpr int R = GLR_TILE / GRP;  // tokens of a lane
+template <int DT>
 struct Geom {
-  static constexpr int LR = VEC > 1 ? 16 : 64;    // lanes across a row
-  static constexpr int CH = LR * VEC;             // channels of a tile
-  static constexpr int GRP = 256 / LR;            // groups of lanes along the tokens
-  static constexpr int R = GLR_TILE / GRP;        // tokens of a lane
+  static constexpr int VEC = 16 / elem_size(DT);   // elements of a lane
+  static constexpr int CH = LR * VEC;              // channels of a tile
 };
 
 __device__ __forceinline__ float decay(float g) { return fast_exp2(g * LOG2E); }
@@ -233,34 +235,33 @@ __global__ __launch_bounds__(256) void kda_glr_prep_kernel(GlrParams p, TileWs w
 
 // ---- forward -----------------------------------------------------------------------
 
-template <int DT, int VEC>
+template <int DT, bool EXACT>
 __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, const int64_t* __restrict__ cu, TileWs w) {
-  using G = Geom<DT, VEC>;
-  constexpr int R = G::R;
-  __shared__ float sA[G::GRP][G::CH], sL[G::GRP][G::CH];
+  constexpr int VEC = Geom<DT>::VEC, CH = Geom<DT>::CH;
+  __shared__ float sA[GRP][CH], sL[GRP][CH];
   __shared__ TilePlaces places;
   __shared__ int s_tile;
-  const int tid = threadIdx.x, lr = tid % G::LR, grp = tid / G::LR;
+  const int tid = threadIdx.x, lr = tid % LR, grp = tid / LR;
   const int col = blockIdx.x % w.cols;
   if (tid == 0)
     s_tile = (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   const int tile = __builtin_amdgcn_readfirstlane(s_tile);
   const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
-  const int d = col * G::CH + lr * VEC;
-  const bool d_ok = d < p.D;   // (a vector lies inside or outside: VEC divides D)
+  const int d = col * CH + lr * VEC;
+  const int c = p.D - d < 0 ? 0 : p.D - d > VEC ? VEC : p.D - d;   // elements of this lane (EXACT: VEC or none)
 
   // token r of a group: a uniform base and the lane's 32-bit offset (one register for all)
   const uint32_t off = ((uint32_t)(grp * R) * p.D + lr * VEC) * elem_size(DT);
-  auto at = [&](int r) { return ((size_t)(t_base + r) * p.D + col * G::CH) * elem_size(DT); };
+  auto at = [&](int r) { return ((size_t)(t_base + r) * p.D + col * CH) * elem_size(DT); };
   Pack<DT, VEC> g[R], x[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     g[r].clear();
     x[r].clear();
-    if (d_ok && t0 + r < p.tokens) {
-      g[r].load_at(p.g, at(r), off);
-      x[r].load_at(p.x, at(r), off);
+    if (c > 0 && t0 + r < p.tokens) {
+      load_part<EXACT>(g[r], static_cast<const uint8_t*>(p.g) + at(r) + off, c);
+      load_part<EXACT>(x[r], static_cast<const uint8_t*>(p.x) + at(r) + off, c);
     }
   }
   find_places(p, cu, t_base, places);
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
       x[r].unpack(xf);
       if (!PLAIN && (first >> r & 1)) {
         float h0[VEC] = {};
-        if (d_ok) load_state<VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, h0);
+        if (c > 0) load_state_part<EXACT, VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h0);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           L[v] = fmaf(decay(gf[v]), h0[v], xf[v]);
@@ -310,21 +311,21 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
     }
   }
   __syncthreads();
-  if (tid < G::CH && col * G::CH + tid < p.D) {   // a lane per channel
+  if (tid < CH && col * CH + tid < p.D) {   // a lane per channel
     float TA = 1.0f, TL = 0.0f;
 #pragma unroll 4
-    for (int i = 0; i < G::GRP; ++i) compose(TA, TL, sA[i][tid], sL[i][tid]);
-    float h = pass_state(w, tile, p.D, col * G::CH, tid, TA, TL);
-    if (p.carry) p.carry[(size_t)tile * p.D + col * G::CH + tid] = h;
+    for (int i = 0; i < GRP; ++i) compose(TA, TL, sA[i][tid], sL[i][tid]);
+    float h = pass_state(w, tile, p.D, col * CH, tid, TA, TL);
+    if (p.carry) p.carry[(size_t)tile * p.D + col * CH + tid] = h;
 #pragma unroll 4
-    for (int i = 0; i < G::GRP; ++i) {   // the state that enters each group
+    for (int i = 0; i < GRP; ++i) {   // the state that enters each group
       const float A = sA[i][tid], L = sL[i][tid];
       sL[i][tid] = h;
       h = apply(A, L, h);
     }
   }
   __syncthreads();
-  if (!d_ok) return;
+  if (c == 0) return;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     g[r].opaque();
@@ -339,13 +340,13 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
     float gf[VEC], xf[VEC];
     g[r].unpack(gf);
     x[r].unpack(xf);
-    if (first >> r & 1) load_state<VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, h);
+    if (first >> r & 1) load_state_part<EXACT, VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
     Pack<DT, VEC> y;
     y.pack(h);
-    y.stream_at(p.y, at(r), off);
-    if (last >> r & 1) store_state<VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, h);
+    store_part<EXACT>(y, static_cast<uint8_t*>(p.y) + at(r) + off, c);
+    if (last >> r & 1) store_state_part<EXACT, VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h);
   }
 }
 
@@ -359,36 +360,34 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
 // are worked on one after the other, their dx and dg written over x and g in the registers:
 // of the states before each token only R times two are held at once (all channels' would take
 // 64 more registers and a third of the waves).
-template <int DT, int VEC>
+template <int DT, bool EXACT>
 __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, const int64_t* __restrict__ cu, TileWs w) {
-  using G = Geom<DT, VEC>;
-  constexpr int R = G::R;
-  constexpr int NV = VEC > 1 && DT != FP32 ? 2 : 1;   // channels of a word
-  __shared__ float sA[G::GRP][G::CH], sL[G::GRP][G::CH], sB[G::GRP][G::CH], sM[G::GRP][G::CH];
+  constexpr int VEC = Geom<DT>::VEC, CH = Geom<DT>::CH;
+  constexpr int NV = 4 / elem_size(DT);   // channels of a word
+  __shared__ float sA[GRP][CH], sL[GRP][CH], sB[GRP][CH], sM[GRP][CH];
   __shared__ TilePlaces places;
   __shared__ int s_tile;
-  const int tid = threadIdx.x, lr = tid % G::LR, grp = tid / G::LR;
+  const int tid = threadIdx.x, lr = tid % LR, grp = tid / LR;
   const int col = blockIdx.x % w.cols;
   if (tid == 0)
     s_tile = (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   const int k = __builtin_amdgcn_readfirstlane(s_tile), tile = w.tiles - 1 - k;
   const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
-  const int d = col * G::CH + lr * VEC;
-  const bool d_ok = d < p.D;
-
+  const int d = col * CH + lr * VEC;
+  const int n_el = p.D - d < 0 ? 0 : p.D - d > VEC ? VEC : p.D - d;   // elements of this lane (EXACT: VEC or none)
   const uint32_t off = ((uint32_t)(grp * R) * p.D + lr * VEC) * elem_size(DT);
-  auto at = [&](int r) { return ((size_t)(t_base + r) * p.D + col * G::CH) * elem_size(DT); };
+  auto at = [&](int r) { return ((size_t)(t_base + r) * p.D + col * CH) * elem_size(DT); };
   Pack<DT, VEC> g[R], x[R], dy[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     g[r].clear();
     x[r].clear();
     dy[r].clear();
-    if (d_ok && t0 + r < p.tokens) {
-      g[r].load_at(p.g, at(r), off);
-      x[r].load_at(p.x, at(r), off);
-      dy[r].load_at(p.dy, at(r), off);
+    if (n_el > 0 && t0 + r < p.tokens) {
+      load_part<EXACT>(g[r], static_cast<const uint8_t*>(p.g) + at(r) + off, n_el);
+      load_part<EXACT>(x[r], static_cast<const uint8_t*>(p.x) + at(r) + off, n_el);
+      load_part<EXACT>(dy[r], static_cast<const uint8_t*>(p.dy) + at(r) + off, n_el);
     }
   }
   find_places(p, cu, t_base, places);
@@ -397,50 +396,62 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   const uint32_t all = (uint32_t)((1ull << R) - 1);
   const uint32_t in = (uint32_t)(places.in[word] >> bit) & all, first = (uint32_t)(places.first[word] >> bit) & all,
                  last = (uint32_t)(places.last[word] >> bit) & all;
-  const bool plain = in == all && first == 0 && last == 0;
+  // What a wave has to look out for among its lanes' runs of tokens: nothing (PLAIN), at most
+  // one first and one last token of a sequence in a run (ONE: chosen by selects), or MANY, also
+  // where tokens lie before or behind all sequences. (Rows behind the last token were not
+  // loaded: zeros, that is no decay, no input and no gradient.)
+  enum { PLAIN, ONE, MANY };
+  const int left = p.tokens - t0;
+  const bool whole = in == (left >= R ? all : left <= 0 ? 0u : all >> (R - left));
+  const int mode = __all(whole && first == 0 && last == 0) ? PLAIN
+                   : __all(whole && (first & (first - 1)) == 0 && (last & (last - 1)) == 0) ? ONE : MANY;
   auto row = [&](int r) { return (size_t)places.n[grp * R + r] * p.D + d; };
+  // a run's initial state and final gradient (ONE), elements c on
+  auto ends = [&](int c, float* h0, float* e0) {
+    int q = grp * R;
+    asm volatile("" : "+v"(q));   // not kept from word to word
+    if (first != 0 && n_el > c)
+      load_state_part<EXACT, NV>(p.init, p.init_dtype, (size_t)places.n[q + __builtin_ctz(first)] * p.D + d + c, n_el - c, h0);
+    if (last != 0 && n_el > c)
+      load_state_part<EXACT, NV>(p.dfin, p.dfin_dtype, (size_t)places.n[q + __builtin_ctz(last)] * p.D + d + c, n_el - c, e0);
+  };
 
-  auto reduce = [&](auto plain_c) {
-    constexpr bool PLAIN = decltype(plain_c)::value;
+  auto reduce = [&](auto mode_c) {
+    constexpr int MODE = decltype(mode_c)::value;
 #pragma unroll
     for (int c = 0; c < VEC; c += NV) {
       __builtin_amdgcn_sched_barrier(0);   // one word after the other
-      float a[R][NV], A[NV], L[NV], B[NV], M[NV];
+      float a[R][NV], A[NV], L[NV], B[NV], M[NV], h0[NV], e0[NV];
 #pragma unroll
-      for (int v = 0; v < NV; ++v) A[v] = B[v] = 1.0f, L[v] = M[v] = 0.0f;
+      for (int v = 0; v < NV; ++v) {
+        A[v] = B[v] = 1.0f;
+        L[v] = M[v] = h0[v] = e0[v] = 0.0f;
+      }
+      if (MODE == ONE) ends(c, h0, e0);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float xf[NV];
         unpack_word<DT, VEC, NV>(g[r], c, a[r]);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) a[r][v] = decay(a[r][v]);
-        if (!PLAIN && !(in >> r & 1)) continue;
         unpack_word<DT, VEC, NV>(x[r], c, xf);
-        if (!PLAIN && (first >> r & 1)) {
-          if (d_ok) load_state<NV>(p.init, p.init_dtype, row(r) + c, L);
-#pragma unroll
-          for (int v = 0; v < NV; ++v) A[v] = RESET;
-        }
+        const bool start = MODE != PLAIN && (first >> r & 1), used = MODE != MANY || (in >> r & 1);
+        if (MODE == MANY && start && n_el > c) load_state_part<EXACT, NV>(p.init, p.init_dtype, row(r) + c, n_el - c, h0);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          L[v] = fmaf(a[r][v], L[v], xf[v]);
-          A[v] = PLAIN ? A[v] * a[r][v] : (A[v] < 0.0f ? RESET : A[v] * a[r][v]);
+          a[r][v] = used ? decay(a[r][v]) : 1.0f;   // a token of no sequence: no decay, no input, no gradient
+          L[v] = fmaf(a[r][v], start ? h0[v] : L[v], used ? xf[v] : 0.0f);
+          A[v] = start || (MODE != PLAIN && A[v] < 0.0f) ? RESET : A[v] * a[r][v];
         }
       }
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
-        if (!PLAIN && !(in >> r & 1)) continue;
         float df[NV];
         unpack_word<DT, VEC, NV>(dy[r], c, df);
-        if (!PLAIN && (last >> r & 1)) {
-          if (d_ok) load_state<NV>(p.dfin, p.dfin_dtype, row(r) + c, M);
-#pragma unroll
-          for (int v = 0; v < NV; ++v) B[v] = RESET;
-        }
+        const bool end = MODE != PLAIN && (last >> r & 1), used = MODE != MANY || (in >> r & 1);
+        if (MODE == MANY && end && n_el > c) load_state_part<EXACT, NV>(p.dfin, p.dfin_dtype, row(r) + c, n_el - c, e0);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          M[v] = a[r][v] * (df[v] + M[v]);
-          B[v] = PLAIN ? B[v] * a[r][v] : (B[v] < 0.0f ? RESET : B[v] * a[r][v]);
+          M[v] = a[r][v] * ((used ? df[v] : 0.0f) + (end ? e0[v] : M[v]));
+          B[v] = end || (MODE != PLAIN && B[v] < 0.0f) ? RESET : B[v] * a[r][v];
         }
       }
 #pragma unroll
@@ -453,31 +464,32 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
       }
     }
   };
-  if (__all(plain)) reduce(std::true_type{});
-  else reduce(std::false_type{});
+  if (mode == PLAIN) reduce(std::integral_constant<int, PLAIN>{});
+  else if (mode == ONE) reduce(std::integral_constant<int, ONE>{});
+  else reduce(std::integral_constant<int, MANY>{});
   __syncthreads();
-  if (tid < G::CH && col * G::CH + tid < p.D) {
-    const size_t dc = (size_t)col * G::CH + tid;
+  if (tid < CH && col * CH + tid < p.D) {
+    const size_t dc = (size_t)col * CH + tid;
     float TB = 1.0f, TM = 0.0f;
 #pragma unroll 4
-    for (int i = G::GRP - 1; i >= 0; --i) compose(TB, TM, sB[i][tid], sM[i][tid]);
+    for (int i = GRP - 1; i >= 0; --i) compose(TB, TM, sB[i][tid], sM[i][tid]);
     float h = p.carry[(size_t)tile * p.D + dc];
-    float E = pass_state(w, k, p.D, col * G::CH, tid, TB, TM);
+    float E = pass_state(w, k, p.D, col * CH, tid, TB, TM);
 #pragma unroll 4
-    for (int i = 0; i < G::GRP; ++i) {
+    for (int i = 0; i < GRP; ++i) {
       const float A = sA[i][tid], L = sL[i][tid];
       sL[i][tid] = h;
       h = apply(A, L, h);
     }
 #pragma unroll 4
-    for (int i = G::GRP - 1; i >= 0; --i) {
+    for (int i = GRP - 1; i >= 0; --i) {
       const float B = sB[i][tid], M = sM[i][tid];
       sM[i][tid] = E;
       E = apply(B, M, E);
     }
   }
   __syncthreads();
-  if (!d_ok) return;
+  if (n_el == 0) return;
 #pragma unroll
   for (int r = 0; r < R; ++r) {   // the exps are computed again: kept, they would take R * VEC registers
     g[r].opaque();
@@ -485,41 +497,48 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     dy[r].opaque();
   }
 
-  if (__all(plain)) {
+  if (mode != MANY) {
 #pragma unroll
     for (int c = 0; c < VEC; c += NV) {
       __builtin_amdgcn_sched_barrier(0);
-      float a[R][NV], before[R][NV], h[NV], E[NV];
+      float a[R][NV], before[R][NV], h[NV], E[NV], h0[NV], e0[NV];
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         h[v] = sL[grp][lr * VEC + c + v];
         E[v] = sM[grp][lr * VEC + c + v];
+        h0[v] = e0[v] = 0.0f;
       }
+      if (mode == ONE) ends(c, h0, e0);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float xf[NV];
         unpack_word<DT, VEC, NV>(g[r], c, a[r]);
         unpack_word<DT, VEC, NV>(x[r], c, xf);
+        const bool start = first >> r & 1;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           a[r][v] = decay(a[r][v]);
-          before[r][v] = h[v];
-          h[v] = fmaf(a[r][v], h[v], xf[v]);
+          before[r][v] = start ? h0[v] : h[v];
+          h[v] = fmaf(a[r][v], before[r][v], xf[v]);
         }
       }
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
         float df[NV], dg[NV];
         unpack_word<DT, VEC, NV>(dy[r], c, df);
+        const bool end = last >> r & 1, start = first >> r & 1;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          df[v] += E[v];
+          df[v] += end ? e0[v] : E[v];
           E[v] = a[r][v] * df[v];
           dg[v] = E[v] * before[r][v];
+          if (start) h0[v] = E[v];   // the gradient of the initial state, from here on
         }
         pack_word<DT, VEC, NV>(x[r], c, df);
         pack_word<DT, VEC, NV>(g[r], c, dg);
       }
+      if (first != 0 && n_el > c)
+        store_state_part<EXACT, NV>(p.fin, p.fin_dtype, row(__builtin_ctz(first)) + c, n_el - c, h0);
 #pragma unroll
       for (int r = 0; r < R; ++r) {   // each pack stays one run of registers: no copies of it
         g[r].opaque();
@@ -528,20 +547,53 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r].stream_at(p.dx, at(r), off);
-      g[r].stream_at(p.dg, at(r), off);
+      if (!(in >> r & 1)) continue;
+      store_part<EXACT>(x[r], static_cast<uint8_t*>(p.dx) + at(r) + off, n_el);
+      store_part<EXACT>(g[r], static_cast<uint8_t*>(p.dg) + at(r) + off, n_el);
     }
     return;
   }
-  // A wave whose tokens begin or end a sequence reads them again (they are in the caches), a
-  // word at a time: with the packs and every case of every token in registers at once, the
-  // kernel would need 242 of them and lose a third of its waves.
-  for (int c = 0; c < VEC; c += NV) {
+  // MANY: the tokens are read again (they are in the caches), a word at a time: with the packs
+  // and every case of every token in registers at once, the kernel would need 242 of them and
+  // lose a third of its waves. Sequences of 8 tokens and more are never here.
+  for (int c = 0; c < VEC && c < n_el; c += NV) {
     float a[R][NV], before[R][NV], h[NV], E[NV];
     int q = grp * R;
     uint32_t o = off + c * elem_size(DT);
     asm volatile("" : "+v"(q), "+v"(o));   // no address is kept from word to word
     auto row = [&](int r) { return (size_t)places.n[q + r] * p.D + d + c; };
+    auto read = [&](const void* from, int r, float* f) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) f[v] = 0.0f;
+      if (EXACT) {
+        Pack<DT, NV> k;
+        k.load_at(from, at(r), o);
+        k.unpack(f);
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (c + v < n_el) {
+            Pack<DT, 1> k;
+            k.load_at(from, at(r), o + v * elem_size(DT));
+            k.unpack(f + v);
+          }
+      }
+    };
+    auto write = [&](void* to, int r, const float* f) {
+      if (EXACT) {
+        Pack<DT, NV> k;
+        k.pack(f);
+        k.store_at(to, at(r), o);
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (c + v < n_el) {
+            Pack<DT, 1> k;
+            k.pack(f + v);
+            k.store_at(to, at(r), o + v * elem_size(DT));
+          }
+      }
+    };
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       h[v] = sL[grp][lr * VEC + c + v];
@@ -550,13 +602,10 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (!(in >> r & 1)) continue;
-      Pack<DT, NV> gq, xq;
-      gq.load_at(p.g, at(r), o);
-      xq.load_at(p.x, at(r), o);
       float xf[NV];
-      gq.unpack(a[r]);
-      xq.unpack(xf);
-      if (first >> r & 1) load_state<NV>(p.init, p.init_dtype, row(r), h);
+      read(p.g, r, a[r]);
+      read(p.x, r, xf);
+      if (first >> r & 1) load_state_part<EXACT, NV>(p.init, p.init_dtype, row(r), n_el - c, h);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         a[r][v] = decay(a[r][v]);
@@ -567,22 +616,18 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
       if (!(in >> r & 1)) continue;
-      Pack<DT, NV> q1, q2;
       float df[NV], dg[NV];
-      q1.load_at(p.dy, at(r), o);
-      q1.unpack(df);
-      if (last >> r & 1) load_state<NV>(p.dfin, p.dfin_dtype, row(r), E);
+      read(p.dy, r, df);
+      if (last >> r & 1) load_state_part<EXACT, NV>(p.dfin, p.dfin_dtype, row(r), n_el - c, E);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         df[v] += E[v];
         E[v] = a[r][v] * df[v];
         dg[v] = E[v] * before[r][v];
       }
-      q1.pack(df);
-      q2.pack(dg);
-      q1.store_at(p.dx, at(r), o);
-      q2.store_at(p.dg, at(r), o);
-      if (first >> r & 1) store_state<NV>(p.fin, p.fin_dtype, row(r), E);
+      write(p.dx, r, df);
+      write(p.dg, r, dg);
+      if (first >> r & 1) store_state_part<EXACT, NV>(p.fin, p.fin_dtype, row(r), n_el - c, E);
     }
   }
 }
@@ -626,28 +671,23 @@ __global__ __launch_bounds__(64) void kda_glr_tokens_kernel(GlrParams p, int col
   store_state<VEC>(p.fin, out_dtype, (size_t)out_row * p.D + d, h);
 }
 
-// f(element type, vector length) for the widest vectors that rows of D elements allow
+// f(element type, elements of a vector, whether rows are whole vectors)
 template <typename F>
 hipError_t by_type(int dt, int32_t D, F f) {
-  const bool wide = D % (16 / elem_size(dt)) == 0;
-  using std::integral_constant;
-  if (dt == BF16) {
-    if (wide) f(integral_constant<int, BF16>{}, integral_constant<int, 8>{});
-    else f(integral_constant<int, BF16>{}, integral_constant<int, 1>{});
-  } else if (dt == FP16) {
-    if (wide) f(integral_constant<int, FP16>{}, integral_constant<int, 8>{});
-    else f(integral_constant<int, FP16>{}, integral_constant<int, 1>{});
-  } else {
-    if (wide) f(integral_constant<int, FP32>{}, integral_constant<int, 4>{});
-    else f(integral_constant<int, FP32>{}, integral_constant<int, 1>{});
-  }
+  const auto go = [&](auto type) {
+    constexpr int VEC = 16 / elem_size(decltype(type)::value);
+    if (D % VEC == 0) f(type, std::integral_constant<int, VEC>{}, std::true_type{});
+    else f(type, std::integral_constant<int, 1>{}, std::false_type{});
+  };
+  if (dt == BF16) go(std::integral_constant<int, BF16>{});
+  else if (dt == FP16) go(std::integral_constant<int, FP16>{});
+  else go(std::integral_constant<int, FP32>{});
   return hipGetLastError();
 }
 
 int32_t tile_count(int64_t tokens) { return (int32_t)((tokens + GLR_TILE - 1) / GLR_TILE); }
 int32_t tile_cols(int dt, int32_t D) {
-  const int v = 16 / elem_size(dt);
-  const int ch = D % v == 0 ? 16 * v : 64;
+  const int ch = LR * (16 / elem_size(dt));
   return (D + ch - 1) / ch;
 }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -693,7 +733,7 @@ bool glr_fits(int64_t tokens, int64_t D, int64_t nseq) {
 hipError_t launch_glr_fwd(const GlrParams& p, void* workspace, hipStream_t stream) {
   if (p.nseq <= 0) return hipSuccess;
   if (p.in_slots || few_tokens(p)) {
-    return by_type(p.dtype, p.D, [&](auto dt, auto vec) {
+    return by_type(p.dtype, p.D, [&](auto dt, auto vec, auto) {
       const int cols = (p.D + 64 * vec.value - 1) / (64 * vec.value);
       const dim3 grid((unsigned)cols * (unsigned)p.nseq);
       if (p.in_slots)
@@ -712,8 +752,8 @@ hipError_t launch_glr_fwd(const GlrParams& p, void* workspace, hipStream_t strea
     q.init = w.stage;
     q.init_dtype = FP32;
   }
-  return by_type(p.dtype, p.D, [&](auto dt, auto vec) {
-    hipLaunchKernelGGL((kda_glr_fwd_tile_kernel<dt.value, vec.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
+  return by_type(p.dtype, p.D, [&](auto dt, auto, auto exact) {
+    hipLaunchKernelGGL((kda_glr_fwd_tile_kernel<dt.value, exact.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
                        0, stream, q, q.cu, w);
   });
 }
@@ -723,8 +763,8 @@ hipError_t launch_glr_bwd(const GlrParams& p, void* workspace, hipStream_t strea
   const TileWs w = tile_ws(p, workspace, false);
   const hipError_t e = launch_prep(p, w, p.dfin, p.dfin_dtype, stream);
   if (e != hipSuccess || w.tiles == 0) return e;
-  return by_type(p.dtype, p.D, [&](auto dt, auto vec) {
-    hipLaunchKernelGGL((kda_glr_bwd_tile_kernel<dt.value, vec.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
+  return by_type(p.dtype, p.D, [&](auto dt, auto, auto exact) {
+    hipLaunchKernelGGL((kda_glr_bwd_tile_kernel<dt.value, exact.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
                        0, stream, p, p.cu, w);
   });
 }
