@@ -45,10 +45,6 @@ struct Pack {
   __device__ __forceinline__ void store_at(void* p, size_t uniform, uint32_t lane) const {
     *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + uniform + lane) = r;
   }
-  // whole rows of outputs, not kept in the caches: the inputs stay there instead
-  __device__ __forceinline__ void stream_at(void* p, size_t uniform, uint32_t lane) const {
-    __builtin_nontemporal_store(r, reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + uniform + lane));
-  }
   // the compiler forgets what it has computed from these registers
   __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void clear() { r = Raw{}; }
@@ -183,11 +179,13 @@ __device__ __forceinline__ void load_part(Pack<DT, VEC>& q, const uint8_t* a, in
     q.r.x = w2(a);
   }
 }
-template <bool EXACT, int DT, int VEC>
+// STREAM: not kept in the caches, the inputs stay there instead
+template <bool EXACT, bool STREAM = true, int DT, int VEC>
 __device__ __forceinline__ void store_part(const Pack<DT, VEC>& q, uint8_t* a, int c) {
   if (EXACT || c >= VEC) {
     using Any = u32x4 __attribute__((aligned(2)));   // any alignment
-    __builtin_nontemporal_store(q.r, reinterpret_cast<Any*>(a));
+    if (STREAM) __builtin_nontemporal_store(q.r, reinterpret_cast<Any*>(a));
+    else *reinterpret_cast<Any*>(a) = q.r;
     return;
   }
   if constexpr (DT == FP32) {

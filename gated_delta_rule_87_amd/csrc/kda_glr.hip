@@ -215,6 +215,20 @@ __device__ __forceinline__ void find_places(const GlrParams& p, const int64_t* c
   }
 }
 
+// The channels of this workgroup. Workgroups go to the 8 XCDs in turn: neighbouring channels,
+// which share lines where rows are not aligned, are put on one XCD and its L2 (8191 channels
+// bf16 backward 214 -> 186 us; 8192: 141 -> 137).
+__device__ __forceinline__ int tile_col(int cols) {
+  const int b = blockIdx.x % cols, eighth = cols >> 3;
+  return b < 8 * eighth ? (b & 7) * eighth + (b >> 3) : b;
+}
+
+// The next tile in the order of processing, from the counter of the channels (one lane asks)
+__device__ __forceinline__ int take_tile(const TileWs& w, int col) {
+  if (w.tiles == 1) return 0;
+  return (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ---- before the tiles: the words EMPTY, the counters zero; states of empty sequences ----
 
 __global__ __launch_bounds__(256) void kda_glr_prep_kernel(GlrParams p, TileWs w, const void* from, int from_dtype) {
@@ -242,9 +256,8 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
   __shared__ TilePlaces places;
   __shared__ int s_tile;
   const int tid = threadIdx.x, lr = tid % LR, grp = tid / LR;
-  const int col = blockIdx.x % w.cols;
-  if (tid == 0)
-    s_tile = (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int col = tile_col(w.cols);
+  if (tid == 0) s_tile = take_tile(w, col);
   __syncthreads();
   const int tile = __builtin_amdgcn_readfirstlane(s_tile);
   const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
@@ -368,9 +381,8 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   __shared__ TilePlaces places;
   __shared__ int s_tile;
   const int tid = threadIdx.x, lr = tid % LR, grp = tid / LR;
-  const int col = blockIdx.x % w.cols;
-  if (tid == 0)
-    s_tile = (int)__hip_atomic_fetch_add(w.ticks + col * TICK_STRIDE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int col = tile_col(w.cols);
+  if (tid == 0) s_tile = take_tile(w, col);
   __syncthreads();
   const int k = __builtin_amdgcn_readfirstlane(s_tile), tile = w.tiles - 1 - k;
   const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
@@ -548,8 +560,10 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (!(in >> r & 1)) continue;
-      store_part<EXACT>(x[r], static_cast<uint8_t*>(p.dx) + at(r) + off, n_el);
-      store_part<EXACT>(g[r], static_cast<uint8_t*>(p.dg) + at(r) + off, n_el);
+      // (lines shared with the next tile's rows are completed in the cache: 8191 channels 207 -> 187 us;
+      // forward, with half as many stores, streaming is faster there too: 111 -> 100 us)
+      store_part<EXACT, EXACT>(x[r], static_cast<uint8_t*>(p.dx) + at(r) + off, n_el);
+      store_part<EXACT, EXACT>(g[r], static_cast<uint8_t*>(p.dg) + at(r) + off, n_el);
     }
     return;
   }
@@ -635,9 +649,11 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
 // ---- few tokens per sequence -----------------------------------------------------------
 
 // One lane per VEC channels of a sequence, token by token, from and to rows of the states or
-// slots of a cache.
+// slots of a cache (SLOTS: a single token). Otherwise 8 tokens are loaded at once (16 tokens of
+// one row of 8192 channels: 6.0 -> 4.8 us).
 template <int DT, int VEC, bool SLOTS>
 __global__ __launch_bounds__(64) void kda_glr_tokens_kernel(GlrParams p, int cols) {
+  constexpr int AHEAD = SLOTS ? 1 : 8;
   const int n = blockIdx.x / cols, d = ((blockIdx.x - n * cols) * 64 + threadIdx.x) * VEC;
   if (d >= p.D) return;
   int64_t b = (int64_t)n * p.T, e = b + p.T;
@@ -654,19 +670,29 @@ __global__ __launch_bounds__(64) void kda_glr_tokens_kernel(GlrParams p, int col
   }
   float h[VEC];
   load_state<VEC>(p.init, in_dtype, (size_t)in_row * p.D + d, h);
-  for (int64_t t = b; t < e; ++t) {
-    const size_t i = (size_t)t * p.D + d;
-    Pack<DT, VEC> g, x, y;
-    g.load(p.g, i);
-    x.load(p.x, i);
-    float gf[VEC], xf[VEC];
-    g.unpack(gf);
-    x.unpack(xf);
-    if (p.carry && t % GLR_TILE == 0) store_f32<FP32, VEC>(p.carry, (size_t)(t / GLR_TILE) * p.D + d, h);
+  for (int64_t t0 = b; t0 < e; t0 += AHEAD) {
+    Pack<DT, VEC> g[AHEAD], x[AHEAD];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
-    y.pack(h);
-    y.store(p.y, i);
+    for (int r = 0; r < AHEAD; ++r) {
+      if (t0 + r < e) {
+        g[r].load(p.g, (size_t)(t0 + r) * p.D + d);
+        x[r].load(p.x, (size_t)(t0 + r) * p.D + d);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) {
+      const int64_t t = t0 + r;
+      if (t >= e) break;
+      float gf[VEC], xf[VEC];
+      g[r].unpack(gf);
+      x[r].unpack(xf);
+      if (p.carry && t % GLR_TILE == 0) store_f32<FP32, VEC>(p.carry, (size_t)(t / GLR_TILE) * p.D + d, h);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
+      Pack<DT, VEC> y;
+      y.pack(h);
+      y.store(p.y, (size_t)t * p.D + d);
+    }
   }
   store_state<VEC>(p.fin, out_dtype, (size_t)out_row * p.D + d, h);
 }
@@ -715,9 +741,13 @@ hipError_t launch_prep(const GlrParams& p, const TileWs& w, const void* from, in
   return hipGetLastError();
 }
 
-// Few tokens per sequence: rows of at most 16 tokens, packed batches of at most 2 on average
-// (as kda_fwd's own rule; the lengths stay on the device).
-bool few_tokens(const GlrParams& p) { return p.cu ? p.T <= 2 * (int64_t)p.nseq : p.T <= 16; }
+// Few tokens per sequence: rows of at most FEW tokens (8192 channels bf16: 16 tokens 4.8 us
+// against 8.1 in tiles, 32 the same, 64 13.0 against 7.5), packed batches of at most 2 on average
+// (256 tokens 5.4 against 19.9 us; the lengths stay on the device, as with kda_fwd's own rule).
+constexpr int32_t FEW = 32;
+bool few_tokens(const GlrParams& p) { return p.cu ? p.T <= 2 * (int64_t)p.nseq : p.T <= FEW; }
+// One tile, and nothing to do before it: no counters, no words to fill.
+bool lone_tile(const GlrParams& p, const TileWs& w) { return w.tiles == 1 && !p.cu && !w.stage; }
 
 }  // namespace
 
@@ -745,8 +775,10 @@ hipError_t launch_glr_fwd(const GlrParams& p, void* workspace, hipStream_t strea
   // a sequence's final state may be written while another workgroup still reads its initial one
   const bool stage = p.init && p.init == p.fin;
   const TileWs w = tile_ws(p, workspace, stage);
-  hipError_t e = launch_prep(p, w, p.init, p.init_dtype, stream);
-  if (e != hipSuccess) return e;
+  if (!lone_tile(p, w)) {
+    const hipError_t e = launch_prep(p, w, p.init, p.init_dtype, stream);
+    if (e != hipSuccess) return e;
+  }
   GlrParams q = p;
   if (stage) {
     q.init = w.stage;
@@ -761,8 +793,11 @@ hipError_t launch_glr_fwd(const GlrParams& p, void* workspace, hipStream_t strea
 hipError_t launch_glr_bwd(const GlrParams& p, void* workspace, hipStream_t stream) {
   if (p.nseq <= 0) return hipSuccess;
   const TileWs w = tile_ws(p, workspace, false);
-  const hipError_t e = launch_prep(p, w, p.dfin, p.dfin_dtype, stream);
-  if (e != hipSuccess || w.tiles == 0) return e;
+  if (!lone_tile(p, w)) {
+    const hipError_t e = launch_prep(p, w, p.dfin, p.dfin_dtype, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (w.tiles == 0) return hipSuccess;
   return by_type(p.dtype, p.D, [&](auto dt, auto, auto exact) {
     hipLaunchKernelGGL((kda_glr_bwd_tile_kernel<dt.value, exact.value>), dim3((unsigned)w.cols * (unsigned)w.tiles), dim3(256),
                        0, stream, p, p.cu, w);
