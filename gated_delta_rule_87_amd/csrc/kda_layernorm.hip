@@ -415,22 +415,26 @@ __global__ __launch_bounds__(64) void kda_layernorm_cols_kernel(NormParams p, in
   }
 }
 
-// The parts' sums: 16 columns of dw (blockIdx.y 0) or db by 64 runs of parts a workgroup.
+// The parts' sums: COLS columns of dw (blockIdx.y 0) or db by 1024 / COLS runs of parts a
+// workgroup: many runs where there are few columns, whole lines where there are many (8192
+// columns, 256 parts: 8 us with 16 columns).
+template <int COLS>
 __global__ __launch_bounds__(1024) void kda_layernorm_sum_kernel(NormParams p, int parts) {
-  __shared__ float buf[64][17];
+  constexpr int RUNS = 1024 / COLS;
+  __shared__ float buf[RUNS][COLS + 1];
   float* out = blockIdx.y ? p.db : p.dw;
   if (!out) return;
   const float* in = p.partial + (blockIdx.y ? (size_t)parts * p.D : 0);
-  const int j = threadIdx.x & 15, run = threadIdx.x >> 4, col = blockIdx.x * 16 + j;
+  const int j = threadIdx.x % COLS, run = threadIdx.x / COLS, col = blockIdx.x * COLS + j;
   float s = 0.0f;
   if (col < p.D) {
 #pragma unroll 8
-    for (int i = run; i < parts; i += 64) s += in[(size_t)i * p.D + col];
+    for (int i = run; i < parts; i += RUNS) s += in[(size_t)i * p.D + col];
   }
   buf[run][j] = s;
   __syncthreads();
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
+  for (int o = RUNS / 2; o >= 1; o >>= 1) {
     if (run < o) buf[run][j] += buf[run + o][j];
     __syncthreads();
   }
@@ -532,7 +536,10 @@ hipError_t launch_layernorm_bwd(const NormParams& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (p.dw || p.db) {
-    hipLaunchKernelGGL(kda_layernorm_sum_kernel, dim3((p.D + 15) / 16, 2), dim3(1024), 0, stream, p, parts);
+    if (p.D <= 2048)
+      hipLaunchKernelGGL(kda_layernorm_sum_kernel<16>, dim3((p.D + 15) / 16, 2), dim3(1024), 0, stream, p, parts);
+    else
+      hipLaunchKernelGGL(kda_layernorm_sum_kernel<64>, dim3((p.D + 63) / 64, 2), dim3(1024), 0, stream, p, parts);
     return hipGetLastError();
   }
   return hipSuccess;
