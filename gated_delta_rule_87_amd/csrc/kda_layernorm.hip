@@ -489,9 +489,10 @@ unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : mos
 }  // namespace
 
 // Workgroups of a backward pass, at most: their sums take two rows of D each in the workspace,
-// so wide rows get one workgroup per compute unit and short ones enough to fill the GPU.
+// so wide rows get one workgroup per compute unit and short ones enough to fill the GPU. Rows of
+// more than 16384 elements: as many parts as fill it beside their columns' lanes.
 size_t layernorm_parts(int64_t M, int64_t D) {
-  const int64_t most = D <= 1024 ? 1024 : D <= 2048 ? 768 : D <= 4096 ? 512 : 256;
+  const int64_t most = D <= 1024 ? 1024 : D <= 2048 ? 768 : D <= 4096 ? 512 : D <= 16384 ? 256 : 1 + (8192 * 512) / D;
   return (size_t)(M < most ? M : most);
 }
 
@@ -525,7 +526,6 @@ hipError_t launch_layernorm_bwd(const NormParams& p, hipStream_t stream) {
       if (!done) {
         if (p.partial) {
           const int64_t cols = ((int64_t)p.D + 64 * vec_of<DT>() - 1) / (64 * vec_of<DT>());
-          parts = (int)at_most(parts, 1 + 8192 / cols);
           hipLaunchKernelGGL(kda_layernorm_cols_kernel<DT>, dim3((unsigned)cols * parts), dim3(64), 0, stream, p, parts);
         }
         if (p.out)

@@ -16,7 +16,8 @@ namespace {
 using kda::aligned;
 
 using kda::MAX_SLOTS;
-constexpr int64_t MAX_D = (int64_t)1 << 24;
+constexpr int64_t MAX_D = (int64_t)1 << 24;          // of a row of layer norm
+constexpr int64_t MAX_CHANNELS = (int64_t)1 << 22;   // of the recurrence: 32-bit offsets inside a tile
 
 bool bad_state_code(int c) { return c != KDA_STATE_NONE && c != KDA_STATE_BF16 && c != KDA_STATE_FP32; }
 bool bad_dtype(int c) { return c != KDA_BF16 && c != KDA_FP32 && c != KDA_FP16; }
@@ -38,7 +39,7 @@ bool any_unaligned(std::initializer_list<const void*> ps, size_t a) {
 int check_glr(const void* a, const void* b, const void* c, int dtype, const int64_t* cu, int64_t N, int64_t B, int64_t T,
               int64_t D) {
   if (T != 0 && (!a || !b || !c)) return KDA_ERR_NULL;
-  if (B < 1 || T < 0 || D < 1 || D > MAX_D) return KDA_ERR_SHAPE;
+  if (B < 1 || T < 0 || D < 1 || D > MAX_CHANNELS) return KDA_ERR_SHAPE;
   if (cu && (B != 1 || N < 1)) return KDA_ERR_SHAPE;
   if (T > INT32_MAX / 2 || B > INT32_MAX / 2 || B * T >= (int64_t)INT32_MAX / 2) return KDA_ERR_SHAPE;
   if ((cu ? N : B) > INT32_MAX / 2 || !kda::glr_fits(B * T, D, cu ? N : B)) return KDA_ERR_SHAPE;
@@ -82,7 +83,7 @@ int64_t kda_glr_carry_rows(int64_t B, int64_t T) {
 }
 
 size_t kda_glr_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N) {
-  if (B < 1 || T < 0 || D < 1 || N < 0 || D > MAX_D || T > INT32_MAX || B > INT32_MAX || N > INT32_MAX) return 0;
+  if (B < 1 || T < 0 || D < 1 || N < 0 || D > MAX_CHANNELS || T > INT32_MAX || B > INT32_MAX || N > INT32_MAX) return 0;
   return kda::glr_workspace(B * T, D, N > 0 ? N : B);
 }
 
@@ -144,7 +145,7 @@ int kda_glr_bwd(const void* x, const void* g, const void* dy, int dtype, const f
 
 int kda_glr_step(const void* x, const void* g, void* y, int dtype, void* state, int state_dtype, int64_t S,
                  const int32_t* in_slots, const int32_t* out_slots, int64_t N, int64_t D, void* stream) {
-  if (N < 0 || N > INT32_MAX || D < 1 || D > MAX_D || S < 1 || S > MAX_SLOTS || !kda::glr_fits(0, D, N)) return KDA_ERR_SHAPE;
+  if (N < 0 || N > INT32_MAX || D < 1 || D > MAX_CHANNELS || S < 1 || S > MAX_SLOTS || !kda::glr_fits(0, D, N)) return KDA_ERR_SHAPE;
   if (!state || (N != 0 && (!x || !g || !y || !in_slots || !out_slots))) return KDA_ERR_NULL;
   if (bad_dtype(dtype) || (state_dtype != KDA_STATE_BF16 && state_dtype != KDA_STATE_FP32)) return KDA_ERR_DTYPE;
   if (any_unaligned({x, g, y, state}, 16) || any_unaligned({in_slots, out_slots}, 4)) return KDA_ERR_ALIGN;
@@ -234,6 +235,7 @@ int kda_cache_fork(void* pool, int64_t L, int64_t S, size_t slot_bytes, int32_t*
   if (rc != KDA_OK) return rc;
   if (!used || (n != 0 && (!src || !dst))) return KDA_ERR_NULL;
   if (any_unaligned({used, src, dst}, 4)) return KDA_ERR_ALIGN;
+  if (n != 0 && (dst == src || dst == used || src == used)) return KDA_ERR_VALUE;
   if (n == 0) return KDA_OK;
   return status(kda::launch_cache_fork({pool, L, S, slot_bytes}, used, src, dst, n, static_cast<hipStream_t>(stream)));
 }
@@ -252,6 +254,7 @@ int kda_cache_compact(void* pool, int64_t L, int64_t S, size_t slot_bytes, int32
   if (!used || !remap) return KDA_ERR_NULL;
   if (!table) n = 0;
   if (any_unaligned({used, remap, table}, 4)) return KDA_ERR_ALIGN;
+  if (used == remap || table == remap || table == used) return KDA_ERR_VALUE;
   if (!workspace || workspace_bytes < kda_cache_workspace_size(S)) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
   return status(kda::launch_cache_compact({pool, L, S, slot_bytes}, used, remap, table, n,

@@ -61,7 +61,8 @@ enum kda_status {
                               state given with different dtypes                     */
     KDA_ERR_VALUE = 4,     /* lower_bound outside [-5, 0] or not finite (safe gate),
                               scale not finite, eps negative or not finite, unknown
-                              flag bits, bad cu_seqlens contents (KDA_VALIDATE=1)   */
+                              flag bits, one buffer given twice where that is ruled
+                              out, bad cu_seqlens contents (KDA_VALIDATE=1)         */
     KDA_ERR_ALIGN = 5,     /* a pointer is not 16-byte aligned                      */
     KDA_ERR_WORKSPACE = 6, /* workspace NULL or too small (kda_fwd_workspace_min, or the
                               operator's own kda_*_workspace_size)                  */
@@ -273,7 +274,7 @@ size_t kda_noalloc_capacity(void);
  *
  * Rules of every kda_cache_* call: S <= 2^24, L >= 1, slot_bytes >= 1; pool is
  * aligned to 16 bytes, used, src, dst, slots, remap and table to 4; the arrays do
- * not overlap each other. n may be 0 (nothing is done; the index arrays may then
+ * not overlap each other (KDA_ERR_VALUE where one is given twice). n may be 0 (nothing is done; the index arrays may then
  * be NULL). A slot number outside [0, S) is never followed: what it means is
  * said at each call.
  *
@@ -340,7 +341,9 @@ enum kda_dtype {
  * Per sequence and channel, from the state h of before its first token:
  *     h_t = exp(g_t) h_{t-1} + x_t,      y_t = h_t
  * g is the log-decay, as kda_fwd takes it with KDA_FUSE_GATE clear (not clamped
- * here): g <= 0 forgets, -inf starts over from x_t. The backward pass, with dy_t
+ * here): g <= 0 forgets, -inf starts over from x_t. Gates above 0 are taken as
+ * they are; where their exponentials' product over 1024 tokens overflows fp32,
+ * results are unspecified. The backward pass, with dy_t
  * and the final state's gradient d_final added at the last token:
  *     G_t = dy_t + exp(g_{t+1}) G_{t+1}
  *     dx_t = G_t,   dg_t = G_t exp(g_t) h_{t-1},   d_initial = exp(g_first) G_first
@@ -348,7 +351,7 @@ enum kda_dtype {
  *
  *   x, g, y, dy, dx, dg   [B, T, D] in `dtype` (KDA_BF16, KDA_FP32 or KDA_FP16).
  *                         T may be 0 (they hold no element and may be NULL).
- *   D                     channels, 1 <= D <= 2^24, any number (whole multiples
+ *   D                     channels, 1 <= D <= 2^22, any number (whole multiples
  *                         of 16 bytes are fastest)
  *   initial_state, final_state, their dtypes, cu_seqlens, N, B, T
  *                         as for kda_fwd, with states [B|N, D]. Tokens of a packed

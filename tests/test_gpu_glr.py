@@ -380,3 +380,79 @@ def test_boundaries_out_of_order_stay_in_bounds():
         kda.glr_fwd(x, -x.abs(), y[32:32 + T].unsqueeze(0), final_state=st, cu_seqlens=torch.tensor(cu, device=d))
         torch.cuda.synchronize()
         assert (y[:32] == 7).all() and (y[32 + T:] == 7).all()
+
+
+@pytest.mark.parametrize("N,T", [(70000, 70000), (70000, 200000)])
+def test_many_sequences(N, T):
+    """More sequences than a launch's second grid dimension holds, by tokens and by tiles."""
+    say("sequences", N, "tokens", T)
+    gen = torch.Generator().manual_seed(0)
+    cut = torch.sort(torch.randint(0, T + 1, (N - 1,), generator=gen)).values
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), cut, torch.full((1,), T)])
+    D = 8
+    x, g = torch.randn(1, T, D, generator=gen), -torch.rand(1, T, D, generator=gen)
+    h0 = torch.randn(N, D, generator=gen)
+    y, fin = torch.empty(1, T, D, device=dev()), torch.empty(N, D, device=dev())
+    kda.glr_fwd(x.to(dev()), g.to(dev()), y, initial_state=h0.to(dev()), final_state=fin, cu_seqlens=cu.to(dev()))
+    # the recurrence over all sequences at once, token i of each (none is longer than the longest)
+    f = torch.float64
+    lengths = cu[1:] - cu[:-1]
+    h, e, s = h0.to(f), torch.zeros(N, D, dtype=f), h0.to(f).abs()
+    yv, ye = torch.zeros(T, D, dtype=f), torch.zeros(T, D, dtype=f)
+    for i in range(int(lengths.max())):
+        on = (lengths > i).nonzero()[:, 0]
+        t = cu[on] + i
+        a = g[0, t].to(f).exp()
+        h[on] = a * h[on] + x[0, t].to(f)
+        s[on] = a * s[on] + x[0, t].to(f).abs()
+        e[on] = a * e[on] + (8 + 2 * g[0, t].to(f).abs()) * po.U * s[on]
+        yv[t], ye[t] = h[on], e[on]
+    po.assert_near("y", y[0], yv, ye)
+    po.assert_near("final", fin, h, e)
+
+
+def test_validation_of_boundaries(monkeypatch):
+    """KDA_VALIDATE=1: contents that break the precondition are refused, nothing is written."""
+    say("KDA_VALIDATE")
+    monkeypatch.setenv("KDA_VALIDATE", "1")
+    d = dev()
+    x = torch.randn(1, 40, 16, device=d)
+    y = torch.full_like(x, 7.0)
+    carry, h = torch.zeros(kda.glr_carry_shape(1, 40, 16), device=d), torch.zeros(2, 16, device=d)
+    for cu in ([0, 30, 20], [1, 20, 40], [0, 20, 39]):
+        c = torch.tensor(cu, device=d)
+        with pytest.raises(kda.KDAError) as e:
+            kda.glr_fwd(x, -x.abs(), y, final_state=h, cu_seqlens=c)
+        assert e.value.code == 4
+        with pytest.raises(kda.KDAError) as e:
+            kda.glr_bwd(x, -x.abs(), x, carry, y, y.clone(), cu_seqlens=c)
+        assert e.value.code == 4
+    assert (y == 7).all()
+    kda.glr_fwd(x, -x.abs(), y, final_state=h, cu_seqlens=torch.tensor([0, 15, 40], device=d))
+
+
+def test_refusals_of_the_wrappers():
+    """Shapes, types, strides and devices that do not fit, before anything is launched."""
+    d = dev()
+    x, i = torch.zeros(2, 40, 16, device=d), torch.zeros(2, dtype=torch.int32, device=d)
+    g, y, st = torch.zeros_like(x), torch.zeros_like(x), torch.zeros(2, 16, device=d)
+    carry = torch.zeros(1, 16, device=d)
+    bad = [lambda: kda.glr_fwd(x, g.bfloat16(), y), lambda: kda.glr_fwd(x, g[:, :39], y), lambda: kda.glr_fwd(x, g, y[..., :15]),
+           lambda: kda.glr_fwd(x.transpose(0, 1), g.transpose(0, 1), y.transpose(0, 1)), lambda: kda.glr_fwd(x, g.cpu(), y),
+           lambda: kda.glr_fwd(x.double(), g.double(), y.double()), lambda: kda.glr_fwd(x, g, y, initial_state=st[:1]),
+           lambda: kda.glr_fwd(x, g, y, initial_state=st, final_state=st.bfloat16()),
+           lambda: kda.glr_fwd(x, g, y, cu_seqlens=torch.tensor([0, 80], device=d)),
+           lambda: kda.glr_fwd(x, g, y, carry=carry.bfloat16()), lambda: kda.glr_bwd(x, g, x, carry[:, :8], y, g),
+           lambda: kda.glr_bwd(x, g, x, carry, y, g.clone(), d_final=st.half()),
+           lambda: kda.glr_step(x[0], g[0], y[0], st, i, i), lambda: kda.glr_step(x[0, :2], g[0, :2], y[0, :2], st, i.long(), i)]
+    for n, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print("not refused:", n)
+    with pytest.raises(kda.KDAError) as e:   # a view that starts between two 16-byte addresses
+        flat = torch.zeros(2 * 40 * 16 + 1, device=d)
+        kda.glr_fwd(flat[1:].view(2, 40, 16), g, y)
+    assert e.value.code == 5
+    with pytest.raises(kda.KDAError) as e:
+        kda.glr_fwd(x, g, y, workspace=torch.empty(16, dtype=torch.uint8, device=d))
+    assert e.value.code == 6

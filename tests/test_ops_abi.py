@@ -51,7 +51,7 @@ def test_glr_refusals(name, d):
     for k in ("x", "g", third) + (("carry", "dx", "dg") if third == "dy" else ()):
         assert go(**{k: None}) == ENULL, k
         assert go(**{k: d[k] + 2}) == EALIGN, k
-    for bad in (dict(B=0), dict(T=-1), dict(D=0), dict(D=(1 << 24) + 1), dict(cu=fake(7), N=2), dict(cu=fake(7), N=0, B=1),
+    for bad in (dict(B=0), dict(T=-1), dict(D=0), dict(D=(1 << 22) + 1), dict(cu=fake(7), N=2), dict(cu=fake(7), N=0, B=1),
                 dict(B=1 << 20, T=1 << 20), dict(B=1 << 62, T=4), dict(T=1 << 62), dict(B=1 << 24, T=1),
                 dict(cu=fake(7), N=1 << 24, B=1), dict(T=1 << 29, D=1 << 20)):
         assert go(**bad) == ESHAPE, bad
@@ -132,6 +132,10 @@ def test_layernorm_refusals():
     assert call("kda_layernorm_bwd", LN_B, ws=fake(9) + 16) == EALIGN
     # nothing wanted: nothing launched
     assert call("kda_layernorm_bwd", LN_B, dx=None, dw=None, db=None, ws=None, wsb=0) == OK
+    # two fp32 rows of D per part, few parts for the widest rows
+    assert kda.layernorm_workspace_size(1 << 20, 128) == 2 * 1024 * 128 * 4
+    assert kda.layernorm_workspace_size(1 << 20, 8192) == 2 * 256 * 8192 * 4
+    assert kda.layernorm_workspace_size(1 << 20, 1 << 24) == 2 * (1 << 24) * 4
     assert kda.layernorm_workspace_size(-1, 5) == 0 and kda.layernorm_workspace_size(5, 0) == 0
 
 
@@ -151,6 +155,10 @@ def test_cache_refusals():
                     dict(L=1 << 40), dict(L=1 << 20, S=1 << 20, size=1 << 30)):
             assert go(**bad) == ESHAPE, (name, bad)
     assert call("kda_cache_compact", comp, table=fake(6) + 2) == EALIGN
+    for bad in (dict(dst=fork["src"]), dict(dst=fork["used"]), dict(src=fork["used"])):
+        assert call("kda_cache_fork", fork, **bad) == EVALUE, bad
+    for bad in (dict(remap=comp["used"]), dict(table=comp["used"]), dict(table=comp["remap"])):
+        assert call("kda_cache_compact", comp, **bad) == EVALUE, bad
     need = kda.lib().kda_cache_workspace_size(8)
     assert call("kda_cache_compact", comp, ws=None) == EWS and call("kda_cache_compact", comp, wsb=need - 1) == EWS
     assert call("kda_cache_compact", comp, ws=fake(7) + 16) == EALIGN
