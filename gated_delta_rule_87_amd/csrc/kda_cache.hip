@@ -131,7 +131,10 @@ template <typename U>
 __global__ __launch_bounds__(256) void kda_cache_copy_kernel(CachePool pool, size_t units, const int32_t* src,
                                                              const int32_t* dst, const int32_t* count, int64_t n,
                                                              bool zeros) {
-  if (count) n = *count;
+  if (count) {   // n is the most there can be (kept to if another call writes the workspace)
+    const int c = *count;
+    n = c < 0 ? 0 : c < n ? c : n;
+  }
   const int64_t pieces = (int64_t)((units + PIECE - 1) / PIECE);
   const int64_t items = n * pool.layers * pieces;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {

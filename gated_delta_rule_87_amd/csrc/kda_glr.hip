@@ -2,18 +2,21 @@
 // and backward (gfx950).
 //
 // The B * T packed tokens are cut into tiles of GLR_TILE tokens by 256 bytes of channels, one
-// workgroup each. A tile acts on
-// the state that enters it as an affine map h -> A h + L, with A = prod exp(g): the workgroup
-// loads its tile once into registers, reduces it to (A, L) per channel, publishes that,
-// obtains the state that enters it from the tiles before, and runs through its registers a
-// second time for the outputs. So every element is read once and written once, also for few
-// channels on long sequences, where one lane per channel would leave most of the GPU idle.
+// workgroup each. A tile acts on the state that enters it as an affine map h -> A h + L, with
+// A = prod exp(g): the workgroup loads its tile once into registers, reduces it to (A, L) per
+// channel, publishes that, obtains the state that enters it from the tiles before, and runs
+// through its registers a second time for the outputs. So every element is read once and
+// written once, also for few channels on long sequences, where one lane per channel would leave
+// most of the GPU idle (8192 x 8192 bf16 so: 3.59 ms forward). Bound by memory: at that size
+// forward 80 us alone in a row (5.0 TB/s), backward 138 us (4.8 TB/s).
 //
 // Inside a tile, 16 groups of 16 lanes hold R = 8 consecutive tokens each, 16 bytes a lane and
-// token (rows that are no whole vectors: at any address, the last elements in smaller pieces); their maps are
-// composed through shared memory. A sequence's first token sets the state instead of
-// continuing it: A = RESET (-1; an exp is never negative) marks a map that does not depend on
-// the state before, which is then not multiplied by zero but left out (it may be NaN).
+// token (rows that are no whole vectors: at any address, the last elements in smaller pieces);
+// their maps are composed through shared memory. 8 tokens of three tensors are 96 registers a
+// lane backward, as many as three workgroups a compute unit can hold. A sequence's first token
+// sets the state instead of continuing it: A = RESET (-1; an exp is never negative) marks a map
+// that does not depend on the state before, which is then not multiplied by zero but left out
+// (it may be NaN).
 //
 // Between tiles: every tile publishes its map; the last of BLOCK tiles also their composition,
 // the block's map, and the state that leaves the block. A tile takes the maps of the tiles
@@ -28,7 +31,10 @@
 //
 // Every wait ends: a workgroup takes its tile's number from a counter of its channels when it
 // starts, so all tiles that it waits for belong to workgroups that have started before it and
-// which themselves wait only for earlier ones; the first waits for none.
+// which themselves wait only for earlier ones; the first waits for none. Only another call in
+// the same workspace could break that; so a wait also ends, with NaN, after a number of polls
+// (seconds), and for all workgroups of its channels once it has ended so for one.
+#include <cstdlib>
 #include <type_traits>
 
 #include "kda_elem.h"
@@ -75,7 +81,8 @@ struct TileWs {
   uint64_t* maps;           // [tiles][D] (L, A) of each tile, by the order of processing
   uint64_t* block_maps;     // [blocks][D] of each whole block of BLOCK tiles
   uint32_t* block_states;   // [blocks][D] state entering each block
-  uint32_t* ticks;          // [channel tiles * TICK_STRIDE]
+  uint32_t* ticks;          // [channel tiles * TICK_STRIDE] next tile of the channels, whether a wait was given up
+  uint32_t polls;           // of a wait, at most
   float* stage;             // [nseq][D] initial states, where final_state overwrites them
   int32_t tiles, cols;
 };
@@ -93,8 +100,19 @@ __host__ __device__ inline int64_t glr_words(int64_t tiles, int64_t D) {
 // block, publishes the block's map and the state that leaves it; k: the tile's place in the
 // order of processing, c0 + ch: the lane's channel. Addresses are formed anew at every poll (t
 // is opaque): kept over the loops they cost 30 registers.
-__device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, int c0, uint32_t ch, float A, float L) {
+__device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, int c0, uint32_t ch, uint32_t* stop, float A,
+                                            float L) {
   auto row = [&](int i) { return (size_t)i * D + c0; };
+  uint32_t left = w.polls;
+  auto give_up = [&]() {   // after a poll that did not find everything
+    if (left == 0 || (left % 1024 == 0 && observe(stop) != 0)) {
+      publish(stop, 1u);
+      return true;
+    }
+    --left;
+    __builtin_amdgcn_s_sleep(1);
+    return false;
+  };
   const int b = k / BLOCK, j = k % BLOCK;
   const bool more = k + 1 < w.tiles, closes = more && j == BLOCK - 1;
   if (more && !closes) publish(w.maps + row(k) + ch, map_word(A, L));
@@ -110,7 +128,7 @@ __device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, i
     whole = true;
 #pragma unroll
     for (int i = 0; i < BLOCK - 1; ++i) whole = whole && m[i] != ~0ull;
-    if (!whole) __builtin_amdgcn_s_sleep(1);
+    if (!whole && give_up()) break;   // (a map that is not there is NaN)
   }
   float BA = 1.0f, BL = 0.0f;   // the block's map up to this tile
 #pragma unroll
@@ -147,8 +165,9 @@ __device__ __forceinline__ float pass_state(const TileWs& w, int k, int32_t D, i
         if (i > 0 && i <= at) S = apply(map_A(n[i]), map_L(n[i]), S);
       }
       found = true;
-    } else {
-      __builtin_amdgcn_s_sleep(1);
+    } else if (give_up()) {
+      S = __uint_as_float(0x7fc00000u);
+      found = true;
     }
   }
   if (closes && !(CA < 0.0f) && b > 0) publish(w.block_states + row(b + 1) + ch, word_of(apply(CA, CL, S)));
@@ -264,6 +283,7 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
   if (tid == 0) s_tile = take_tile(w, col);
   __syncthreads();
   const int tile = __builtin_amdgcn_readfirstlane(s_tile);
+  if ((uint32_t)tile >= (uint32_t)w.tiles) return;   // (another call in the same workspace)
   const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
   const int d = col * CH + lr * VEC;
   const int c = p.D - d < 0 ? 0 : p.D - d > VEC ? VEC : p.D - d;   // elements of this lane (EXACT: VEC or none)
@@ -332,7 +352,7 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
     float TA = 1.0f, TL = 0.0f;
 #pragma unroll 4
     for (int i = 0; i < GRP; ++i) compose(TA, TL, sA[i][tid], sL[i][tid]);
-    float h = pass_state(w, tile, p.D, col * CH, tid, TA, TL);
+    float h = pass_state(w, tile, p.D, col * CH, tid, w.ticks + col * TICK_STRIDE + 1, TA, TL);
     if (p.carry) p.carry[(size_t)tile * p.D + col * CH + tid] = h;
 #pragma unroll 4
     for (int i = 0; i < GRP; ++i) {   // the state that enters each group
@@ -389,6 +409,7 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   if (tid == 0) s_tile = take_tile(w, col);
   __syncthreads();
   const int k = __builtin_amdgcn_readfirstlane(s_tile), tile = w.tiles - 1 - k;
+  if ((uint32_t)k >= (uint32_t)w.tiles) return;   // (another call in the same workspace)
   const int t_base = tile * GLR_TILE, t0 = t_base + grp * R;
   const int d = col * CH + lr * VEC;
   const int n_el = p.D - d < 0 ? 0 : p.D - d > VEC ? VEC : p.D - d;   // elements of this lane (EXACT: VEC or none)
@@ -490,7 +511,7 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
 #pragma unroll 4
     for (int i = GRP - 1; i >= 0; --i) compose(TB, TM, sB[i][tid], sM[i][tid]);
     float h = p.carry[(size_t)tile * p.D + dc];
-    float E = pass_state(w, k, p.D, col * CH, tid, TB, TM);
+    float E = pass_state(w, k, p.D, col * CH, tid, w.ticks + col * TICK_STRIDE + 1, TB, TM);
 #pragma unroll 4
     for (int i = 0; i < GRP; ++i) {
       const float A = sA[i][tid], L = sL[i][tid];
@@ -725,6 +746,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 TileWs tile_ws(const GlrParams& p, void* workspace, bool stage) {
   TileWs w{};
   uint8_t* b = static_cast<uint8_t*>(workspace);
+  w.polls = 1u << 24;   // a poll takes a microsecond
+  if (const char* e = std::getenv("KDA_GLR_POLLS")) w.polls = (uint32_t)std::strtoul(e, nullptr, 10);
   w.tiles = tile_count(p.tokens);
   w.cols = tile_cols(p.dtype, p.D);
   const size_t words = (size_t)glr_words(w.tiles, p.D), blocks = (size_t)((w.tiles + BLOCK - 1) / BLOCK);

@@ -13,7 +13,7 @@ Inputs are the directories rocprofv3 wrote with --output-format csv:
   --sq           --pmc runs of SQ_* counters
 Writes one <kernel>__<workload>.md per kernel of the profiled call, the
 copy_calibration__1GiB.md table, and merges the per-launch HBM bytes into
-traffic.json, keyed by workload and by the hash of the kernel sources (bench.py
+traffic.json, keyed by workload and by the hash of the KDA kernels' sources (bench.py
 reports a measured "traffic" only while that hash matches).
 """
 import argparse
@@ -30,11 +30,16 @@ COPY_KERNEL = "__amd_rocclr_copyBuffer"
 GIB = 1 << 30
 
 
+# what the profiled kernels are built from (the operators beside kda_fwd have sources of their own)
+SOURCES = ("kda_api.cpp", "kda_api_util.h", "kda_chain.hip", "kda_device.h", "kda_internal.h", "kda_intra.hip",
+           "kda_noalloc.hip", "kda_recurrent.hip", "kda_scan.hip", "kda_sched.hip")
+
+
 def kernel_source_hash():
-    """Same hash as bench.py: every file under the package's csrc/."""
+    """Same hash as bench.py: every source of the KDA forward's kernels."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "gated_delta_rule_87_amd", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in SOURCES:
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

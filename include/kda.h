@@ -38,7 +38,8 @@
  *   - Other environment variables: KDA_LOG=1 prints each kda_fwd call's sizes
  *     and chain segment count to stderr; KDA_CHAIN_SEGMENTS=n caps the number
  *     of segments of the segment-parallel state chain (see
- *     kda_fwd_workspace_size; 1 keeps the plain chain).
+ *     kda_fwd_workspace_size; 1 keeps the plain chain); KDA_GLR_POLLS=n caps the
+ *     polls of a wait inside kda_glr_fwd and kda_glr_bwd (see there).
  */
 #ifndef KDA_H
 #define KDA_H
@@ -371,7 +372,11 @@ enum kda_dtype {
  *   workspace             caller-owned, kda_glr_workspace_size(B, T, D, N) bytes
  *                         (N = 0 without cu_seqlens) for either direction, 256-byte
  *                         aligned; contents need no initialisation and are clobbered
- * Outputs do not overlap inputs, except that final_state may be initial_state.
+ * Outputs do not overlap inputs, except that final_state may be initial_state. The
+ * workspace is one call's until that call's work is done: calls that overlap in it
+ * give unspecified results, NaN among them, after a wait of seconds (workgroups hand
+ * states to each other through it; a wait ends after KDA_GLR_POLLS polls of about a
+ * microsecond, by default 2^24).
  * Results do not depend on timing: the same call gives the same bits. cu_seqlens'
  * contents are the caller's precondition, as for kda_fwd (KDA_VALIDATE=1 checks).
  */

@@ -456,3 +456,21 @@ def test_refusals_of_the_wrappers():
     with pytest.raises(kda.KDAError) as e:
         kda.glr_fwd(x, g, y, workspace=torch.empty(16, dtype=torch.uint8, device=d))
     assert e.value.code == 6
+
+
+def test_waits_end(monkeypatch):
+    """With no polls allowed every wait ends at once: values that had to be waited for are NaN,
+    nothing else is written, and the next call is as ever."""
+    say("waits cut short")
+    c = Case(F, 192, lengths=[3000, 5, 2000], state=F, seed=16)
+    ref = c.run()
+    monkeypatch.setenv("KDA_GLR_POLLS", "0")
+    cut = c.run()
+    for k in ("y", "dx", "dg"):
+        v, r = cut[k], ref[k]
+        assert bool(((v == r) | torch.isnan(v)).all()), k
+    assert torch.equal(cut["y"][0, :128], ref["y"][0, :128]) and torch.equal(cut["dx"][0, -1], ref["dx"][0, -1])
+    monkeypatch.delenv("KDA_GLR_POLLS")
+    again = c.run()
+    for k in ref:
+        assert torch.equal(torch.nan_to_num(again[k]), torch.nan_to_num(ref[k])), k
