@@ -127,6 +127,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _check(name, t, dtype, shape, device):
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return   # as it is in nearly every call: what is wrong is found out below
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:

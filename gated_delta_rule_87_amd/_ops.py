@@ -50,11 +50,8 @@ def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
 
 
-def _like(name, t, dtype, shape, device):
-    """_check, its messages only where something is wrong (small calls wait for these lines)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        _kda._check(name, t, dtype, shape, device)
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _done(rc: int) -> None:
@@ -112,7 +109,7 @@ def _pool(pool):
 def _slots(name, t, dev, n=None):
     if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise ValueError(f"{name} must be a 1-D tensor")
-    _like(name, t, torch.int32, (t.numel() if n is None else n,), dev)
+    _kda._check(name, t, torch.int32, (t.numel() if n is None else n,), dev)
     return t.numel()
 
 
@@ -161,7 +158,7 @@ def cache_compact(pool, used, remap, table=None, workspace: Optional[torch.Tenso
     lib = _kda.lib()
     with _on(dev):
         ws = _space(workspace, lib.kda_cache_workspace_size(S), dev)
-        _done(lib.kda_cache_compact(pool.data_ptr(), L, S, size, used.data_ptr(), remap.data_ptr(), _kda._ptr(table), n,
+        _done(lib.kda_cache_compact(pool.data_ptr(), L, S, size, used.data_ptr(), remap.data_ptr(), _ptr(table), n,
                                     ws.data_ptr(), _bytes(ws), _stream(dev)))
 
 
@@ -178,11 +175,11 @@ def fwd_slots(q, k, v, g, beta, scale: float, out, A_log, dt_bias, lower_bound: 
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a 4-D tensor [slots, H, V, K]")
     S = state.shape[0]
-    _like("state", state, state.dtype, (S, H, V, K), dev)
+    _kda._check("state", state, state.dtype, (S, H, V, K), dev)
     n = N if cu_seqlens is not None else B
     _slots("in_slots", in_slots, dev, n)
     _slots("out_slots", out_slots, dev, n)
-    ptr = _kda._ptr
+    ptr = _ptr
     with _on(dev):
         _done(_kda.lib().kda_fwd_slots(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), float(scale), ptr(out), ptr(A_log),
                                        ptr(dt_bias), float(lower_bound), ptr(state), _kda._state_code(state), S,
@@ -201,14 +198,14 @@ def _glr_sizes(x, cu_seqlens, dev):
             raise ValueError("cu_seqlens requires B == 1")
         if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be int64 [N+1] with N >= 1")
-        _like("cu_seqlens", cu_seqlens, torch.int64, tuple(cu_seqlens.shape), dev)
+        _kda._check("cu_seqlens", cu_seqlens, torch.int64, tuple(cu_seqlens.shape), dev)
         N = cu_seqlens.numel() - 1
     return B, T, D, N
 
 
 def _state(name, t, shape, dev) -> int:
     if t is not None:
-        _like(name, t, t.dtype, shape, dev)
+        _kda._check(name, t, t.dtype, shape, dev)
     return _kda._state_code(t)
 
 
@@ -232,9 +229,9 @@ def glr_fwd(x, g, y, initial_state=None, final_state=None, cu_seqlens=None, carr
     dev = _gpu("x", x, 3)
     B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
     dt = _dtype("x", x)
-    _like("g", g, x.dtype, x.shape, dev)
-    _like("x", x, x.dtype, x.shape, dev)
-    _like("y", y, x.dtype, x.shape, dev)
+    _kda._check("g", g, x.dtype, x.shape, dev)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
     n = N if cu_seqlens is not None else B
     ic = _state("initial_state", initial_state, (n, D), dev)
     fc = _state("final_state", final_state, (n, D), dev)
@@ -242,8 +239,8 @@ def glr_fwd(x, g, y, initial_state=None, final_state=None, cu_seqlens=None, carr
         raise ValueError("initial_state and final_state must have the same dtype")
     lib = _kda.lib()
     if carry is not None:
-        _like("carry", carry, torch.float32, (lib.kda_glr_carry_rows(B, T), D), dev)
-    ptr = _kda._ptr
+        _kda._check("carry", carry, torch.float32, (lib.kda_glr_carry_rows(B, T), D), dev)
+    ptr = _ptr
     with _on(dev):
         ws = _space(workspace, lib.kda_glr_workspace_size(B, T, D, N), dev)
         _done(lib.kda_glr_fwd(ptr(x), ptr(g), ptr(y), dt, ptr(initial_state), ic, ptr(final_state), fc, ptr(carry),
@@ -259,14 +256,14 @@ def glr_bwd(x, g, dy, carry, dx, dg, initial_state=None, d_final=None, d_initial
     B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
     dt = _dtype("x", x)
     for name, t in (("x", x), ("g", g), ("dy", dy), ("dx", dx), ("dg", dg)):
-        _like(name, t, x.dtype, x.shape, dev)
+        _kda._check(name, t, x.dtype, x.shape, dev)
     lib = _kda.lib()
-    _like("carry", carry, torch.float32, (lib.kda_glr_carry_rows(B, T), D), dev)
+    _kda._check("carry", carry, torch.float32, (lib.kda_glr_carry_rows(B, T), D), dev)
     n = N if cu_seqlens is not None else B
     ic = _state("initial_state", initial_state, (n, D), dev)
     fc = _state("d_final", d_final, (n, D), dev)
     dc = _state("d_initial", d_initial, (n, D), dev)
-    ptr = _kda._ptr
+    ptr = _ptr
     with _on(dev):
         ws = _space(workspace, lib.kda_glr_workspace_size(B, T, D, N), dev)
         _done(lib.kda_glr_bwd(ptr(x), ptr(g), ptr(dy), dt, ptr(carry), ptr(initial_state), ic, ptr(d_final), fc, ptr(dx),
@@ -282,10 +279,10 @@ def glr_step(x, g, y, state, in_slots, out_slots) -> None:
     N, D = x.shape
     dt = _dtype("x", x)
     for name, t in (("x", x), ("g", g), ("y", y)):
-        _like(name, t, x.dtype, x.shape, dev)
+        _kda._check(name, t, x.dtype, x.shape, dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise ValueError("state must be a 2-D tensor [slots, D]")
-    _like("state", state, state.dtype, (state.shape[0], D), dev)
+    _kda._check("state", state, state.dtype, (state.shape[0], D), dev)
     _slots("in_slots", in_slots, dev, N)
     _slots("out_slots", out_slots, dev, N)
     with _on(dev):
@@ -309,7 +306,7 @@ def _vector(name, t, n, dev):
     if t is not None:
         if not isinstance(t, torch.Tensor) or t.numel() != n:
             raise ValueError(f"{name} must hold {n} elements")
-        _like(name, t, torch.float32, t.shape, dev)
+        _kda._check(name, t, torch.float32, t.shape, dev)
 
 
 def layernorm_workspace_size(M: int, D: int) -> int:
@@ -322,13 +319,13 @@ def layernorm_fwd(x, weight, bias, eps: float, y, mean=None, rstd=None) -> None:
     (which may be x); weight and bias fp32 [D] or None; each row's mean and 1 / sqrt(variance
     + eps) into ``mean`` and ``rstd`` (fp32, one per row) where given (kda_layernorm_fwd)."""
     dev, M, D, dt = _rows(x)
-    _like("x", x, x.dtype, x.shape, dev)
-    _like("y", y, x.dtype, x.shape, dev)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
     _vector("weight", weight, D, dev)
     _vector("bias", bias, D, dev)
     _vector("mean", mean, M, dev)
     _vector("rstd", rstd, M, dev)
-    ptr = _kda._ptr
+    ptr = _ptr
     with _on(dev):
         _done(_kda.lib().kda_layernorm_fwd(ptr(x), ptr(weight), ptr(bias), float(eps), ptr(y), dt, ptr(mean), ptr(rstd),
                                            M, D, _stream(dev)))
@@ -339,17 +336,17 @@ def layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight=None, d_bias=None,
     """Backward pass of layernorm_fwd from its ``mean`` and ``rstd``: ``dx`` like x (it may be
     dy or x, or None), ``d_weight`` and ``d_bias`` fp32 [D] or None (kda_layernorm_bwd)."""
     dev, M, D, dt = _rows(x)
-    _like("x", x, x.dtype, x.shape, dev)
-    _like("dy", dy, x.dtype, x.shape, dev)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("dy", dy, x.dtype, x.shape, dev)
     if dx is not None:
-        _like("dx", dx, x.dtype, x.shape, dev)
+        _kda._check("dx", dx, x.dtype, x.shape, dev)
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are required")
     for name, t, n in (("weight", weight, D), ("mean", mean, M), ("rstd", rstd, M), ("d_weight", d_weight, D),
                        ("d_bias", d_bias, D)):
         _vector(name, t, n, dev)
     lib = _kda.lib()
-    ptr = _kda._ptr
+    ptr = _ptr
     with _on(dev):
         ws = None
         if d_weight is not None or d_bias is not None:
