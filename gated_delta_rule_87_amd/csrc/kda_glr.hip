@@ -257,16 +257,14 @@ __global__ __launch_bounds__(256) void kda_glr_prep_kernel(GlrParams p, TileWs w
   for (int64_t i = i0; i < (words + 3) / 4; i += step) reinterpret_cast<u32x4*>(w.maps)[i] = ones;
   for (int64_t i = i0; i < (int64_t)w.cols * TICK_STRIDE; i += step) w.ticks[i] = 0;
   if (!w.stage && !p.cu && p.T > 0) return;
-  for (int n = blockIdx.x; n < p.nseq; n += gridDim.x) {
+  for (int64_t i = i0; i < (int64_t)p.nseq * p.D; i += step) {
+    const int n = (int)(i / p.D);
     const bool empty = p.cu ? bound_of(p.cu, n, p.T) >= bound_of(p.cu, n + 1, p.T) : p.T == 0;
     if (!w.stage && !empty) continue;
-    for (int d = threadIdx.x; d < p.D; d += 256) {
-      const size_t i = (size_t)n * p.D + d;
-      float h;
-      load_state<1>(from, from_dtype, i, &h);
-      if (w.stage) w.stage[i] = h;
-      if (empty) store_state<1>(p.fin, p.fin_dtype, i, &h);
-    }
+    float h;
+    load_state<1>(from, from_dtype, i, &h);
+    if (w.stage) w.stage[i] = h;
+    if (empty) store_state<1>(p.fin, p.fin_dtype, i, &h);
   }
 }
 
@@ -761,8 +759,8 @@ TileWs tile_ws(const GlrParams& p, void* workspace, bool stage) {
 }
 
 hipError_t launch_prep(const GlrParams& p, const TileWs& w, const void* from, int from_dtype, hipStream_t stream) {
-  const int64_t fill = ((glr_words(w.tiles, p.D) + 3) / 4 + 255) / 256, rows = w.stage || p.cu || p.T == 0 ? p.nseq : 0;
-  const int64_t blocks = fill > rows ? fill : rows;
+  const int64_t fill = (glr_words(w.tiles, p.D) + 3) / 4, rows = w.stage || p.cu || p.T == 0 ? (int64_t)p.nseq * p.D : 0;
+  const int64_t blocks = ((fill > rows ? fill : rows) + 255) / 256;
   hipLaunchKernelGGL(kda_glr_prep_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream, p, w, from,
                      from_dtype);
   return hipGetLastError();
