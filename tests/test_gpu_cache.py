@@ -295,3 +295,33 @@ def test_operators_together():
     kda.glr_step(gx, gg, gy, g_pool[0], slots, slots)
     v3, e3 = po.glr(gx.cpu(), gg.cpu(), [(i, i + 1) for i in range(4)], v2["final"][order])
     po.assert_near("step", gy, v3["y"], e3["y"] + e2["final"][order])
+
+
+def guarded(need):
+    """A workspace of exactly `need` bytes with a guard behind it."""
+    room = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=dev())
+    return room[:need], room[need:]
+
+
+@pytest.mark.parametrize("T,D", [(40, 8), (300, 129), (1000, 64), (1025, 7), (5000, 264)])
+def test_workspaces_are_not_overrun(T, D):
+    """Every operator inside a workspace of the size that it asks for, whatever was in it."""
+    say("workspaces of the exact size", T, D)
+    d = dev()
+    cu = torch.tensor([0, T // 3, T // 3, T], device=d)
+    x, g = torch.randn(1, T, D, device=d), -torch.rand(1, T, D, device=d)
+    y, dx, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    st, d0, carry = torch.randn(3, D, device=d), torch.empty(3, D, device=d), torch.empty(kda.glr_carry_shape(1, T, D), device=d)
+    ws, guard = guarded(kda.glr_workspace_size(1, T, D, 3))
+    kda.glr_fwd(x, g, y, initial_state=st, final_state=st, cu_seqlens=cu, carry=carry, workspace=ws)   # states staged there
+    assert (guard == 0x5A).all()
+    kda.glr_bwd(x, g, y, carry, dx, dg, d_initial=d0, cu_seqlens=cu, workspace=ws)
+    assert (guard == 0x5A).all()
+    mean, rstd, dw, db = (torch.ones(n, device=d) for n in (T, T, D, D))
+    ws, guard = guarded(kda.layernorm_workspace_size(T, D))
+    kda.layernorm_bwd(y[0], x[0], None, mean, rstd, dx[0], d_weight=dw, d_bias=db, workspace=ws)
+    assert (guard == 0x5A).all()
+    ws, guard = guarded(kda.lib().kda_cache_workspace_size(T))
+    pool, used, remap = torch.zeros(1, T, 4, device=d), ints([i % 2 for i in range(T)]), ints([0] * T)
+    kda.cache_compact(pool, used, remap, workspace=ws)
+    assert (guard == 0x5A).all()
