@@ -84,6 +84,7 @@ int64_t kda_glr_carry_rows(int64_t B, int64_t T) {
 
 size_t kda_glr_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N) {
   if (B < 1 || T < 0 || D < 1 || N < 0 || D > MAX_CHANNELS || T > INT32_MAX || B > INT32_MAX || N > INT32_MAX) return 0;
+  if (B * T >= (int64_t)INT32_MAX / 2 || !kda::glr_fits(B * T, D, N > 0 ? N : B)) return 0;
   return kda::glr_workspace(B * T, D, N > 0 ? N : B);
 }
 

@@ -380,7 +380,7 @@ enum kda_dtype {
  * Results do not depend on timing: the same call gives the same bits. cu_seqlens'
  * contents are the caller's precondition, as for kda_fwd (KDA_VALIDATE=1 checks).
  */
-int64_t kda_glr_carry_rows(int64_t B, int64_t T);
+int64_t kda_glr_carry_rows(int64_t B, int64_t T);   /* 0 for invalid sizes, as below */
 size_t kda_glr_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N);
 int kda_glr_fwd(const void *x, const void *g, void *y, int dtype, const void *initial_state, int initial_dtype,
                 void *final_state, int final_dtype, float *carry, const int64_t *cu_seqlens, int64_t N, int64_t B,

@@ -77,7 +77,8 @@ def test_glr_sizes():
     assert kda.glr_carry_shape(1, 8192, 64) == (64, 64) and kda.glr_carry_shape(3, 43, 5) == (2, 5)
     assert kda.glr_carry_shape(1, 0, 5) == (0, 5)
     assert kda.lib().kda_glr_carry_rows(0, 5) == 0 and kda.lib().kda_glr_carry_rows(1, -5) == 0
-    for bad in ((0, 10, 4), (1, -1, 4), (1, 10, 0)):
+    for bad in ((0, 10, 4), (1, -1, 4), (1, 10, 0), (1, 10, (1 << 22) + 1), (1 << 30, 1 << 30, 8), (1, 1 << 29, 1 << 20),
+                (1, 10, 64, 1 << 24)):
         assert kda.glr_workspace_size(*bad) == 0
 
 
