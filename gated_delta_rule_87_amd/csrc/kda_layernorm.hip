@@ -456,6 +456,7 @@ struct Shape {
 // more registers, so fewer at once.
 template <int DT, bool BWD, bool E, typename F>
 bool by_width_of(int32_t D, F f) {
+  constexpr bool FULL = BWD && !E && DT != FP32;   // 175 registers with two vectors (3001 bf16: 120 against 112 us)
   constexpr int V = vec_of<DT>(), MANY = E || !BWD || V == 4 ? 4 : 2;
   if (D <= 8 * V) f(Shape<E, 8, 1, MANY>{});
   else if (D <= 16 * V) f(Shape<E, 16, 1, MANY>{});
@@ -463,7 +464,7 @@ bool by_width_of(int32_t D, F f) {
   else if (D <= 64 * V) f(Shape<E, 64, 1, MANY>{});
   else if (D <= 128 * V) f(Shape<E, 64, 2, 2>{});
   else if (D <= 256 * V) f(Shape<E, 256, 1, MANY>{});
-  else if (D <= 512 * V) f(Shape<E, 256, 2, 2>{});
+  else if (D <= 512 * V) f(Shape<E, FULL ? 512 : 256, FULL ? 1 : 2, 2>{});
   else if (D <= 1024 * V) f(Shape<E, BWD ? 1024 : 512, BWD ? 1 : 2, BWD ? MANY : 2>{});
   else if (D <= 2048 * V) f(Shape<E, 1024, 2, BWD ? 1 : 2>{});
   else if constexpr (V == 4) {

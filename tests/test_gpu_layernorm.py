@@ -57,7 +57,7 @@ def check(x, dy, w, b, o, eps=EPS):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, F], ids=["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("D", [1, 2, 7, 8, 64, 100, 127, 128, 136, 256, 513, 1000, 1024, 2048, 4104, 8192, 12288, 16384, 20001, 40960])
+@pytest.mark.parametrize("D", [1, 2, 7, 8, 64, 100, 127, 128, 136, 256, 513, 1000, 1024, 2048, 4104, 8192, 12288, 16384, 20001, 40960, 1027, 2051, 4001, 6007, 13001])
 @pytest.mark.parametrize("M", [1, 5, 131])
 def test_sizes(dtype, D, M):
     say("layer norm", dtype, M, D)
