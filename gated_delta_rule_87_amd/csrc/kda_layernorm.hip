@@ -5,8 +5,11 @@
 // TB/s; 8192 rows of 8192: 87 us, 4.8 TB/s with its sums; both and 5 us for adding them). A row
 // is loaded once into the registers of LANES lanes (8 of a wave for the shortest rows, a
 // workgroup of 1024 for the widest), 16 bytes a lane and vector; statistics are two sums over
-// those registers (the mean, then the squares of the centred values: no cancellation for rows
-// far from zero). Workgroups take rows in strides and keep the weight, and in the backward pass
+// those registers: the mean, then the squares of the differences from it. That mean is off by
+// the sum's roundings, some u = 2^-24 of |x|, which is nothing beside a deviation of |mean| and
+// more, and too much in a row far from zero (one of 12345.678 throughout came out as -0.3 and
+// not 0). Such rows take a third sum, of the differences, which are exact there: its mean is
+// what the first one is off by. Workgroups take rows in strides and keep the weight, and in the backward pass
 // the sums of dy xhat and dy of their columns, in registers from row to row; each writes its
 // sums once to the workspace, and a second kernel adds those in a fixed order.
 //
@@ -46,14 +49,14 @@ __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 // Sums of K values over LANES lanes. Rows of several waves go through buf, one barrier a call:
-// consecutive calls take different halves of it.
+// consecutive calls take different parts of it.
 template <int LANES, int K>
-__device__ __forceinline__ void row_sums(float* v, float (*buf)[K], int half) {
+__device__ __forceinline__ void row_sums(float* v, float (*buf)[K], int part) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = lanes_sum<(LANES > 64 ? 64 : LANES)>(v[k]);
   if constexpr (LANES > 64) {
     constexpr int W = LANES / 64;
-    float (*b)[K] = buf + half * W;
+    float (*b)[K] = buf + part * W;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) b[threadIdx.x >> 6][k] = v[k];
@@ -87,11 +90,21 @@ constexpr int wg_of(int lanes) { return lanes > 256 ? lanes : 256; }
 
 // ---- forward ----------------------------------------------------------------------
 
+// A row whose mean is more than its deviation (squares: the mean of the squared differences
+// from it): only there can the roundings of the mean be more than those of what follows.
+__device__ __forceinline__ bool is_far(float mean, float squares) { return mean * mean > squares; }
+// The variance, from that and what the mean was off by, which is roundings only: nothing
+// cancels, but a row of one value may come out below zero.
+__device__ __forceinline__ float about_mean(float squares, float off) {
+  const float var = fmaf(-off, off, squares);
+  return var < 0.0f ? 0.0f : var;
+}
+
 // A lane holds NV vectors of a row, U rows at a time.
 template <int DT, bool EXACT, int LANES, int NV, int U>
 __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormParams p) {
   constexpr int VEC = vec_of<DT>(), G = wg_of(LANES) / LANES;
-  __shared__ float buf[LANES > 64 ? 2 * LANES / 64 : 1][U];
+  __shared__ float buf[LANES > 64 ? 3 * LANES / 64 : 1][U];
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
   const float inv = 1.0f / p.D;
   float w[NV][VEC], b[NV][VEC];
@@ -129,7 +142,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormPar
     row_sums<LANES, U>(s, buf, 0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      s[u] /= p.D;   // a division: the mean of a row of one value is that value, its centred values zero
+      s[u] /= p.D;
       q[u] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -143,38 +156,82 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_layernorm_fwd_kernel(NormPar
       }
     }
     row_sums<LANES, U>(q, buf, 1);
+    bool far = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t m = m0 + u * G + grp;
-      const float mean = s[u], rstd = 1.0f / sqrtf(q[u] * inv + p.eps);
-      if (m >= p.M) continue;
-      if (lane == 0) {
-        if (p.mean) p.mean[m] = mean;
-        if (p.rstd) p.rstd[m] = rstd;
+      q[u] *= inv;
+      far = far || is_far(s[u], q[u]);
+    }
+    auto outputs = [&](auto corrected, const float* off) {
+      constexpr bool CORRECTED = decltype(corrected)::value;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t m = m0 + u * G + grp;
+        const float mean = s[u], rstd = 1.0f / sqrtf(q[u] + p.eps);
+        if (m >= p.M) continue;
+        if (lane == 0) {
+          if (p.mean) p.mean[m] = CORRECTED ? mean + off[u] : mean;
+          if (p.rstd) p.rstd[m] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float f[VEC];
+          if (CORRECTED) x[u][i].opaque();
+          x[u][i].unpack(f);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float d = CORRECTED ? (f[e] - mean) - off[u] : f[e] - mean;
+            f[e] = fmaf(d * rstd, w[i][e], b[i][e]);
+          }
+          Pack<DT, VEC> y;
+          y.pack(f);
+          if (c[i] > 0) store_part<EXACT>(y, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+        }
       }
+    };
+    // Outputs of their own where no row is far: the differences from the mean are kept from the
+    // sum of their squares (3001 bf16: 48.1 us, 50.9 with one form for both; fp32 rows of whole
+    // vectors take a subtraction more and 20 registers fewer: 8192 wide 41.3 us, 43.4 with two).
+    constexpr bool TWO = DT != FP32 || !EXACT;
+    const bool any_far = __any(far);   // (of a row over several waves: the same in all of them)
+    if (TWO && !any_far) {
+      outputs(std::false_type{}, nullptr);
+      continue;
+    }
+    float off[U] = {};
+    if (any_far) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float f[VEC];
-        x[u][i].unpack(f);
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[i][e], b[i][e]);
-        Pack<DT, VEC> y;
-        y.pack(f);
-        if (c[i] > 0) store_part<EXACT>(y, p.out, (size_t)m * p.D + (i * LANES + lane) * VEC, c[i]);
+        for (int i = 0; i < NV; ++i) {
+          float f[VEC];
+          x[u][i].opaque();   // its elements are not kept for here (up to 30 registers)
+          x[u][i].unpack(f);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) off[u] += (EXACT ? c[i] > 0 : e < c[i]) ? f[e] - s[u] : 0.0f;
+        }
+      }
+      row_sums<LANES, U>(off, buf, 2);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {   // no row's result depends on the rows beside it
+        off[u] = is_far(s[u], q[u]) ? off[u] / p.D : 0.0f;
+        q[u] = about_mean(q[u], off[u]);
       }
     }
+    outputs(std::true_type{}, off);
   }
 }
 
-// Rows of more than 16384 elements: a workgroup reads a row three times.
+// Rows of more than 16384 elements: a workgroup reads a row three times, four where it is far
+// from zero.
 template <int DT>
 __global__ __launch_bounds__(1024) void kda_layernorm_fwd_long_kernel(NormParams p) {
   constexpr int VEC = vec_of<DT>();
-  __shared__ float buf[2 * 16][1];
+  __shared__ float buf[3 * 16][1];
   const float inv = 1.0f / p.D;
   for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
     const size_t row = (size_t)m * p.D;
-    float s = 0.0f, q = 0.0f;
+    float s = 0.0f, q = 0.0f, off = 0.0f;
     auto each = [&](auto f) {
       for (int64_t col = (int64_t)threadIdx.x * VEC; col < p.D; col += 1024 * VEC) {
         const int c = p.D - col < VEC ? (int)(p.D - col) : VEC;
@@ -197,9 +254,20 @@ __global__ __launch_bounds__(1024) void kda_layernorm_fwd_long_kernel(NormParams
         if (e < c) q = fmaf(v[e] - mean, v[e] - mean, q);
     });
     row_sums<1024, 1>(&q, buf, 1);
-    const float rstd = 1.0f / sqrtf(q * inv + p.eps);
+    q *= inv;
+    if (is_far(mean, q)) {
+      each([&](int, int c, const float* v) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e < c) off += v[e] - mean;
+      });
+      row_sums<1024, 1>(&off, buf, 2);
+      off /= p.D;
+      q = about_mean(q, off);
+    }
+    const float rstd = 1.0f / sqrtf(q + p.eps);
     if (threadIdx.x == 0) {
-      if (p.mean) p.mean[m] = mean;
+      if (p.mean) p.mean[m] = mean + off;
       if (p.rstd) p.rstd[m] = rstd;
     }
     each([&](int col, int c, const float* v) {
@@ -207,7 +275,7 @@ __global__ __launch_bounds__(1024) void kda_layernorm_fwd_long_kernel(NormParams
       load_param<VEC>(p.weight, col, c, 1.0f, w);
       load_param<VEC>(p.bias, col, c, 0.0f, b);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+      for (int e = 0; e < VEC; ++e) w[e] = fmaf(((v[e] - mean) - off) * rstd, w[e], b[e]);
       Pack<DT, VEC> y;
       y.pack(w);
       store_part<false>(y, p.out, row + col, c);

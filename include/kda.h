@@ -415,7 +415,9 @@ int kda_glr_step(const void *x, const void *g, void *y, int dtype, void *state, 
  *   weight, bias      fp32 [D], or NULL (ones, zeros)
  *   eps               finite, >= 0
  *   mean, rstd        fp32 [M]: written by kda_layernorm_fwd where not NULL, read
- *                     by kda_layernorm_bwd (needed there where M > 0)
+ *                     by kda_layernorm_bwd (needed there where M > 0). The forward
+ *                     pass centres rows beyond fp32's step of their mean; the
+ *                     backward pass takes mean and rstd as they are given, rounded.
  *   d_weight, d_bias  fp32 [D] or NULL, overwritten (zeros where M = 0). Their sums
  *                     have an order of their own that no timing changes.
  *   dx                may be NULL (only the weight's and bias's gradients are wanted)

@@ -242,3 +242,48 @@ def test_graph_replays():
         step(e)
         torch.cuda.synchronize()
         assert all(torch.equal(o[k], e[k]) for k in o), seed
+
+
+@pytest.mark.parametrize("value,D,dtype", [(v, D, F) for v in (0.1, 12345.678, 1e6 + 0.37, -3e-5) for D in (96, 100, 1000, 8192, 20001)]
+                         + [(201.0, 300001, BF)])
+def test_rows_of_one_value_give_the_bias(value, D, dtype):
+    """y of a row of one value is its bias to the bit, and the mean is that value, also where the
+    sum of D of them is rounded. The first mean is off by at most 31 roundings (a lane adds up
+    to 20 terms, ten levels of partial sums, the division; of the bf16 rows the 296 terms of a
+    lane add up exactly, below 2^24 of the value's last places), so by less than 62 half units
+    in the value's last place (22 for the bf16 rows). The differences from it are whole numbers
+    of those: their sums, below 62 * 20001 and 22 * 300001 and so below 2^24 of them, are exact,
+    so is their mean, and what is left of each difference is zero. rstd: the squares' mean and
+    the mean's square differ by at most 31 u of them."""
+    say("rows of", value, D, dtype)
+    x = torch.full((3, D), value).to(dtype)
+    _, dy, w, b = inputs(3, D, dtype, seed=11)
+    o = run(x, dy, w, b)
+    assert torch.equal(o["y"].cpu(), b.to(dtype).expand(3, D))
+    assert torch.equal(o["mean"].cpu(), x[:, 0].float())
+    off = 31 * po.U * abs(value)   # of the first mean
+    worst = 31 * po.U * off ** 2 / EPS
+    assert bool(((o["rstd"].cpu() / EPS ** -0.5 - 1).abs() <= worst + 8 * po.U).all())
+    assert torch.isfinite(o["dx"]).all()
+
+
+@pytest.mark.parametrize("D", [100, 1000, 8192, 20001])
+@pytest.mark.parametrize("offset", [1e4, -3e5])
+def test_rows_far_from_zero(offset, D):
+    """fp32 rows of deviation 1.5 around 1e4 and -3e5. x - m is exact beside any m within a
+    factor of two; a sum of D such terms takes at most 31 roundings (as above). So with xh the
+    exact normalised values: centred values are off by u of themselves and 33 u of their mean
+    absolute value, the variance by 36 u of itself and rstd by 22 u, and the products add 3:
+    28 u of |xh| and 33 u of its mean, times the weight, and 2 u of y's two terms."""
+    say("rows around", offset, D)
+    x, dy, w, b = inputs(9, D, F, seed=12, offset=offset)
+    o = run(x, dy, w, b)
+    f = torch.float64
+    c = x.to(f) - x.to(f).mean(1, keepdim=True)
+    rstd = (c.square().mean(1, keepdim=True) + EPS) ** -0.5
+    xh = c * rstd
+    u = po.U
+    bound = w.abs().to(f) * (28 * u * xh.abs() + 33 * u * xh.abs().mean(1, keepdim=True)) + 2 * u * ((xh * w).abs() + b.abs())
+    po.assert_near("y", o["y"], xh * w.to(f) + b.to(f), bound)
+    po.assert_near("mean", o["mean"], x.to(f).mean(1), 33 * u * c.abs().mean(1))
+    po.assert_near("rstd", o["rstd"], rstd[:, 0], 22 * u * rstd[:, 0])
