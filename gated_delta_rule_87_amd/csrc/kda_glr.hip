@@ -18,6 +18,13 @@
 // that does not depend on the state before, which is then not multiplied by zero but left out
 // (it may be NaN).
 //
+// A decay of zero is such a start as well: zero times an infinite or NaN state would be NaN.
+// (Gates below -87.4 have one: the instruction for 2^x gives zero below 2^-126.) Every other
+// decay is above zero, and so has to be every product of them, or an infinite state would become
+// NaN where tiles are joined: products are kept at FAINT, the smallest number, or above. Only
+// waves that find a zero among their decays, or among the products over 8 tokens, take the
+// paths that look at each decay.
+//
 // Between tiles: every tile publishes its map; the last of BLOCK tiles also their composition,
 // the block's map, and the state that leaves the block. A tile takes the maps of the tiles
 // before it in its block, and the state that enters the block: as published, or, looking back
@@ -58,13 +65,22 @@ struct Geom {
   static constexpr int CH = LR * VEC;              // channels of a tile
 };
 
+constexpr float FAINT = 0x1p-149f;
+
 __device__ __forceinline__ float decay(float g) { return fast_exp2(g * LOG2E); }
+// a h + x, for a decay of zero x alone
+__device__ __forceinline__ float follow(float a, float h, float x) { return a == 0.0f ? x : fmaf(a, h, x); }
 // the map (A, L) on a state
 __device__ __forceinline__ float apply(float A, float L, float h) { return A < 0.0f ? L : fmaf(A, h, L); }
+// the A of a map followed by the decay a >= 0, and by another map's (fmaxf drops a NaN, but then
+// L is NaN)
+__device__ __forceinline__ float lasting(float A, float a) {
+  return A < 0.0f || a == 0.0f ? RESET : fmaxf(A * a, FAINT);
+}
 // (A, L) followed by (a, l)
 __device__ __forceinline__ void compose(float& A, float& L, float a, float l) {
   L = apply(a, l, L);
-  A = a < 0.0f || A < 0.0f ? RESET : A * a;
+  A = a < 0.0f || A < 0.0f ? RESET : fmaxf(A * a, FAINT);
 }
 
 __device__ __forceinline__ uint32_t word_of(float f) { return f != f ? 0x7fc00000u : __float_as_uint(f); }
@@ -208,6 +224,38 @@ __device__ __forceinline__ Place place_of(const GlrParams& p, const int64_t* cu,
   return {n, t == b, t == e - 1};
 }
 
+// Whether one of a lane's gates is -87 or less (NaN of that sign too): its exp may be zero. Bits
+// of negative numbers grow with their size, so it is one maximum a word.
+template <int DT, int VEC>
+using Bits = std::conditional_t<DT == FP32, uint32_t, uint16_t> __attribute__((ext_vector_type(VEC)));
+template <int DT, int VEC>
+__device__ __forceinline__ bool any_low(const Pack<DT, VEC> (&g)[R]) {
+  Bits<DT, VEC> m = __builtin_bit_cast(Bits<DT, VEC>, g[0].r);
+#pragma unroll
+  for (int r = 1; r < R; ++r) m = __builtin_elementwise_max(m, __builtin_bit_cast(Bits<DT, VEC>, g[r].r));
+  return __builtin_reduce_max(m) >= (DT == FP32 ? 0xc2ae0000u : DT == BF16 ? 0xc2aeu : 0xd570u);
+}
+// Whether one of them is above zero (or a NaN of that sign)
+template <int DT, int VEC>
+__device__ __forceinline__ bool any_above(const Pack<DT, VEC> (&g)[R]) {
+  using Int = std::conditional_t<DT == FP32, int32_t, int16_t> __attribute__((ext_vector_type(VEC)));
+  Int m = __builtin_bit_cast(Int, g[0].r);
+#pragma unroll
+  for (int r = 1; r < R; ++r) m = __builtin_elementwise_max(m, __builtin_bit_cast(Int, g[r].r));
+  return __builtin_reduce_max(m) > 0;
+}
+// Values that sums of a run's 8, each multiplied by at most 1, may not stay finite with: of 2^120
+// and more, infinities and NaN
+__device__ __forceinline__ bool is_large(float f) { return !(fabsf(f) < 0x1p120f); }
+template <int DT, int VEC>
+__device__ __forceinline__ bool any_large(const Pack<DT, VEC> (&q)[R]) {
+  constexpr uint32_t SIZE = DT == FP32 ? 0x7fffffffu : 0x7fffu;
+  Bits<DT, VEC> m = {};
+#pragma unroll
+  for (int r = 0; r < R; ++r) m = __builtin_elementwise_max(m, __builtin_bit_cast(Bits<DT, VEC>, q[r].r) & (Bits<DT, VEC>)SIZE);
+  return __builtin_reduce_max(m) >= (DT == FP32 ? 0x7b800000u : DT == BF16 ? 0x7b80u : 0x7c00u);
+}
+
 // The sequences that a tile's tokens belong to, in shared memory: masks of tokens in a
 // sequence, first of one and last of one; numbers of the sequences of all tokens.
 struct TilePlaces {
@@ -309,40 +357,50 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
   const uint32_t all = (uint32_t)((1ull << R) - 1);
   const uint32_t in = (uint32_t)(places.in[word] >> bit) & all, first = (uint32_t)(places.first[word] >> bit) & all,
                  last = (uint32_t)(places.last[word] >> bit) & all;
-  const bool plain = in == all && first == 0;
+  // What a wave has to look out for: nothing (PLAIN), boundaries of sequences (ENDS), or those and
+  // decays of zero, or products of them (CARE).
+  enum { PLAIN, ENDS, CARE };
+  int mode = __all(in == all && first == 0) ? PLAIN : __any(any_low(g)) ? CARE : ENDS;
 
-  auto reduce = [&](auto plain_c, float* A, float* L) {
-    constexpr bool PLAIN = decltype(plain_c)::value;
+  auto reduce = [&](auto mode_c, float* A, float* L) {   // returns whether decays of this lane multiply to zero, or are NaN
+    constexpr int MODE = decltype(mode_c)::value;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) A[v] = 1.0f, L[v] = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (!PLAIN && !(in >> r & 1)) continue;
+      if (MODE != PLAIN && !(in >> r & 1)) continue;
       float gf[VEC], xf[VEC];
       g[r].unpack(gf);
       x[r].unpack(xf);
-      if (!PLAIN && (first >> r & 1)) {
+      if (MODE != PLAIN && (first >> r & 1)) {
         float h0[VEC] = {};
         if (c > 0) load_state_part<EXACT, VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h0);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-          L[v] = fmaf(decay(gf[v]), h0[v], xf[v]);
+          L[v] = follow(decay(gf[v]), h0[v], xf[v]);
           A[v] = RESET;
         }
       } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           const float a = decay(gf[v]);
-          L[v] = fmaf(a, L[v], xf[v]);
-          A[v] = PLAIN ? A[v] * a : (A[v] < 0.0f ? RESET : A[v] * a);
+          L[v] = MODE == CARE ? follow(a, L[v], xf[v]) : fmaf(a, L[v], xf[v]);
+          A[v] = MODE == CARE ? lasting(A[v], a) : MODE == ENDS && A[v] < 0.0f ? RESET : A[v] * a;
         }
       }
     }
+    bool zero = false;
+    if (MODE != CARE) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) zero = zero || !(MODE == ENDS ? A[v] != 0.0f : A[v] > 0.0f);
+    }
+    return zero;
   };
   {
     float A[VEC], L[VEC];
-    if (__all(plain)) reduce(std::true_type{}, A, L);
-    else reduce(std::false_type{}, A, L);
+    if (mode == PLAIN && __any(reduce(std::integral_constant<int, PLAIN>{}, A, L))) mode = CARE;
+    else if (mode == ENDS && __any(reduce(std::integral_constant<int, ENDS>{}, A, L))) mode = CARE;
+    if (mode == CARE) reduce(std::integral_constant<int, CARE>{}, A, L);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       sA[grp][lr * VEC + v] = A[v];
@@ -370,23 +428,30 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
     g[r].opaque();
     x[r].opaque();
   }
-  float h[VEC];
+  auto outputs = [&](auto mode_c) {
+    constexpr int MODE = decltype(mode_c)::value;
+    float h[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) h[v] = sL[grp][lr * VEC + v];
+    for (int v = 0; v < VEC; ++v) h[v] = sL[grp][lr * VEC + v];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (!(in >> r & 1)) continue;
-    float gf[VEC], xf[VEC];
-    g[r].unpack(gf);
-    x[r].unpack(xf);
-    if (first >> r & 1) load_state_part<EXACT, VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h);
+    for (int r = 0; r < R; ++r) {
+      if (MODE != PLAIN && !(in >> r & 1)) continue;
+      float gf[VEC], xf[VEC];
+      g[r].unpack(gf);
+      x[r].unpack(xf);
+      if (MODE != PLAIN && (first >> r & 1))
+        load_state_part<EXACT, VEC>(p.init, p.init_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
-    Pack<DT, VEC> y;
-    y.pack(h);
-    store_part<EXACT>(y, static_cast<uint8_t*>(p.y) + at(r) + off, c);
-    if (last >> r & 1) store_state_part<EXACT, VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h);
-  }
+      for (int v = 0; v < VEC; ++v)
+        h[v] = MODE == PLAIN ? fmaf(decay(gf[v]), h[v], xf[v]) : follow(decay(gf[v]), h[v], xf[v]);
+      Pack<DT, VEC> y;
+      y.pack(h);
+      store_part<EXACT>(y, static_cast<uint8_t*>(p.y) + at(r) + off, c);
+      if (last >> r & 1) store_state_part<EXACT, VEC>(p.fin, p.fin_dtype, (size_t)places.n[grp * R + r] * p.D + d, c, h);
+    }
+  };
+  if (mode == PLAIN) outputs(std::integral_constant<int, PLAIN>{});
+  else outputs(std::integral_constant<int, CARE>{});
 }
 
 // ---- backward ------------------------------------------------------------------------
@@ -436,14 +501,17 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   const uint32_t in = (uint32_t)(places.in[word] >> bit) & all, first = (uint32_t)(places.first[word] >> bit) & all,
                  last = (uint32_t)(places.last[word] >> bit) & all;
   // What a wave has to look out for among its lanes' runs of tokens: nothing (PLAIN), at most
-  // one first and one last token of a sequence in a run (ONE: chosen by selects), or MANY, also
-  // where tokens lie before or behind all sequences. (Rows behind the last token were not
-  // loaded: zeros, that is no decay, no input and no gradient.)
+  // one first and one last token of a sequence in a run (chosen by selects) and decays of zero,
+  // or products of them (ONE), or MANY, also where tokens lie before or behind all sequences.
+  // (Rows behind the last token were not loaded: zeros, that is no decay, no input and no
+  // gradient.) The outputs of ONE multiply by decays of zero, which gives the zero it has to be
+  // as long as everything is finite: waves where it might not be (odd) become MANY.
   enum { PLAIN, ONE, MANY };
   const int left = p.tokens - t0;
   const bool whole = in == (left >= R ? all : left <= 0 ? 0u : all >> (R - left));
-  const int mode = __all(whole && first == 0 && last == 0) ? PLAIN
-                   : __all(whole && (first & (first - 1)) == 0 && (last & (last - 1)) == 0) ? ONE : MANY;
+  int mode = !__all(whole && (first & (first - 1)) == 0 && (last & (last - 1)) == 0) ? MANY
+             : __all(first == 0 && last == 0) ? PLAIN : ONE;
+  bool low = false;   // ONE: whether there are decays of zero
   auto row = [&](int r) { return (size_t)places.n[grp * R + r] * p.D + d; };
   // a run's initial state and final gradient (ONE), elements c on
   auto ends = [&](int c, float* h0, float* e0) {
@@ -455,8 +523,9 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
       load_state_part<EXACT, NV>(p.dfin, p.dfin_dtype, (size_t)places.n[q + __builtin_ctz(last)] * p.D + d + c, n_el - c, e0);
   };
 
-  auto reduce = [&](auto mode_c) {
+  auto reduce = [&](auto mode_c) {   // returns PLAIN: whether decays of this lane multiply to zero, or are NaN; ONE: whether it is odd
     constexpr int MODE = decltype(mode_c)::value;
+    bool found = false;
 #pragma unroll
     for (int c = 0; c < VEC; c += NV) {
       __builtin_amdgcn_sched_barrier(0);   // one word after the other
@@ -466,7 +535,11 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         A[v] = B[v] = 1.0f;
         L[v] = M[v] = h0[v] = e0[v] = 0.0f;
       }
-      if (MODE == ONE) ends(c, h0, e0);
+      if (MODE == ONE) {
+        ends(c, h0, e0);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) found = found || is_large(h0[v]) || is_large(e0[v]);
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float xf[NV];
@@ -476,9 +549,16 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         if (MODE == MANY && start && n_el > c) load_state_part<EXACT, NV>(p.init, p.init_dtype, row(r) + c, n_el - c, h0);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          a[r][v] = used ? decay(a[r][v]) : 1.0f;   // a token of no sequence: no decay, no input, no gradient
-          L[v] = fmaf(a[r][v], start ? h0[v] : L[v], used ? xf[v] : 0.0f);
-          A[v] = start || (MODE != PLAIN && A[v] < 0.0f) ? RESET : A[v] * a[r][v];
+          const float before = start ? h0[v] : L[v];
+          if (MODE != PLAIN) {
+            a[r][v] = used ? decay(a[r][v]) : 1.0f;   // a token of no sequence: no decay, no input, no gradient
+            L[v] = follow(a[r][v], before, used ? xf[v] : 0.0f);
+            A[v] = start ? RESET : lasting(A[v], a[r][v]);
+          } else {
+            a[r][v] = decay(a[r][v]);
+            L[v] = fmaf(a[r][v], before, xf[v]);
+            A[v] *= a[r][v];
+          }
         }
       }
 #pragma unroll
@@ -489,9 +569,14 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         if (MODE == MANY && end && n_el > c) load_state_part<EXACT, NV>(p.dfin, p.dfin_dtype, row(r) + c, n_el - c, e0);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          M[v] = a[r][v] * ((used ? df[v] : 0.0f) + (end ? e0[v] : M[v]));
-          B[v] = end || (MODE != PLAIN && B[v] < 0.0f) ? RESET : B[v] * a[r][v];
+          const float G = (used ? df[v] : 0.0f) + (end ? e0[v] : M[v]);
+          M[v] = MODE != PLAIN && a[r][v] == 0.0f ? 0.0f : a[r][v] * G;
+          B[v] = MODE == PLAIN ? B[v] * a[r][v] : end ? RESET : lasting(B[v], a[r][v]);
         }
+      }
+      if (MODE == PLAIN) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) found = found || !(A[v] > 0.0f) || !(B[v] > 0.0f);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -502,10 +587,25 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         sM[grp][ch] = M[v];
       }
     }
+    return found;
   };
-  if (mode == PLAIN) reduce(std::integral_constant<int, PLAIN>{});
-  else if (mode == ONE) reduce(std::integral_constant<int, ONE>{});
-  else reduce(std::integral_constant<int, MANY>{});
+  if (mode == PLAIN && __any(reduce(std::integral_constant<int, PLAIN>{}))) mode = ONE;
+  if (mode != PLAIN) {
+    if (EXACT) {   // nothing is kept from the other form (56 registers; without whole vectors none)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        g[r].opaque();
+        x[r].opaque();
+        dy[r].opaque();
+      }
+    }
+    if (mode == MANY) {
+      reduce(std::integral_constant<int, MANY>{});
+    } else {
+      low = __any(any_low(g));
+      if (__any(reduce(std::integral_constant<int, ONE>{}) || any_above(g) || any_large(x) || any_large(dy)) && low) mode = MANY;
+    }
+  }
   __syncthreads();
   if (tid < CH && col * CH + tid < p.D) {
     const size_t dc = (size_t)col * CH + tid;
@@ -536,6 +636,12 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     dy[r].opaque();
   }
 
+  if (mode == ONE && low) {
+    bool odd = false;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) odd = odd || is_large(sL[grp][lr * VEC + v]) || is_large(sM[grp][lr * VEC + v]);
+    if (__any(odd)) mode = MANY;
+  }
   if (mode != MANY) {
 #pragma unroll
     for (int c = 0; c < VEC; c += NV) {
@@ -547,7 +653,7 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
         E[v] = sM[grp][lr * VEC + c + v];
         h0[v] = e0[v] = 0.0f;
       }
-      if (mode == ONE) ends(c, h0, e0);
+      if (mode != PLAIN) ends(c, h0, e0);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float xf[NV];
@@ -596,7 +702,9 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
   }
   // MANY: the tokens are read again (they are in the caches), a word at a time: with the packs
   // and every case of every token in registers at once, the kernel would need 242 of them and
-  // lose a third of its waves. Sequences of 8 tokens and more are never here.
+  // lose a third of its waves. A wave is here with all its 32 tokens if one of its runs of 8 has
+  // two first or two last tokens, a token of no sequence, or both a decay of zero and a value
+  // that is not finite.
   for (int c = 0; c < VEC && c < n_el; c += NV) {
     float a[R][NV], before[R][NV], h[NV], E[NV];
     int q = grp * R;
@@ -651,7 +759,7 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
       for (int v = 0; v < NV; ++v) {
         a[r][v] = decay(a[r][v]);
         before[r][v] = h[v];
-        h[v] = fmaf(a[r][v], h[v], xf[v]);
+        h[v] = follow(a[r][v], h[v], xf[v]);
       }
     }
 #pragma unroll
@@ -663,8 +771,8 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         df[v] += E[v];
-        E[v] = a[r][v] * df[v];
-        dg[v] = E[v] * before[r][v];
+        E[v] = a[r][v] == 0.0f ? 0.0f : a[r][v] * df[v];
+        dg[v] = a[r][v] == 0.0f ? 0.0f : E[v] * before[r][v];
       }
       write(p.dx, r, df);
       write(p.dg, r, dg);
@@ -715,7 +823,7 @@ __global__ __launch_bounds__(64) void kda_glr_tokens_kernel(GlrParams p, int col
       x[r].unpack(xf);
       if (p.carry && t % GLR_TILE == 0) store_f32<FP32, VEC>(p.carry, (size_t)(t / GLR_TILE) * p.D + d, h);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) h[v] = fmaf(decay(gf[v]), h[v], xf[v]);
+      for (int v = 0; v < VEC; ++v) h[v] = follow(decay(gf[v]), h[v], xf[v]);
       Pack<DT, VEC> y;
       y.pack(h);
       y.store(p.y, (size_t)t * p.D + d);

@@ -342,7 +342,10 @@ enum kda_dtype {
  * Per sequence and channel, from the state h of before its first token:
  *     h_t = exp(g_t) h_{t-1} + x_t,      y_t = h_t
  * g is the log-decay, as kda_fwd takes it with KDA_FUSE_GATE clear (not clamped
- * here): g <= 0 forgets, -inf starts over from x_t. Gates above 0 are taken as
+ * here): g <= 0 forgets. A gate whose exponential is below 2^-126 (g < -87.4: -inf
+ * and a type's lowest value among them) starts over from x_t, whatever state is
+ * before it, infinities and NaN too; no gradient passes it, and its own is 0. All
+ * others multiply: an infinite state stays infinite. Gates above 0 are taken as
  * they are; where their exponentials' product over 1024 tokens overflows fp32,
  * results are unspecified. The backward pass, with dy_t
  * and the final state's gradient d_final added at the last token:

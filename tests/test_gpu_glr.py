@@ -474,3 +474,100 @@ def test_waits_end(monkeypatch):
     again = c.run()
     for k in ref:
         assert torch.equal(torch.nan_to_num(again[k]), torch.nan_to_num(ref[k])), k
+
+
+@pytest.mark.parametrize("gate", [1.0, 40.0, 400.0], ids=["usual", "strong", "strongest"])
+@pytest.mark.parametrize("dtype", [F, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("kw", [dict(lengths=[5, 3000, 200]), dict(B=2, T=2500)], ids=["packed", "rows"])
+def test_infinite_states_stay_infinite(kw, dtype, gate):
+    """exp(g) of a gate from -87 on is above zero, however many are multiplied: an infinite state
+    stays so to its sequence's end, and an infinite gradient to its first token."""
+    say("infinite states", kw, dtype, gate)
+    c = Case(dtype, 24, state=F, seed=17, **kw)
+    c.g = (c.g.float() * gate).clamp(min=-87.0).to(dtype)
+    clean = c.run()
+    flat = lambda t: t.view(-1, 24)
+    b, e = c.sp[1]
+    flat(c.x)[b + 100, 3] = float("inf")
+    flat(c.x)[b + 1111, 4] = float("-inf")
+    c.h0[1, 5] = float("inf")
+    flat(c.dy)[e - 200, 9] = float("inf")
+    c.dhT[1, 10] = float("-inf")
+    out = c.run()
+    inf = float("inf")
+    y, dx = out["y"].view(-1, 24).cpu(), out["dx"].view(-1, 24).cpu()
+    assert (y[b + 100:e, 3] == inf).all() and (y[b + 1111:e, 4] == -inf).all() and (y[b:e, 5] == inf).all()
+    assert out["final"][1, 3:6].tolist() == [inf, -inf, inf]
+    assert (dx[b:e - 199, 9] == inf).all() and (dx[b:e, 10] == -inf).all()
+    assert out["d_initial"][1, 9:11].tolist() == [inf, -inf]
+    assert torch.equal(y[b:b + 100, 3], clean["y"].view(-1, 24)[b:b + 100, 3].cpu())
+    keep = [d for d in range(24) if d not in (3, 4, 5, 9, 10)]
+    for k in ("y", "dx", "dg"):
+        t, r = out[k].view(-1, 24).cpu(), clean[k].view(-1, 24).cpu()
+        assert torch.equal(t[:, keep], r[:, keep]) and torch.equal(t[:b], r[:b]) and torch.equal(t[e:], r[e:]), k
+    # h_{t-1} is infinite and nothing that multiplies it is zero
+    grad, h = out["dg"].view(-1, 24).cpu(), clean["dx"].view(-1, 24).cpu()
+    some = h[b + 101:e, 3].float().abs() > 1e-30
+    if gate == 1.0:
+        assert torch.isinf(grad[b + 101:e, 3][some]).all()
+
+
+@pytest.mark.parametrize("low", ["-inf", "lowest", "-88"])
+@pytest.mark.parametrize("dtype", [F, BF, HF], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("kw", [dict(lengths=[900, 40]), dict(lengths=[512, 30, 300]), dict(B=2, T=470), dict(B=1, T=30),
+                                dict(lengths=[2, 1, 1, 1, 1, 2, 1])], ids=["packed", "tile", "rows", "few", "tokens"])
+@pytest.mark.parametrize("D", [40, 41])
+def test_starting_over_forgets_nan_and_infinities(D, kw, dtype, low):
+    """A gate whose exponential is below 2^-126 (-87.4 and less, a type's lowest value and -inf
+    among them) starts over from x_t whatever the state before it was, and no gradient passes it:
+    the tokens after it, the gradients of those before it, and the initial state's, have the
+    bits of a clean run."""
+    say("starting over", D, kw, dtype, low)
+    low = {"-inf": float("-inf"), "lowest": torch.finfo(dtype).min, "-88": -88.0}[low]
+    c = Case(dtype, D, state=F, seed=18, **kw)
+    where = []
+    for b, e in c.sp:
+        where.append(sorted({b, b + (e - b) // 2, e - 1}) if e - b > 2 else [e - 1])
+    for ts in where:
+        for t in ts:
+            c.g.view(-1, D)[t] = low
+    clean = c.run()
+    c.h0[:, 1::3] = float("nan")
+    c.h0[:, 2::6] = float("inf")
+    for (b, e), ts in zip(c.sp, where):
+        if e - b > 8:   # garbage between the gates
+            c.x.view(-1, D)[ts[1] - 3, ::3] = float("nan")
+            c.x.view(-1, D)[ts[2] - 3, 1::3] = float("-inf")
+            c.dy.view(-1, D)[ts[1] + 2, ::2] = float("nan")
+            c.dy.view(-1, D)[ts[2] - 1, 1::2] = float("inf")
+    out = c.run()
+    v = {k: t.reshape(-1, D).cpu() for k, t in out.items()}
+    r = {k: t.reshape(-1, D).cpu() for k, t in clean.items()}
+    for i, ((b, e), ts) in enumerate(zip(c.sp, where)):
+        assert torch.equal(v["final"][i], r["final"][i])
+        if ts[0] == b:
+            assert (v["d_initial"][i] == 0).all()
+        for t in ts:
+            assert (v["dg"][t] == 0).all()
+            assert torch.equal(v["y"][t], r["y"][t])
+        if e - b > 8:
+            half = ts[1]
+            assert torch.equal(v["y"][half:ts[2] - 3], r["y"][half:ts[2] - 3])
+            assert torch.equal(v["dx"][b:half], r["dx"][b:half])
+            assert torch.equal(v["dg"][half + 1:ts[2] - 3].isnan(), v["dx"][half + 1:ts[2] - 3].isnan())
+            assert v["y"][half - 3:half, ::3].isnan().all() and torch.isfinite(v["y"][half:ts[2] - 3]).all()
+            assert v["dx"][half:half + 3, ::2].isnan().all()
+
+
+def test_step_starts_over():
+    say("a step that starts over")
+    d = dev()
+    pool = torch.full((3, 16), float("nan"), device=d)
+    x, g = torch.randn(3, 16, device=d), torch.full((3, 16), float("-inf"), device=d)
+    y = torch.empty_like(x)
+    i = torch.arange(3, dtype=torch.int32, device=d)
+    kda.glr_step(x, g, y, pool, i, i)
+    assert torch.equal(y, x) and torch.equal(pool, x)
+    pool.fill_(float("inf"))
+    kda.glr_step(x, torch.full_like(x, -87.0), y, pool, i, i)
+    assert (y == float("inf")).all()
