@@ -35,6 +35,16 @@ bool any_unaligned(std::initializer_list<const void*> ps, size_t a) {
   return false;
 }
 
+// Whether a state of the recurrence is where the kernels can take it: an element at a time where
+// rows are no whole vectors of the token tensors (layers of a cache begin anywhere then), else as
+// many elements as such a vector holds.
+bool state_unaligned(const void* p, int state_dtype, int dtype, int64_t D) {
+  if (!p) return false;
+  const int64_t vec = dtype == KDA_FP32 ? 4 : 8;
+  const size_t elem = state_dtype == KDA_STATE_FP32 ? 4 : 2, all = (size_t)vec * elem;
+  return !aligned(p, D % vec != 0 ? elem : all < 16 ? all : 16);
+}
+
 // Checks that both directions of the recurrence share; a, b, c are its token tensors.
 int check_glr(const void* a, const void* b, const void* c, int dtype, const int64_t* cu, int64_t N, int64_t B, int64_t T,
               int64_t D) {
@@ -96,7 +106,9 @@ int kda_glr_fwd(const void* x, const void* g, void* y, int dtype, const void* in
   if (rc == KDA_OK) rc = check_state(final_state, final_dtype);
   if (rc != KDA_OK) return rc;
   if (initial_state && final_state && initial_dtype != final_dtype) return KDA_ERR_DTYPE;
-  if (any_unaligned({x, g, y, initial_state, final_state, carry}, 16) || any_unaligned({cu_seqlens}, 8)) return KDA_ERR_ALIGN;
+  if (any_unaligned({x, g, y, carry}, 16) || any_unaligned({cu_seqlens}, 8) ||
+      state_unaligned(initial_state, initial_dtype, dtype, D) || state_unaligned(final_state, final_dtype, dtype, D))
+    return KDA_ERR_ALIGN;
   if (!workspace || workspace_bytes < kda_glr_workspace_size(B, T, D, cu_seqlens ? N : 0)) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -123,7 +135,9 @@ int kda_glr_bwd(const void* x, const void* g, const void* dy, int dtype, const f
   if (rc == KDA_OK) rc = check_state(d_initial, d_initial_dtype);
   if (rc != KDA_OK) return rc;
   if (d_initial && (d_initial == d_final || d_initial == initial_state)) return KDA_ERR_VALUE;
-  if (any_unaligned({x, g, dy, carry, initial_state, d_final, dx, dg, d_initial}, 16) || any_unaligned({cu_seqlens}, 8))
+  if (any_unaligned({x, g, dy, carry, dx, dg}, 16) || any_unaligned({cu_seqlens}, 8) ||
+      state_unaligned(initial_state, initial_dtype, dtype, D) || state_unaligned(d_final, d_final_dtype, dtype, D) ||
+      state_unaligned(d_initial, d_initial_dtype, dtype, D))
     return KDA_ERR_ALIGN;
   if (!workspace || workspace_bytes < kda_glr_workspace_size(B, T, D, cu_seqlens ? N : 0)) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, kda::ALIGN)) return KDA_ERR_ALIGN;
@@ -149,7 +163,8 @@ int kda_glr_step(const void* x, const void* g, void* y, int dtype, void* state, 
   if (N < 0 || N > INT32_MAX || D < 1 || D > MAX_CHANNELS || S < 1 || S > MAX_SLOTS || !kda::glr_fits(0, D, N)) return KDA_ERR_SHAPE;
   if (!state || (N != 0 && (!x || !g || !y || !in_slots || !out_slots))) return KDA_ERR_NULL;
   if (bad_dtype(dtype) || (state_dtype != KDA_STATE_BF16 && state_dtype != KDA_STATE_FP32)) return KDA_ERR_DTYPE;
-  if (any_unaligned({x, g, y, state}, 16) || any_unaligned({in_slots, out_slots}, 4)) return KDA_ERR_ALIGN;
+  if (any_unaligned({x, g, y}, 16) || any_unaligned({in_slots, out_slots}, 4) || state_unaligned(state, state_dtype, dtype, D))
+    return KDA_ERR_ALIGN;
   kda::GlrParams p = glr_params(x, g, dtype, state, state_dtype, nullptr, 0, N, 1, D);
   p.y = y;
   p.fin = state;

@@ -23,7 +23,8 @@
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers (hipMalloc'd or from a caching
  *     allocator), row-major and contiguous, aligned to 16 bytes (the state
- *     and fp32 parameters to 16 bytes as well).
+ *     and fp32 parameters to 16 bytes as well; index arrays to their elements;
+ *     states of the gated linear recurrence as said there).
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).
  *     Calls are stream-ordered and asynchronous: they return as soon as the
  *     work is enqueued. The library allocates nothing per call and keeps no
@@ -64,7 +65,7 @@ enum kda_status {
                               scale not finite, eps negative or not finite, unknown
                               flag bits, one buffer given twice where that is ruled
                               out, bad cu_seqlens contents (KDA_VALIDATE=1)         */
-    KDA_ERR_ALIGN = 5,     /* a pointer is not 16-byte aligned                      */
+    KDA_ERR_ALIGN = 5,     /* a pointer is not aligned as its argument has to be    */
     KDA_ERR_WORKSPACE = 6, /* workspace NULL or too small (kda_fwd_workspace_min, or the
                               operator's own kda_*_workspace_size)                  */
     KDA_ERR_HIP = 7,       /* a HIP runtime call or kernel launch failed            */
@@ -358,7 +359,11 @@ enum kda_dtype {
  *   D                     channels, 1 <= D <= 2^22, any number (whole multiples
  *                         of 16 bytes are fastest)
  *   initial_state, final_state, their dtypes, cu_seqlens, N, B, T
- *                         as for kda_fwd, with states [B|N, D]. Tokens of a packed
+ *                         as for kda_fwd, with states [B|N, D]. A state is aligned
+ *                         to as many of its elements as 16 bytes of x hold (at most
+ *                         to 16 bytes) where D is a multiple of that number, else to
+ *                         its element: as every layer of a cache [L, S, D] is.
+ *                         d_final and d_initial likewise. Tokens of a packed
  *                         batch that no sequence covers are not used, and their
  *                         outputs are left as they were.
  *   carry                 fp32 [kda_glr_carry_rows(B, T), D]: the state that enters
@@ -397,7 +402,7 @@ int kda_glr_bwd(const void *x, const void *g, const void *dy, int dtype, const f
  * kda_glr_step -- one token for each of N sequences, the states in the slots of a
  * cache's layer [S, D] (bf16/fp32): y[n] = exp(g[n]) state[in_slots[n]] + x[n], left
  * in slot out_slots[n]. x, g, y are [N, D] in `dtype`; the rules for slots are
- * kda_fwd_slots'. N >= 0.
+ * kda_fwd_slots', the state's alignment kda_glr_fwd's. N >= 0.
  */
 int kda_glr_step(const void *x, const void *g, void *y, int dtype, void *state, int state_dtype, int64_t S,
                  const int32_t *in_slots, const int32_t *out_slots, int64_t N, int64_t D, void *stream);

@@ -325,3 +325,41 @@ def test_workspaces_are_not_overrun(T, D):
     pool, used, remap = torch.zeros(1, T, 4, device=d), ints([i % 2 for i in range(T)]), ints([0] * T)
     kda.cache_compact(pool, used, remap, workspace=ws)
     assert (guard == 0x5A).all()
+
+
+@pytest.mark.parametrize("state", [F, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("dtype", [F, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("L,S,D", [(2, 3, 129), (3, 5, 7), (3, 3, 4), (2, 1, 1), (2, 7, 12)])
+def test_every_layer_of_a_cache(dtype, state, L, S, D):
+    """Layers of a pool [L, S, D] begin at any multiple of their element: steps, and states
+    passed to and from the recurrence, on each of them as on a copy."""
+    say("layers of odd widths", dtype, state, L, S, D)
+    gen = torch.Generator().manual_seed(D)
+    d = dev()
+    pool = torch.randn(L, S, D, generator=gen).to(state).to(d)
+    n = max(1, S // 2)
+    src, dst = (torch.arange(k, k + n, dtype=torch.int32, device=d) for k in (0, S - n))
+    for layer in range(L):
+        x, g = torch.randn(n, D, generator=gen).to(dtype).to(d), -torch.rand(n, D, generator=gen).to(dtype).to(d)
+        y, y2 = torch.empty_like(x), torch.empty_like(x)
+        want = pool.clone()
+        copy = pool[layer].clone()
+        kda.glr_step(x, g, y2, copy, src, dst)
+        want[layer] = copy
+        kda.glr_step(x, g, y, pool[layer], src, dst)
+        assert torch.equal(y, y2) and torch.equal(pool, want), layer
+    for T in (20, 300):
+        x, g = torch.randn(S, T, D, generator=gen).to(dtype).to(d), -torch.rand(S, T, D, generator=gen).to(dtype).to(d)
+        for layer in range(1, L):
+            fin, other = torch.zeros_like(pool), torch.zeros_like(pool)
+            grad, g0 = torch.zeros_like(pool), [torch.empty(S, D, dtype=state, device=d) for _ in range(2)]
+            outs = []
+            for h0, f, dh, d0 in ((pool[layer], fin[layer], pool[layer - 1], grad[layer]),
+                                  (pool[layer].clone(), g0[0], pool[layer - 1].clone(), g0[1])):
+                y, dx, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+                carry = torch.empty(kda.glr_carry_shape(S, T, D), device=d)
+                kda.glr_fwd(x, g, y, initial_state=h0, final_state=f, carry=carry)
+                kda.glr_bwd(x, g, x, carry, dx, dg, initial_state=h0, d_final=dh, d_initial=d0)
+                outs.append((y, dx, dg, f, d0))
+            assert all(torch.equal(a, b) for a, b in zip(*outs)), (T, layer)
+            assert not fin[layer - 1].any() and not grad[layer - 1].any()

@@ -192,3 +192,17 @@ def test_no_operator_kernel_uses_scratch(tmp_path):
         spills = [int(v) for v in re.findall(r"\.vgpr_spill_count:\s+(\d+)", text)]
         priv = [int(v) for v in re.findall(r"\.private_segment_fixed_size:\s+(\d+)", text)]
         assert spills and not any(spills) and not any(priv), (src, spills, priv)
+
+
+def test_states_of_a_cache_layer_are_accepted():
+    """A state begins where a layer of a cache [L, S, D] can: at any element where rows are no
+    whole vectors, at a vector's elements (8 bytes of bf16 beside fp32 tokens) where they are."""
+    for dtype, sd, D, unit in ((2, 2, 129, 4), (1, 1, 129, 2), (1, 2, 12, 4), (3, 1, 100, 2), (2, 1, 7, 2), (2, 1, 12, 8),
+                               (2, 2, 12, 16), (1, 1, 64, 16), (1, 2, 64, 16)):
+        go = lambda off: call("kda_glr_step", STEP, dtype=dtype, sd=sd, D=D, N=0, state=fake(4) + off)   # N = 0: no launch
+        assert go(unit) == OK and go(unit // 2) == EALIGN, (dtype, sd, D)
+        for name, d, states in (("kda_glr_fwd", GLR_F, (("h0", "h0d"), ("hT", "hTd"))),
+                                ("kda_glr_bwd", GLR_B, (("h0", "h0d"), ("df", "dfd"), ("d0", "d0d")))):
+            for p, c in states:
+                go = lambda off: call(name, d, dtype=dtype, D=D, ws=None, **{p: fake(8) + off, c: sd})   # refused after it
+                assert go(unit) == EWS and go(unit // 2) == EALIGN, (name, p, dtype, sd, D)
