@@ -853,11 +853,22 @@ int32_t tile_cols(int dt, int32_t D) {
 }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Polls of a wait at most: a poll takes a microsecond. KDA_GLR_POLLS where it is a whole number
+// (above 32 bits: the most there can be); any other text leaves it as it is.
+uint32_t polls_of_a_wait() {
+  constexpr uint32_t MOST = 1u << 24;
+  const char* e = std::getenv("KDA_GLR_POLLS");
+  if (!e || *e < '0' || *e > '9') return MOST;
+  char* end = nullptr;
+  const unsigned long long v = std::strtoull(e, &end, 10);
+  if (*end != '\0') return MOST;
+  return v < UINT32_MAX ? (uint32_t)v : UINT32_MAX;
+}
+
 TileWs tile_ws(const GlrParams& p, void* workspace, bool stage) {
   TileWs w{};
   uint8_t* b = static_cast<uint8_t*>(workspace);
-  w.polls = 1u << 24;   // a poll takes a microsecond
-  if (const char* e = std::getenv("KDA_GLR_POLLS")) w.polls = (uint32_t)std::strtoul(e, nullptr, 10);
+  w.polls = polls_of_a_wait();
   w.tiles = tile_count(p.tokens);
   w.cols = tile_cols(p.dtype, p.D);
   const size_t words = (size_t)glr_words(w.tiles, p.D), blocks = (size_t)((w.tiles + BLOCK - 1) / BLOCK);

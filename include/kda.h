@@ -39,8 +39,9 @@
  *   - Other environment variables: KDA_LOG=1 prints each kda_fwd call's sizes
  *     and chain segment count to stderr; KDA_CHAIN_SEGMENTS=n caps the number
  *     of segments of the segment-parallel state chain (see
- *     kda_fwd_workspace_size; 1 keeps the plain chain); KDA_GLR_POLLS=n caps the
- *     polls of a wait inside kda_glr_fwd and kda_glr_bwd (see there).
+ *     kda_fwd_workspace_size; 1 keeps the plain chain); KDA_GLR_POLLS=n (a whole
+ *     number, else ignored) caps the polls of a wait inside kda_glr_fwd and
+ *     kda_glr_bwd (see there).
  */
 #ifndef KDA_H
 #define KDA_H

@@ -571,3 +571,16 @@ def test_step_starts_over():
     pool.fill_(float("inf"))
     kda.glr_step(x, torch.full_like(x, -87.0), y, pool, i, i)
     assert (y == float("inf")).all()
+
+
+@pytest.mark.parametrize("value", ["", "many", "12x", "-1", "4294967296", "99999999999999999999999"])
+def test_a_cap_on_polls_that_is_no_number(monkeypatch, value):
+    """KDA_GLR_POLLS that is not a whole number is not set, and one past 32 bits is the most
+    there can be: waits go on."""
+    say("KDA_GLR_POLLS", repr(value))
+    c = Case(F, 192, lengths=[3000, 5, 2000], state=F, seed=16)
+    ref = c.run()
+    monkeypatch.setenv("KDA_GLR_POLLS", value)
+    out = c.run()
+    for k in ("y", "final", "dx", "dg", "d_initial"):
+        assert torch.equal(out[k], ref[k]), k
