@@ -891,9 +891,15 @@ hipError_t launch_prep(const GlrParams& p, const TileWs& w, const void* from, in
 
 // Few tokens per sequence: rows of at most FEW tokens (8192 channels bf16: 16 tokens 4.8 us
 // against 8.1 in tiles, 32 the same, 64 13.0 against 7.5), packed batches of at most 2 on average
-// (256 tokens 5.4 against 19.9 us; the lengths stay on the device, as with kda_fwd's own rule).
-constexpr int32_t FEW = 32;
-bool few_tokens(const GlrParams& p) { return p.cu ? p.T <= 2 * (int64_t)p.nseq : p.T <= FEW; }
+// (1024 channels, 512 tokens of a sequence each 4.3 against 19.7 us). Their lengths stay on the
+// device, and the tokens of a long sequence among them are walked one after the other, 0.21 us
+// each, which tiles would not do: of 512 tokens half in one sequence 53 against 18 us, all 102
+// against 13; of 8192 870 against 35 and 1727 against 30. So not beyond FEW_PACKED tokens, where
+// what the even batch gains is about what the uneven one loses.
+constexpr int32_t FEW = 32, FEW_PACKED = 512;
+bool few_tokens(const GlrParams& p) {
+  return p.cu ? p.T <= FEW_PACKED && p.T <= 2 * (int64_t)p.nseq : p.T <= FEW;
+}
 // One tile, and nothing to do before it: no counters, no words to fill.
 bool lone_tile(const GlrParams& p, const TileWs& w) { return w.tiles == 1 && !p.cu && !w.stage; }
 
