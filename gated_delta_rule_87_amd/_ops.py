@@ -1,7 +1,10 @@
 """Python binding of the operators beside kda_fwd: caches of states in slots, the gated
 linear recurrence, layer norm (include/kda.h). Argument marshalling only, as in the
 package's __init__: outputs are the caller's tensors, written in place; contiguous GPU
-tensors of one device; work goes to that device's current stream."""
+tensors of one device; work goes to that device's current stream. Autograd records none of
+it, whatever requires a gradient: gradients come from the calls named _bwd, for instance
+inside a torch.autograd.Function. What a call has written counts as changed in place (its
+version goes up), so that autograd does not use it for what it was."""
 from __future__ import annotations
 
 import contextlib
@@ -17,6 +20,7 @@ _DTYPES = {torch.bfloat16: 1, torch.float32: 2, torch.float16: 3}
 _NULL = contextlib.nullcontext()
 # the current stream's handle without a Stream object (2 us less on every call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_changed = torch.autograd.graph.increment_version
 
 
 def _setup(L):
@@ -54,9 +58,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _done(rc: int) -> None:
+def _done(rc: int, *written) -> None:
+    """Raises for a status other than 0; the tensors written (or None) count as changed in place."""
     if rc != 0:
         raise _kda.KDAError(rc, _kda.status_string(rc))
+    _changed([t for t in written if t is not None])
 
 
 def _gpu(name, t, dim=None) -> torch.device:
@@ -107,10 +113,12 @@ def _pool(pool):
 
 
 def _slots(name, t, dev, n=None):
-    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+    if not isinstance(t, torch.Tensor) or (n is None and t.dim() != 1):
         raise ValueError(f"{name} must be a 1-D tensor")
-    _kda._check(name, t, torch.int32, (t.numel() if n is None else n,), dev)
-    return t.numel()
+    if n is None:
+        n = t.numel()
+    _kda._check(name, t, torch.int32, (n,), dev)
+    return n
 
 
 def cache_copy(pool, src, dst) -> None:
@@ -121,7 +129,7 @@ def cache_copy(pool, src, dst) -> None:
     _slots("dst", dst, dev, n)
     with _on(dev):
         _done(_kda.lib().kda_cache_copy(pool.data_ptr(), L, S, size, src.data_ptr(), dst.data_ptr(), n,
-                                        _stream(dev)))
+                                        _stream(dev)), pool)
 
 
 def cache_fork(pool, used, src, dst) -> None:
@@ -134,7 +142,7 @@ def cache_fork(pool, used, src, dst) -> None:
     _slots("dst", dst, dev, n)
     with _on(dev):
         _done(_kda.lib().kda_cache_fork(pool.data_ptr(), L, S, size, used.data_ptr(), src.data_ptr(), dst.data_ptr(),
-                                        n, _stream(dev)))
+                                        n, _stream(dev)), pool, used, dst)
 
 
 def cache_free(used, slots) -> None:
@@ -144,7 +152,7 @@ def cache_free(used, slots) -> None:
     S = _slots("used", used, dev)
     n = _slots("slots", slots, dev)
     with _on(dev):
-        _done(_kda.lib().kda_cache_free(used.data_ptr(), S, slots.data_ptr(), n, _stream(dev)))
+        _done(_kda.lib().kda_cache_free(used.data_ptr(), S, slots.data_ptr(), n, _stream(dev)), used)
 
 
 def cache_compact(pool, used, remap, table=None, workspace: Optional[torch.Tensor] = None) -> None:
@@ -159,7 +167,7 @@ def cache_compact(pool, used, remap, table=None, workspace: Optional[torch.Tenso
     with _on(dev):
         ws = _space(workspace, lib.kda_cache_workspace_size(S), dev)
         _done(lib.kda_cache_compact(pool.data_ptr(), L, S, size, used.data_ptr(), remap.data_ptr(), _ptr(table), n,
-                                    ws.data_ptr(), _bytes(ws), _stream(dev)))
+                                    ws.data_ptr(), _bytes(ws), _stream(dev)), pool, used, remap, table)
 
 
 def fwd_slots(q, k, v, g, beta, scale: float, out, A_log, dt_bias, lower_bound: float, state, in_slots, out_slots,
@@ -184,7 +192,7 @@ def fwd_slots(q, k, v, g, beta, scale: float, out, A_log, dt_bias, lower_bound: 
         _done(_kda.lib().kda_fwd_slots(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), float(scale), ptr(out), ptr(A_log),
                                        ptr(dt_bias), float(lower_bound), ptr(state), _kda._state_code(state), S,
                                        ptr(in_slots), ptr(out_slots), ptr(cu_seqlens), N, B, T, H, K, V, flags,
-                                       _stream(dev)))
+                                       _stream(dev)), out, state)
 
 
 # ---- gated linear recurrence --------------------------------------------------------
@@ -244,7 +252,7 @@ def glr_fwd(x, g, y, initial_state=None, final_state=None, cu_seqlens=None, carr
     with _on(dev):
         ws = _space(workspace, lib.kda_glr_workspace_size(B, T, D, N), dev)
         _done(lib.kda_glr_fwd(ptr(x), ptr(g), ptr(y), dt, ptr(initial_state), ic, ptr(final_state), fc, ptr(carry),
-                              ptr(cu_seqlens), N, B, T, D, ptr(ws), _bytes(ws), _stream(dev)))
+                              ptr(cu_seqlens), N, B, T, D, ptr(ws), _bytes(ws), _stream(dev)), y, final_state, carry)
 
 
 def glr_bwd(x, g, dy, carry, dx, dg, initial_state=None, d_final=None, d_initial=None, cu_seqlens=None,
@@ -268,7 +276,7 @@ def glr_bwd(x, g, dy, carry, dx, dg, initial_state=None, d_final=None, d_initial
         ws = _space(workspace, lib.kda_glr_workspace_size(B, T, D, N), dev)
         _done(lib.kda_glr_bwd(ptr(x), ptr(g), ptr(dy), dt, ptr(carry), ptr(initial_state), ic, ptr(d_final), fc, ptr(dx),
                               ptr(dg), ptr(d_initial), dc, ptr(cu_seqlens), N, B, T, D, ptr(ws), _bytes(ws),
-                              _stream(dev)))
+                              _stream(dev)), dx, dg, d_initial)
 
 
 def glr_step(x, g, y, state, in_slots, out_slots) -> None:
@@ -288,7 +296,7 @@ def glr_step(x, g, y, state, in_slots, out_slots) -> None:
     with _on(dev):
         _done(_kda.lib().kda_glr_step(x.data_ptr(), g.data_ptr(), y.data_ptr(), dt, state.data_ptr(),
                                       _kda._state_code(state), state.shape[0], in_slots.data_ptr(),
-                                      out_slots.data_ptr(), N, D, _stream(dev)))
+                                      out_slots.data_ptr(), N, D, _stream(dev)), y, state)
 
 
 # ---- layer norm -----------------------------------------------------------------------
@@ -328,7 +336,7 @@ def layernorm_fwd(x, weight, bias, eps: float, y, mean=None, rstd=None) -> None:
     ptr = _ptr
     with _on(dev):
         _done(_kda.lib().kda_layernorm_fwd(ptr(x), ptr(weight), ptr(bias), float(eps), ptr(y), dt, ptr(mean), ptr(rstd),
-                                           M, D, _stream(dev)))
+                                           M, D, _stream(dev)), y, mean, rstd)
 
 
 def layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight=None, d_bias=None,
@@ -352,4 +360,5 @@ def layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight=None, d_bias=None,
         if d_weight is not None or d_bias is not None:
             ws = _space(workspace, lib.kda_layernorm_workspace_size(M, D), dev)
         _done(lib.kda_layernorm_bwd(ptr(dy), ptr(x), ptr(weight), ptr(mean), ptr(rstd), ptr(dx), dt, ptr(d_weight),
-                                    ptr(d_bias), M, D, ptr(ws), 0 if ws is None else _bytes(ws), _stream(dev)))
+                                    ptr(d_bias), M, D, ptr(ws), 0 if ws is None else _bytes(ws), _stream(dev)),
+              dx, d_weight, d_bias)

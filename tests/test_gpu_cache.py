@@ -363,3 +363,43 @@ def test_every_layer_of_a_cache(dtype, state, L, S, D):
                 outs.append((y, dx, dg, f, d0))
             assert all(torch.equal(a, b) for a, b in zip(*outs)), (T, layer)
             assert not fin[layer - 1].any() and not grad[layer - 1].any()
+
+
+def test_outputs_count_their_versions():
+    """A tensor that an operator has written counts as changed: autograd refuses to use what it
+    had saved of it, instead of taking the new values for the old."""
+    say("versions")
+    d = dev()
+    x, g = torch.randn(1, 40, 16, device=d), -torch.rand(1, 40, 16, device=d)
+    new = lambda: torch.zeros_like(x)
+    i, st = torch.zeros(1, dtype=torch.int32, device=d), torch.zeros(1, 16, device=d)
+    carry = torch.zeros(kda.glr_carry_shape(1, 40, 16), device=d)
+    o = {k: new() for k in ("y", "dx", "dg", "n", "dn")}
+    v = {k: torch.zeros(40, device=d) for k in ("mean", "rstd")}
+    w = {k: torch.zeros(16, device=d) for k in ("dw", "db")}
+    pool, used, dst, remap, table = torch.zeros(1, 4, 16, device=d), i.new_zeros(4), i.clone(), i.new_zeros(4), i.clone()
+    fin, d0, step = st.clone(), st.clone(), torch.zeros(1, 16, device=d)
+    calls = [
+        (lambda: kda.glr_fwd(x, g, o["y"], final_state=fin, carry=carry), (o["y"], fin, carry)),
+        (lambda: kda.glr_bwd(x, g, x, carry, o["dx"], o["dg"], d_initial=d0), (o["dx"], o["dg"], d0)),
+        (lambda: kda.glr_step(x[0, :1], g[0, :1], step, pool[0], i, i), (step, pool)),
+        (lambda: kda.layernorm_fwd(x, None, None, 1e-5, o["n"], mean=v["mean"], rstd=v["rstd"]), (o["n"], v["mean"], v["rstd"])),
+        (lambda: kda.layernorm_bwd(x, x, None, v["mean"], v["rstd"], o["dn"], d_weight=w["dw"], d_bias=w["db"]), (o["dn"], w["dw"], w["db"])),
+        (lambda: kda.cache_fork(pool, used, i - 1, dst), (pool, used, dst)),
+        (lambda: kda.cache_copy(pool, i, i + 1), (pool,)),
+        (lambda: kda.cache_compact(pool, used, remap, table=table), (pool, used, remap, table)),
+        (lambda: kda.cache_free(used, i), (used,))]
+    inputs = (x, g, i)
+    before = [t._version for t in inputs]
+    for n, (call, outs) in enumerate(calls):
+        old = [t._version for t in outs]
+        call()
+        assert all(t._version > k for t, k in zip(outs, old)), n
+    assert [t._version for t in inputs] == before
+    p = torch.ones(16, device=d, requires_grad=True)
+    loss = (o["n"] * p).sum()
+    kda.layernorm_fwd(x * 2, None, None, 1e-5, o["n"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        kda.layernorm_fwd(x * 2, None, None, 1e-5, torch.empty_like(x))
