@@ -260,6 +260,7 @@ int kda_cache_free(int32_t* used, int64_t S, const int32_t* slots, int64_t n, vo
   if (S < 1 || S > MAX_SLOTS || n < 0 || n > INT32_MAX) return KDA_ERR_SHAPE;
   if (!used || (n != 0 && !slots)) return KDA_ERR_NULL;
   if (any_unaligned({used, slots}, 4)) return KDA_ERR_ALIGN;
+  if (n != 0 && used == slots) return KDA_ERR_VALUE;
   return status(kda::launch_cache_free(used, S, slots, n, static_cast<hipStream_t>(stream)));
 }
 

@@ -277,9 +277,9 @@ size_t kda_noalloc_capacity(void);
  *
  * Rules of every kda_cache_* call: S <= 2^24, L >= 1, slot_bytes >= 1; pool is
  * aligned to 16 bytes, used, src, dst, slots, remap and table to 4; the arrays do
- * not overlap each other (KDA_ERR_VALUE where one is given twice). n may be 0 (nothing is done; the index arrays may then
- * be NULL). A slot number outside [0, S) is never followed: what it means is
- * said at each call.
+ * not overlap each other (KDA_ERR_VALUE where one that is written is given twice).
+ * n may be 0 (nothing is done; the index arrays may then be NULL). A slot number
+ * outside [0, S) is never followed: what it means is said at each call.
  *
  * kda_cache_copy: in every layer, slot dst[i] becomes a copy of slot src[i],
  *   0 <= i < n. Pairs with a number outside [0, S) or with src[i] == dst[i] do

@@ -206,3 +206,10 @@ def test_states_of_a_cache_layer_are_accepted():
             for p, c in states:
                 go = lambda off: call(name, d, dtype=dtype, D=D, ws=None, **{p: fake(8) + off, c: sd})   # refused after it
                 assert go(unit) == EWS and go(unit // 2) == EALIGN, (name, p, dtype, sd, D)
+
+
+def test_flags_given_as_the_slots_to_free_are_refused():
+    """kda_cache_free writes used while it reads slots: one array for both would be a race."""
+    free = dict(used=fake(4), S=8, slots=fake(4), n=4, stream=None)
+    assert call("kda_cache_free", free) == EVALUE
+    assert call("kda_cache_free", free, n=0) == OK   # nothing is done
