@@ -603,7 +603,8 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
       reduce(std::integral_constant<int, MANY>{});
     } else {
       low = __any(any_low(g));
-      if (__any(reduce(std::integral_constant<int, ONE>{}) || any_above(g) || any_large(x) || any_large(dy)) && low) mode = MANY;
+      const bool odd = reduce(std::integral_constant<int, ONE>{});
+      if (low && __any(odd || any_above(g) || any_large(x) || any_large(dy))) mode = MANY;
     }
   }
   __syncthreads();
