@@ -8,7 +8,7 @@
 // through its registers a second time for the outputs. So every element is read once and
 // written once, also for few channels on long sequences, where one lane per channel would leave
 // most of the GPU idle (8192 x 8192 bf16 so: 3.59 ms forward). Bound by memory: at that size
-// forward 84 us (4.9 TB/s), backward 131 us (5.2 TB/s) after a forward pass.
+// forward 83 us (5.0 TB/s), backward 133 us (5.2 TB/s) after a forward pass.
 //
 // Inside a tile, 16 groups of 16 lanes hold R = 8 consecutive tokens each, 16 bytes a lane and
 // token (rows that are no whole vectors: at any address, the last elements in smaller pieces);
@@ -224,16 +224,24 @@ __device__ __forceinline__ Place place_of(const GlrParams& p, const int64_t* cu,
   return {n, t == b, t == e - 1};
 }
 
-// Whether one of a lane's gates is -87 or less (NaN of that sign too): its exp may be zero. Bits
-// of negative numbers grow with their size, so it is one maximum a word.
+// The lowest of a lane's gates as bits, which grow with a negative number's size: one maximum a
+// word. is_low: -87 or less, so that its exp may be zero; is_nan: NaN of that sign.
 template <int DT, int VEC>
 using Bits = std::conditional_t<DT == FP32, uint32_t, uint16_t> __attribute__((ext_vector_type(VEC)));
 template <int DT, int VEC>
-__device__ __forceinline__ bool any_low(const Pack<DT, VEC> (&g)[R]) {
+__device__ __forceinline__ uint32_t lowest(const Pack<DT, VEC> (&g)[R]) {
   Bits<DT, VEC> m = __builtin_bit_cast(Bits<DT, VEC>, g[0].r);
 #pragma unroll
   for (int r = 1; r < R; ++r) m = __builtin_elementwise_max(m, __builtin_bit_cast(Bits<DT, VEC>, g[r].r));
-  return __builtin_reduce_max(m) >= (DT == FP32 ? 0xc2ae0000u : DT == BF16 ? 0xc2aeu : 0xd570u);
+  return __builtin_reduce_max(m);
+}
+template <int DT>
+__device__ __forceinline__ bool is_low(uint32_t bits) {
+  return bits >= (DT == FP32 ? 0xc2ae0000u : DT == BF16 ? 0xc2aeu : 0xd570u);
+}
+template <int DT>
+__device__ __forceinline__ bool is_nan(uint32_t bits) {
+  return bits > (DT == FP32 ? 0xff800000u : DT == BF16 ? 0xff80u : 0xfc00u);
 }
 // Whether one of them is above zero (or a NaN of that sign)
 template <int DT, int VEC>
@@ -360,7 +368,7 @@ __global__ __launch_bounds__(256) void kda_glr_fwd_tile_kernel(GlrParams p, cons
   // What a wave has to look out for: nothing (PLAIN), boundaries of sequences (ENDS), or those and
   // decays of zero, or products of them (CARE).
   enum { PLAIN, ENDS, CARE };
-  int mode = __all(in == all && first == 0) ? PLAIN : __any(any_low(g)) ? CARE : ENDS;
+  int mode = __all(in == all && first == 0) ? PLAIN : __any(is_low<DT>(lowest(g))) ? CARE : ENDS;
 
   auto reduce = [&](auto mode_c, float* A, float* L) {   // returns whether decays of this lane multiply to zero, or are NaN
     constexpr int MODE = decltype(mode_c)::value;
@@ -602,9 +610,10 @@ __global__ __launch_bounds__(256) void kda_glr_bwd_tile_kernel(GlrParams p, cons
     if (mode == MANY) {
       reduce(std::integral_constant<int, MANY>{});
     } else {
-      low = __any(any_low(g));
+      const uint32_t lowest_gate = lowest(g);
+      low = __any(is_low<DT>(lowest_gate));
       const bool odd = reduce(std::integral_constant<int, ONE>{});
-      if (low && __any(odd || any_above(g) || any_large(x) || any_large(dy))) mode = MANY;
+      if (low && __any(odd || is_nan<DT>(lowest_gate) || any_above(g) || any_large(x) || any_large(dy))) mode = MANY;
     }
   }
   __syncthreads();

@@ -559,6 +559,28 @@ def test_starting_over_forgets_nan_and_infinities(D, kw, dtype, low):
             assert v["dx"][half:half + 3, ::2].isnan().all()
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0], ids=["nan", "-nan"])
+@pytest.mark.parametrize("dtype", [F, BF, HF], ids=["fp32", "bf16", "fp16"])
+def test_nan_gates_stop_at_a_start_over(dtype, sign):
+    """A NaN gate, of either sign, reaches no token before or after a gate that starts over."""
+    say("NaN gates", dtype, sign)
+    c = Case(dtype, 16, lengths=[300], state=F, seed=19)
+    for t in (41, 47, 200):
+        c.g[0, t] = float("-inf")
+    clean = c.run()
+    bits = {F: torch.int32, BF: torch.int16, HF: torch.int16}[dtype]
+    nan = torch.full((16,), float("nan")).to(dtype).view(bits) | 1
+    low = torch.iinfo(bits).min
+    c.g[0, 44] = (nan & torch.iinfo(bits).max if sign > 0 else nan | low).view(dtype)
+    out = c.run()
+    v, r = ({k: t.reshape(-1, 16).cpu() for k, t in o.items()} for o in (out, clean))
+    for k, first, last in (("y", 44, 46), ("dx", 41, 43), ("dg", 42, 46)):
+        assert v[k][first:last + 1].isnan().all(), k
+        assert torch.equal(v[k][:first], r[k][:first]) and torch.equal(v[k][last + 1:], r[k][last + 1:]), k
+    assert torch.equal(v["final"], r["final"]) and torch.equal(v["d_initial"], r["d_initial"])
+
+
+
 def test_step_starts_over():
     say("a step that starts over")
     d = dev()
