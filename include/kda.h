@@ -64,8 +64,8 @@ enum kda_status {
                               state given with different dtypes                     */
     KDA_ERR_VALUE = 4,     /* lower_bound outside [-5, 0] or not finite (safe gate),
                               scale not finite, eps negative or not finite, unknown
-                              flag bits, one buffer given twice where that is ruled
-                              out, bad cu_seqlens contents (KDA_VALIDATE=1)         */
+                              flag bits, one buffer given twice where the call says
+                              so, bad cu_seqlens contents (KDA_VALIDATE=1)          */
     KDA_ERR_ALIGN = 5,     /* a pointer is not aligned as its argument has to be    */
     KDA_ERR_WORKSPACE = 6, /* workspace NULL or too small (kda_fwd_workspace_min, or the
                               operator's own kda_*_workspace_size)                  */
@@ -305,6 +305,13 @@ size_t kda_noalloc_capacity(void);
  *   there on). table (int32 [n] or NULL) holds slot numbers that are replaced by
  *   their new ones, -1 for free slots and numbers outside [0, S). workspace:
  *   kda_cache_workspace_size(S) bytes, 256-byte aligned.
+ *
+ * A pool has slots of one size. Two of them under the same slot numbers (the states
+ * of KDA and those of a recurrence) are forked by kda_cache_fork on one and
+ * kda_cache_copy with the same src and dst on the other, which leaves the slots of
+ * requests -1 there as they were: a sequence begins in them from slot -1 (in_slots
+ * of kda_fwd_slots and kda_glr_step: zeros). kda_cache_compact rewrites used, so the
+ * second pool's call takes a copy of used from before the first.
  */
 size_t kda_cache_workspace_size(int64_t S);
 int kda_cache_copy(void *pool, int64_t L, int64_t S, size_t slot_bytes, const int32_t *src, const int32_t *dst,
@@ -387,7 +394,9 @@ enum kda_dtype {
  * states to each other through it; a wait ends after KDA_GLR_POLLS polls of about a
  * microsecond, by default 2^24).
  * Results do not depend on timing: the same call gives the same bits. cu_seqlens'
- * contents are the caller's precondition, as for kda_fwd (KDA_VALIDATE=1 checks).
+ * contents are the caller's precondition: non-decreasing, within 0 .. T. KDA_VALIDATE=1
+ * checks kda_fwd's rule, with cu[0] = 0 and cu[N] = T, so it also refuses packed
+ * batches with tokens that no sequence covers.
  */
 int64_t kda_glr_carry_rows(int64_t B, int64_t T);   /* 0 for invalid sizes, as below */
 size_t kda_glr_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N);

@@ -403,3 +403,31 @@ def test_outputs_count_their_versions():
         loss.backward()
     with torch.inference_mode():
         kda.layernorm_fwd(x * 2, None, None, 1e-5, torch.empty_like(x))
+
+
+def test_two_caches_of_one_numbering():
+    """KDA's states and those of a recurrence under the same slot numbers, as the header describes
+    it: forked in one cache and copied in the other, where a new sequence begins from slot -1;
+    the second cache compacted by the flags from before the first was."""
+    say("two caches of one numbering")
+    d = dev()
+    S, D = 6, 40
+    k_pool, g_pool = make_pool(1, S, (3,), F, seed=4).to(d), make_pool(1, S, (D,), F, seed=5).to(d)
+    used = ints([0, 1, 0, 1, 0, 1])
+    src, dst = ints([3, -1, 5]), ints([0] * 3)
+    old = g_pool.clone()
+    kda.cache_fork(k_pool, used, src, dst)
+    kda.cache_copy(g_pool, src, dst)
+    assert dst.tolist() == [0, 2, 4]
+    x, g, y = torch.randn(3, D, device=d), -torch.rand(3, D, device=d), torch.empty(3, D, device=d)
+    begin = torch.where(src < 0, src, dst)
+    kda.glr_step(x, g, y, g_pool[0], begin, dst)
+    v, e = po.glr(x.cpu(), g.cpu(), [(i, i + 1) for i in range(3)], torch.stack([old[0, 3], torch.zeros(D, device=d), old[0, 5]]).cpu())
+    po.assert_near("y", y, v["y"], e["y"])
+    kda.cache_free(used, ints([1, 2]))   # 0, 3, 4 and 5 are left
+    flags_before, remap = used.clone(), ints([0] * S)
+    before = g_pool.clone()
+    kda.cache_compact(k_pool, used, remap)
+    kda.cache_compact(g_pool, flags_before, remap)
+    assert used.tolist() == flags_before.tolist() == [1, 1, 1, 1, 0, 0] and remap.tolist() == [0, -1, -1, 3, 1, 2]
+    assert torch.equal(g_pool[0, :4], before[0, [0, 4, 5, 3]])
