@@ -14,7 +14,9 @@ beta bf16 [B, T, H] (logits); out bf16 [B, T, H, 128] written in place;
 A_log fp32 [H]; dt_bias fp32 [H, 128]; lower_bound in [-5, 0]; states bf16 or
 fp32 [B|N, H, 128, 128] with equal dtypes; cu_seqlens int64 [N+1] with B = 1.
 Returns None. Beside it: ``fwd_slots`` (KDA on a cache's slots) and ``cache_*``, the
-gated linear recurrence ``glr_*`` and layer norm ``layernorm_*``, in the same manner.
+gated linear recurrence ``glr_*`` and layer norm ``layernorm_*``; a state space layer's
+``rmsnorm_*``, ``conv_*`` and ``ssm_*``; beam search with ``beam_select`` and ``cache_reorder``,
+all in the same manner.
 There is no CPU fallback: if libkda.so is missing or fails to
 load, every call raises.
 """
@@ -30,7 +32,11 @@ __all__ = ["fwd", "fwd_recurrent", "workspace_size", "workspace_min", "record_by
            "profile_start", "profile_stop",
            "fwd_slots", "cache_copy", "cache_fork", "cache_free", "cache_compact",
            "glr_fwd", "glr_bwd", "glr_step", "glr_carry_shape", "glr_workspace_size",
-           "layernorm_fwd", "layernorm_bwd", "layernorm_workspace_size"]
+           "layernorm_fwd", "layernorm_bwd", "layernorm_workspace_size",
+           "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_workspace_size",
+           "conv_fwd", "conv_bwd", "conv_step", "conv_workspace_size",
+           "ssm_fwd", "ssm_bwd", "ssm_step", "ssm_carry_shape", "ssm_workspace_size",
+           "beam_select", "beam_workspace_size", "cache_reorder"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -89,6 +95,7 @@ def _setup(L):
     L.kda_profile_kernel_name.restype = ctypes.c_char_p
     L.kda_profile_kernel_name.argtypes = [I]
     _ops._setup(L)
+    _layer._setup(L)
     return L
 
 
@@ -277,3 +284,7 @@ def profile_stop() -> dict:
 from . import _ops  # noqa: E402  (its wrappers use the helpers above)
 from ._ops import (cache_compact, cache_copy, cache_fork, cache_free, fwd_slots, glr_bwd, glr_carry_shape,  # noqa: E402
                    glr_fwd, glr_step, glr_workspace_size, layernorm_bwd, layernorm_fwd, layernorm_workspace_size)
+from . import _layer  # noqa: E402
+from ._layer import (beam_select, beam_workspace_size, cache_reorder, conv_bwd, conv_fwd, conv_step,  # noqa: E402
+                     conv_workspace_size, rmsnorm_bwd, rmsnorm_fwd, rmsnorm_workspace_size, ssm_bwd, ssm_carry_shape, ssm_fwd,
+                     ssm_step, ssm_workspace_size)

@@ -1,0 +1,380 @@
+"""Python binding of a state space layer's operators: the root-mean-square norm, the short
+causal convolution, the selective scan, and beam search with the beams' states in a cache
+(include/kda.h). In the manner of _ops: outputs are the caller's tensors, written in place;
+contiguous GPU tensors of one device; work goes to that device's current stream; gradients
+come from the calls named _bwd."""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+import gated_delta_rule_87_amd as _kda
+from ._ops import (F, I, I64, P, SZ, _bytes, _done, _dtype, _glr_sizes, _gpu, _on, _pool, _ptr, _rows, _slots, _space, _state,
+                   _stream, _vector)
+
+U32 = ctypes.c_uint32
+E4M3 = 4
+CONV_SILU = 1
+SSM_SOFTPLUS = 1
+
+
+def _setup(L):
+    """Declare the C signatures of these operators on a loaded libkda.so."""
+    def sig(name, restype, *args):
+        f = getattr(L, name)
+        f.restype, f.argtypes = restype, list(args)
+    sig("kda_rmsnorm_workspace_size", SZ, I64, I64)
+    sig("kda_rmsnorm_fwd", I, P, P, P, F, P, I, P, I64, P, I, P, I64, I64, P)
+    sig("kda_rmsnorm_bwd", I, P, P, P, P, P, P, I, P, I64, I64, P, SZ, P)
+    sig("kda_conv_workspace_size", SZ, I64, I64, I64, I64)
+    sig("kda_conv_fwd", I, P, P, P, P, I, I64, U32, P, I, P, I, P, I64, I64, I64, I64, P)
+    sig("kda_conv_bwd", I, P, P, P, P, I, I64, U32, P, I, P, I, P, P, P, P, I, P, I64, I64, I64, I64, P, SZ, P)
+    sig("kda_conv_step", I, P, P, P, P, I, I64, U32, P, I, I64, P, P, I64, I64, P)
+    sig("kda_ssm_carry_rows", I64, I64, I64)
+    sig("kda_ssm_workspace_size", SZ, I64, I64, I64, I64, I64, I64, I)
+    sig("kda_ssm_fwd", I, P, P, P, P, P, P, P, P, P, I, U32, P, I, P, I, P, P, I64, I64, I64, I64, I64, I64, P, SZ, P)
+    sig("kda_ssm_bwd", I, P, P, P, P, P, P, P, P, P, I, U32, P, P, I, P, I, P, P, P, P, P, P, P, P, P, I, P, I64, I64, I64, I64,
+        I64, I64, P, SZ, P)
+    sig("kda_ssm_step", I, P, P, P, P, P, P, P, P, P, I, U32, P, I, I64, P, P, I64, I64, I64, I64, P)
+    sig("kda_beam_workspace_size", SZ, I64, I64, I64, I64)
+    sig("kda_beam_select", I, P, I, P, P, I64, P, P, P, I64, I64, I64, I64, P, SZ, P)
+    sig("kda_cache_reorder", I, P, I64, I64, SZ, P, P, P, I64, I64, P)
+
+
+def _fp32(name, t, shape, dev, optional=False):
+    if t is None and optional:
+        return
+    _kda._check(name, t, torch.float32, shape, dev)
+
+
+# ---- root-mean-square norm ------------------------------------------------------------
+
+
+def rmsnorm_workspace_size(M: int, D: int) -> int:
+    """Bytes of workspace rmsnorm_bwd needs for the weight's gradient."""
+    return int(_kda.lib().kda_rmsnorm_workspace_size(int(M), int(D)))
+
+
+def rmsnorm_fwd(x, weight, eps: float, y, residual=None, residual_out=None, scales=None, rstd=None) -> None:
+    """Root-mean-square norm over the last dimension of ``x + residual`` [..., D] (bf16, fp32 or
+    fp16; residual None: of x) into ``y``: of x's type, or float8_e4m3fn with ``scales`` fp32
+    [..., ceil(D / 128)] (one for each 128 elements) or [..., 1] (one a row), which y's values
+    are to be multiplied by. weight fp32 [D] or None. The sum into ``residual_out`` (like x) and
+    each row's 1 / sqrt(mean square + eps) into ``rstd`` (fp32, one per row) where given. y (of
+    x's type) and residual_out may be x or residual (kda_rmsnorm_fwd)."""
+    dev, M, D, dt = _rows(x)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if t is not None:
+            _kda._check(name, t, x.dtype, x.shape, dev)
+    group, y_dt = 0, dt
+    if isinstance(y, torch.Tensor) and y.dtype == torch.float8_e4m3fn:
+        _kda._check("y", y, torch.float8_e4m3fn, x.shape, dev)
+        y_dt, blocks = E4M3, (D + 127) // 128
+        if not isinstance(scales, torch.Tensor) or scales.dim() != x.dim() or scales.shape[-1] not in (1, blocks):
+            raise ValueError(f"scales must be [..., {blocks}] or [..., 1] for an 8-bit y")
+        _fp32("scales", scales, (*x.shape[:-1], scales.shape[-1]), dev)
+        group = D if scales.shape[-1] == 1 else 128
+    else:
+        _kda._check("y", y, x.dtype, x.shape, dev)
+        if scales is not None:
+            raise ValueError("scales go with a float8_e4m3fn y only")
+    _vector("weight", weight, D, dev)
+    _vector("rstd", rstd, M, dev)
+    ptr = _ptr
+    with _on(dev):
+        _done(_kda.lib().kda_rmsnorm_fwd(ptr(x), ptr(residual), ptr(weight), float(eps), ptr(y), y_dt, ptr(scales), group,
+                                         ptr(residual_out), dt, ptr(rstd), M, D, _stream(dev)), y, residual_out, scales, rstd)
+
+
+def rmsnorm_bwd(dy, x, weight, rstd, dx, d_weight=None, d_residual=None, workspace: Optional[torch.Tensor] = None) -> None:
+    """Backward pass of rmsnorm_fwd from its ``rstd`` and ``x``, the sum that was normed
+    (residual_out): ``dx`` like x, the gradient of x and of the residual alike (it may be dy, x
+    or d_residual, or None), with ``d_residual``, the gradient of residual_out, added to it;
+    ``d_weight`` fp32 [D] or None (kda_rmsnorm_bwd)."""
+    dev, M, D, dt = _rows(x)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("dy", dy, x.dtype, x.shape, dev)
+    for name, t in (("dx", dx), ("d_residual", d_residual)):
+        if t is not None:
+            _kda._check(name, t, x.dtype, x.shape, dev)
+    if rstd is None:
+        raise ValueError("rstd of the forward pass is required")
+    for name, t, n in (("weight", weight, D), ("rstd", rstd, M), ("d_weight", d_weight, D)):
+        _vector(name, t, n, dev)
+    lib, ptr = _kda.lib(), _ptr
+    with _on(dev):
+        ws = None if d_weight is None else _space(workspace, lib.kda_rmsnorm_workspace_size(M, D), dev)
+        _done(lib.kda_rmsnorm_bwd(ptr(dy), ptr(x), ptr(weight), ptr(rstd), ptr(d_residual), ptr(dx), dt, ptr(d_weight), M, D,
+                                  ptr(ws), 0 if ws is None else _bytes(ws), _stream(dev)), dx, d_weight)
+
+
+# ---- short causal convolution -----------------------------------------------------------
+
+
+def _conv_weights(weight, bias, D, dev) -> int:
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a 2-D tensor [D, W]")
+    W = weight.shape[1]
+    _fp32("weight", weight, (D, W), dev)
+    _fp32("bias", bias, (D,), dev, optional=True)
+    return W
+
+
+def conv_workspace_size(B: int, T: int, D: int, W: int) -> int:
+    """Bytes of workspace conv_bwd needs for the weight's and the bias's gradient."""
+    return int(_kda.lib().kda_conv_workspace_size(int(B), int(T), int(D), int(W)))
+
+
+def conv_fwd(x, weight, bias, y, initial_state=None, final_state=None, cu_seqlens=None, silu: bool = True) -> None:
+    """Short causal convolution per channel, ``u_t = bias + sum_j weight[:, j] x_{t-W+1+j}``, then
+    SiLU (unless ``silu`` is False), into ``y``.
+
+    x, y [B, T, D] of one dtype (bf16, fp32 or fp16); weight fp32 [D, W], W = 2, 3 or 4; bias
+    fp32 [D] or None; states bf16/fp32 [B|N, W - 1, D], the inputs before the next token, the
+    oldest first (kda_conv_fwd)."""
+    dev = _gpu("x", x, 3)
+    B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
+    dt = _dtype("x", x)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
+    W = _conv_weights(weight, bias, D, dev)
+    shape = (N if cu_seqlens is not None else B, W - 1, D)
+    ic = _state("initial_state", initial_state, shape, dev)
+    fc = _state("final_state", final_state, shape, dev)
+    if ic and fc and ic != fc:
+        raise ValueError("initial_state and final_state must have the same dtype")
+    ptr = _ptr
+    with _on(dev):
+        _done(_kda.lib().kda_conv_fwd(ptr(x), ptr(weight), ptr(bias), ptr(y), dt, W, CONV_SILU if silu else 0, ptr(initial_state),
+                                      ic, ptr(final_state), fc, ptr(cu_seqlens), N, B, T, D, _stream(dev)), y, final_state)
+
+
+def conv_bwd(x, weight, bias, dy, dx, d_weight=None, d_bias=None, initial_state=None, d_final=None, d_initial=None,
+             cu_seqlens=None, silu: bool = True, workspace: Optional[torch.Tensor] = None) -> None:
+    """Backward pass of conv_fwd: ``dx`` like x, ``d_weight`` fp32 [D, W], ``d_bias`` fp32 [D]
+    (each may be None) and ``d_initial`` ([B|N, W - 1, D] or None) from ``dy`` and ``d_final``
+    (None: zero) (kda_conv_bwd)."""
+    dev = _gpu("x", x, 3)
+    B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
+    dt = _dtype("x", x)
+    for name, t in (("x", x), ("dy", dy), ("dx", dx)):
+        _kda._check(name, t, x.dtype, x.shape, dev)
+    W = _conv_weights(weight, bias, D, dev)
+    _fp32("d_weight", d_weight, (D, W), dev, optional=True)
+    _fp32("d_bias", d_bias, (D,), dev, optional=True)
+    shape = (N if cu_seqlens is not None else B, W - 1, D)
+    ic = _state("initial_state", initial_state, shape, dev)
+    fc = _state("d_final", d_final, shape, dev)
+    dc = _state("d_initial", d_initial, shape, dev)
+    lib, ptr = _kda.lib(), _ptr
+    with _on(dev):
+        ws = None
+        if d_weight is not None or d_bias is not None:
+            ws = _space(workspace, lib.kda_conv_workspace_size(B, T, D, W), dev)
+        _done(lib.kda_conv_bwd(ptr(x), ptr(weight), ptr(bias), ptr(dy), dt, W, CONV_SILU if silu else 0, ptr(initial_state), ic,
+                               ptr(d_final), fc, ptr(dx), ptr(d_weight), ptr(d_bias), ptr(d_initial), dc, ptr(cu_seqlens), N, B, T,
+                               D, ptr(ws), 0 if ws is None else _bytes(ws), _stream(dev)), dx, d_weight, d_bias, d_initial)
+
+
+def conv_step(x, weight, bias, y, state, in_slots, out_slots, silu: bool = True) -> None:
+    """One token of the convolution for each of N sequences, x, y [N, D]: the inputs before it are
+    read from slots ``in_slots`` and left, with it, in slots ``out_slots`` (int32 [N]) of a cache's
+    layer ``state`` [slots, W - 1, D] (kda_conv_step)."""
+    dev = _gpu("x", x, 2)
+    N, D = x.shape
+    dt = _dtype("x", x)
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
+    W = _conv_weights(weight, bias, D, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be a 3-D tensor [slots, W - 1, D]")
+    _kda._check("state", state, state.dtype, (state.shape[0], W - 1, D), dev)
+    _slots("in_slots", in_slots, dev, N)
+    _slots("out_slots", out_slots, dev, N)
+    with _on(dev):
+        _done(_kda.lib().kda_conv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), dt, W, CONV_SILU if silu else 0,
+                                       state.data_ptr(), _kda._state_code(state), state.shape[0], in_slots.data_ptr(),
+                                       out_slots.data_ptr(), N, D, _stream(dev)), y, state)
+
+
+# ---- selective state space scan -----------------------------------------------------------
+
+
+def _ssm_inputs(x, dt, A, B, C, skip, z, dt_bias, dev):
+    """E and G, after checking the operator's inputs against x [..., D]."""
+    D = x.shape[-1]
+    _kda._check("x", x, x.dtype, x.shape, dev)
+    _kda._check("dt", dt, x.dtype, x.shape, dev)
+    if z is not None:
+        _kda._check("z", z, x.dtype, x.shape, dev)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a 2-D tensor [D, E]")
+    E = A.shape[1]
+    _fp32("A", A, (D, E), dev)
+    if not isinstance(B, torch.Tensor) or B.dim() != x.dim() + 1:
+        raise ValueError(f"B must be a tensor [{'B, T' if x.dim() == 3 else 'N'}, G, E]")
+    G = B.shape[-2]
+    for name, t in (("B", B), ("C", C)):
+        _kda._check(name, t, x.dtype, (*x.shape[:-1], G, E), dev)
+    if G < 1 or D % G:
+        raise ValueError(f"G must divide D (got D={D}, G={G})")
+    _fp32("D", skip, (D,), dev, optional=True)
+    _fp32("dt_bias", dt_bias, (D,), dev, optional=True)
+    return E, G
+
+
+def ssm_carry_shape(B: int, T: int, D: int, E: int) -> tuple:
+    """Shape of the fp32 ``carry`` that ssm_fwd saves for ssm_bwd."""
+    return int(_kda.lib().kda_ssm_carry_rows(int(B), int(T))), int(D), int(E)
+
+
+def ssm_workspace_size(B: int, T: int, D: int, E: int, G: int = 1, N: int = 0, backward: bool = False) -> int:
+    """Bytes of workspace ssm_fwd, or ssm_bwd, needs (N = number of sequences with cu_seqlens, else 0)."""
+    return int(_kda.lib().kda_ssm_workspace_size(int(B), int(T), int(D), int(E), int(G), int(N), int(bool(backward))))
+
+
+def ssm_fwd(x, dt, A, B, C, y, D=None, z=None, dt_bias=None, softplus: bool = True, initial_state=None, final_state=None,
+            cu_seqlens=None, carry=None, workspace: Optional[torch.Tensor] = None) -> None:
+    """Selective state space scan: per channel and state ``h_t = exp(s_t A) h_{t-1} + s_t x_t B_t``
+    with ``s_t = softplus(dt_t + dt_bias)`` (``softplus`` False: without it), and
+    ``y_t = (C_t . h_t + D x_t) silu(z_t)`` into ``y`` (and ``final_state``, and ``carry`` for the
+    backward pass).
+
+    x, dt, z, y [B, T, D] of one dtype (bf16, fp32 or fp16); A fp32 [D, E], E <= 64; B, C
+    [B, T, G, E] of x's dtype, G dividing D; D, dt_bias fp32 [D]; D, z and dt_bias may be None;
+    states bf16/fp32 [B|N, D, E]; carry fp32 of ssm_carry_shape (kda_ssm_fwd)."""
+    dev = _gpu("x", x, 3)
+    Bn, T, Dn, N = _glr_sizes(x, cu_seqlens, dev)
+    code = _dtype("x", x)
+    E, G = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
+    shape = (N if cu_seqlens is not None else Bn, Dn, E)
+    ic = _state("initial_state", initial_state, shape, dev)
+    fc = _state("final_state", final_state, shape, dev)
+    if ic and fc and ic != fc:
+        raise ValueError("initial_state and final_state must have the same dtype")
+    lib, ptr = _kda.lib(), _ptr
+    if carry is not None:
+        _fp32("carry", carry, (lib.kda_ssm_carry_rows(Bn, T), Dn, E), dev)
+    with _on(dev):
+        ws = _space(workspace, lib.kda_ssm_workspace_size(Bn, T, Dn, E, G, N, 0), dev)
+        _done(lib.kda_ssm_fwd(ptr(x), ptr(dt), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(dt_bias), ptr(y), code,
+                              SSM_SOFTPLUS if softplus else 0, ptr(initial_state), ic, ptr(final_state), fc, ptr(carry),
+                              ptr(cu_seqlens), N, Bn, T, Dn, E, G, ptr(ws), _bytes(ws), _stream(dev)), y, final_state, carry)
+
+
+def ssm_bwd(x, dt, A, B, C, dy, carry, dx, d_dt, dA, dB, dC, D=None, d_D=None, z=None, d_z=None, dt_bias=None, d_dt_bias=None,
+            softplus: bool = True, initial_state=None, d_final=None, d_initial=None, cu_seqlens=None,
+            workspace: Optional[torch.Tensor] = None) -> None:
+    """Backward pass of ssm_fwd: writes the gradients ``dx``, ``d_dt`` (like x), ``dA`` fp32 [D, E],
+    ``dB``, ``dC`` (like B), and where given ``d_D``, ``d_dt_bias`` fp32 [D], ``d_z`` (like x) and
+    ``d_initial`` [B|N, D, E] from ``dy`` and ``d_final`` (None: zero). ``carry`` is what ssm_fwd saved
+    for the same inputs (kda_ssm_bwd)."""
+    dev = _gpu("x", x, 3)
+    Bn, T, Dn, N = _glr_sizes(x, cu_seqlens, dev)
+    code = _dtype("x", x)
+    E, G = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dev)
+    for name, t in (("dy", dy), ("dx", dx), ("d_dt", d_dt)):
+        _kda._check(name, t, x.dtype, x.shape, dev)
+    for name, t in (("dB", dB), ("dC", dC)):
+        _kda._check(name, t, x.dtype, B.shape, dev)
+    _fp32("dA", dA, (Dn, E), dev)
+    for name, t, of, given in (("d_D", d_D, "D", D), ("d_z", d_z, "z", z), ("d_dt_bias", d_dt_bias, "dt_bias", dt_bias)):
+        if t is None:
+            continue
+        if given is None:
+            raise ValueError(f"{name} without {of}")
+        _kda._check(name, t, given.dtype, given.shape, dev)
+    shape = (N if cu_seqlens is not None else Bn, Dn, E)
+    ic = _state("initial_state", initial_state, shape, dev)
+    fc = _state("d_final", d_final, shape, dev)
+    dc = _state("d_initial", d_initial, shape, dev)
+    lib, ptr = _kda.lib(), _ptr
+    _fp32("carry", carry, (lib.kda_ssm_carry_rows(Bn, T), Dn, E), dev)
+    with _on(dev):
+        ws = _space(workspace, lib.kda_ssm_workspace_size(Bn, T, Dn, E, G, N, 1), dev)
+        _done(lib.kda_ssm_bwd(ptr(x), ptr(dt), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(dt_bias), ptr(dy), code,
+                              SSM_SOFTPLUS if softplus else 0, ptr(carry), ptr(initial_state), ic, ptr(d_final), fc, ptr(dx),
+                              ptr(d_dt), ptr(dA), ptr(dB), ptr(dC), ptr(d_D), ptr(d_z), ptr(d_dt_bias), ptr(d_initial), dc,
+                              ptr(cu_seqlens), N, Bn, T, Dn, E, G, ptr(ws), _bytes(ws), _stream(dev)),
+              dx, d_dt, dA, dB, dC, d_D, d_z, d_dt_bias, d_initial)
+
+
+def ssm_step(x, dt, A, B, C, y, state, in_slots, out_slots, D=None, z=None, dt_bias=None, softplus: bool = True) -> None:
+    """One token of the scan for each of N sequences, x, dt, z, y [N, D], B, C [N, G, E]: the states
+    are read from slots ``in_slots`` and left in slots ``out_slots`` (int32 [N]) of a cache's layer
+    ``state`` [slots, D, E] (kda_ssm_step)."""
+    dev = _gpu("x", x, 2)
+    N, Dn = x.shape
+    code = _dtype("x", x)
+    E, G = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dev)
+    _kda._check("y", y, x.dtype, x.shape, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be a 3-D tensor [slots, D, E]")
+    _kda._check("state", state, state.dtype, (state.shape[0], Dn, E), dev)
+    _slots("in_slots", in_slots, dev, N)
+    _slots("out_slots", out_slots, dev, N)
+    ptr = _ptr
+    with _on(dev):
+        _done(_kda.lib().kda_ssm_step(ptr(x), ptr(dt), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(dt_bias), ptr(y), code,
+                                      SSM_SOFTPLUS if softplus else 0, ptr(state), _kda._state_code(state), state.shape[0],
+                                      ptr(in_slots), ptr(out_slots), N, Dn, E, G, _stream(dev)), y, state)
+
+
+# ---- beam search ------------------------------------------------------------------------------
+
+
+def _int32(name, t, shape, dev):
+    _kda._check(name, t, torch.int32, shape, dev)
+
+
+def beam_workspace_size(N: int, W: int, V: int, k: int) -> int:
+    """Bytes of workspace beam_select needs."""
+    return int(_kda.lib().kda_beam_workspace_size(int(N), int(W), int(V), int(k)))
+
+
+def beam_select(logits, scores, tokens, parents, new_scores, finished=None, eos: int = 0,
+                workspace: Optional[torch.Tensor] = None) -> None:
+    """The k best continuations of N sequences' W beams: ``logits`` [N, W, V] (bf16, fp32 or fp16),
+    ``scores`` fp32 [N, W] the beams' log-probabilities so far; writes each continuation's token
+    and beam to ``tokens`` and ``parents`` (int32 [N, k], -1 where there are fewer) and its
+    log-probability to ``new_scores`` (fp32 [N, k]), the best first. A beam whose flag in
+    ``finished`` (int32 [N, W] or None) is not zero goes on with ``eos`` alone, at its score
+    (kda_beam_select)."""
+    dev = _gpu("logits", logits, 3)
+    N, W, V = logits.shape
+    dt = _dtype("logits", logits)
+    _kda._check("logits", logits, logits.dtype, logits.shape, dev)
+    _fp32("scores", scores, (N, W), dev)
+    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
+        raise ValueError("tokens must be a 2-D tensor [N, k]")
+    k = tokens.shape[1]
+    _int32("tokens", tokens, (N, k), dev)
+    _int32("parents", parents, (N, k), dev)
+    _fp32("new_scores", new_scores, (N, k), dev)
+    if finished is not None:
+        _int32("finished", finished, (N, W), dev)
+    lib, ptr = _kda.lib(), _ptr
+    with _on(dev):
+        ws = _space(workspace, lib.kda_beam_workspace_size(N, W, V, k), dev)
+        _done(lib.kda_beam_select(ptr(logits), dt, ptr(scores), ptr(finished), int(eos), ptr(tokens), ptr(parents), ptr(new_scores),
+                                  N, W, V, k, ptr(ws), _bytes(ws), _stream(dev)), tokens, parents, new_scores)
+
+
+def cache_reorder(pool, slots, parents, new_slots) -> None:
+    """The beams' states follow a step of beam search: ``pool`` [layers, slots, ...], ``slots``,
+    ``parents``, ``new_slots`` int32 [N, W]. New beam j of sequence n continues beam
+    ``parents[n, j]``: the first one that does keeps its slot, the others get copies in the slots
+    of beams that no one continues. ``new_slots`` (OUTPUT) says which (kda_cache_reorder)."""
+    dev, L, S, size = _pool(pool)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise ValueError("slots must be a 2-D tensor [N, W]")
+    N, W = slots.shape
+    for name, t in (("slots", slots), ("parents", parents), ("new_slots", new_slots)):
+        _int32(name, t, (N, W), dev)
+    with _on(dev):
+        _done(_kda.lib().kda_cache_reorder(pool.data_ptr(), L, S, size, slots.data_ptr(), parents.data_ptr(), new_slots.data_ptr(), N,
+                                           W, _stream(dev)), pool, new_slots)

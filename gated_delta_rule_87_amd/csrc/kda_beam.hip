@@ -1,0 +1,390 @@
+// kda_beam.hip -- beam search: the best continuations of every sequence's beams (gfx950).
+//
+//     score(b, v) = scores[b] + logits[b][v] - log sum_v' exp(logits[b][v'])
+//
+// A beam's logits are cut into pieces, one workgroup each, which holds its piece in registers: it
+// is read once for the largest value, the sum of exponentials and the best k values. A second
+// kernel, one workgroup a sequence, joins the beams' sums and picks the best k of all pieces'.
+// Bound by reading the logits. Scores of different beams lie close together and their order is the
+// result, so sums and scores are 64 bits (an fp64 operation takes as long as an fp32 one here; the
+// exponential of 13 operations is good to 1e-11).
+//
+// The best k are found by counting, not by sorting: the 256 lanes form k' >= k groups, each with
+// its best element, and the least of those k' is a threshold that at least k elements reach, about
+// k' ln k' of them as a rule. Those go to shared memory, where each counts the ones before it:
+// its place among the results. Keys hold the value and, below it, the index, so no two are equal,
+// and what is chosen does not depend on the order in which lanes run. Where more elements than
+// shared memory holds reach the threshold, it is raised by bisection.
+#include <type_traits>
+
+#include "kda_elem.h"
+#include "kda_ops.h"
+
+namespace kda {
+namespace {
+
+using std::integral_constant;
+
+constexpr int HOLD = 512;   // elements that may reach the threshold
+
+// bits that grow with the number; 0 is below all of them
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
+__device__ __forceinline__ uint64_t ordered(double f) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, f);
+  return u >> 63 ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ double unordered(uint64_t u) {
+  return __builtin_bit_cast(double, u >> 63 ? u & ~(1ull << 63) : ~u);
+}
+
+// exp(t), t <= 0: 2^n 2^f, |f| <= 1/2, a Taylor series of nine terms (7e-12). Below -40 it is
+// nothing beside the sum, which is at least 1.
+__device__ __forceinline__ double exp_below(double t) {
+  t = t < -40.0 ? -40.0 : t;
+  const double y = t * 1.4426950408889634074, n = __builtin_rint(y), f = (y - n) * 0.69314718055994530942;
+  double s = 1.0 / 362880.0;
+  s = fma(s, f, 1.0 / 40320.0);
+  s = fma(s, f, 1.0 / 5040.0);
+  s = fma(s, f, 1.0 / 720.0);
+  s = fma(s, f, 1.0 / 120.0);
+  s = fma(s, f, 1.0 / 24.0);
+  s = fma(s, f, 1.0 / 6.0);
+  s = fma(s, f, 0.5);
+  s = fma(s, f, 1.0);
+  s = fma(s, f, 1.0);
+  return __builtin_ldexp(s, (int)n);
+}
+
+template <typename T>
+__device__ __forceinline__ T from_lane(T v, int mask) {   // of lane ^ mask
+  return __shfl_xor(v, mask, 64);
+}
+
+// A piece's results: [rows][pieces]
+struct BeamWs {
+  uint64_t* best;   // [k] keys: value and ~index; 0 where there are fewer
+  double* sum;      // of exp(value - top)
+  float* top;       // largest value; NaN where one is NaN or +infinity
+  int32_t pieces;
+  int32_t groups;   // k': a power of two from 4 to 64, at least k
+};
+
+// Least of the groups' largest keys, as KEY has them (an operator > and a zero); the same in all
+// lanes. buf: 64 keys
+template <typename KEY>
+__device__ __forceinline__ KEY threshold(KEY most, int groups, KEY* buf) {
+  const int size = 256 / groups, lane = threadIdx.x & 63;   // lanes of a group: 4 .. 64
+  for (int o = 1; o < size; o <<= 1) {
+    const KEY other = most.from(o);
+    if (other > most) most = other;
+  }
+  if (threadIdx.x % size == 0) buf[threadIdx.x / size] = most;
+  __syncthreads();
+  KEY least = buf[lane % groups];
+  for (int o = 1; o < groups; o <<= 1) {
+    const KEY other = least.from(o);
+    if (least > other) least = other;
+  }
+  __syncthreads();
+  return least;
+}
+
+// Sum of v over the workgroup, in all lanes. buf: 4
+template <typename T>
+__device__ __forceinline__ T wg_sum(T v, T* buf) {
+  for (int o = 1; o < 64; o <<= 1) v += from_lane(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+}
+
+struct Key64 {
+  uint64_t v;
+  __device__ __forceinline__ bool operator>(const Key64& o) const { return v > o.v; }
+  __device__ __forceinline__ Key64 from(int mask) const { return {from_lane(v, mask)}; }
+};
+
+// PER elements of a lane. A workgroup takes a piece of 256 PER elements of a beam's logits.
+template <int DT, int PER>
+__global__ __launch_bounds__(256) void kda_beam_piece_kernel(BeamParams p, BeamWs w) {
+  constexpr int VEC = 16 / elem_size(DT), NV = PER / VEC;
+  __shared__ Key64 s_group[64];
+  __shared__ uint64_t s_keys[HOLD];
+  __shared__ double s_sum[4];
+  __shared__ int s_count[4], s_used;
+  __shared__ float s_top[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t items = (int64_t)p.N * p.W * w.pieces;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t row = it / w.pieces;
+    const int first = (int)(it - row * w.pieces) * 256 * PER;
+    if (p.finished && p.finished[row] != 0) continue;   // the same in all lanes
+    Pack<DT, VEC> raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = first + (i * 256 + tid) * VEC;
+      raw[i].clear();
+      if (at < p.V) load_part<false>(raw[i], p.logits, (size_t)row * p.V + at, p.V - at < VEC ? p.V - at : VEC);
+    }
+    float x[PER], top = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      raw[i].unpack(x + i * VEC);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float& f = x[i * VEC + e];
+        if (first + (i * 256 + tid) * VEC + e >= p.V) f = -INFINITY;
+        bad = bad || !(f < INFINITY);
+        top = fmaxf(top, f);
+      }
+    }
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, from_lane(top, o));
+    if (__any(bad)) top = __uint_as_float(0x7fc00000u);
+    __syncthreads();   // the item before has been read
+    if (lane == 0) s_top[wave] = top;
+    if (tid == 0) s_used = 0;
+    __syncthreads();
+    bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bad = bad || s_top[i] != s_top[i];
+      top = i == 0 ? s_top[0] : fmaxf(top, s_top[i]);
+    }
+    if (bad || top == -INFINITY) {   // no continuation here
+      if (tid == 0) {
+        w.top[it] = bad ? __uint_as_float(0x7fc00000u) : -INFINITY;
+        w.sum[it] = 0.0;
+      }
+      for (int i = tid; i < p.k; i += 256) w.best[it * p.k + i] = 0;
+      continue;
+    }
+    double sum = 0.0;
+    uint64_t most = 0;
+    auto key = [&](int j) -> uint64_t {   // element j of the lane's
+      const int at = first + ((j / VEC) * 256 + tid) * VEC + j % VEC;
+      return x[j] == -INFINITY ? 0ull : ((uint64_t)ordered(x[j]) << 32) | (uint32_t)~at;
+    };
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (x[j] != -INFINITY) sum += exp_below((double)x[j] - (double)top);
+      const uint64_t q = key(j);
+      most = q > most ? q : most;
+    }
+    sum = wg_sum(sum, s_sum);
+    uint64_t least = threshold(Key64{most}, w.groups, s_group).v;
+    if (least == 0) least = 1;
+    auto reach = [&](uint64_t t) {   // elements of the workgroup with keys of t and more
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) n += key(j) >= t;
+      return wg_sum(n, s_count);
+    };
+    int count = reach(least);
+    for (uint64_t high = ~0ull; count > HOLD;) {   // reach(least) >= k > reach(high)
+      const uint64_t mid = least + (high - least) / 2;
+      const int n = reach(mid);
+      if (n >= p.k) {
+        least = mid;
+        count = n;
+      } else {
+        high = mid;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint64_t q = key(j);
+      if (q >= least) s_keys[atomicAdd(&s_used, 1)] = q;
+    }
+    __syncthreads();
+    for (int i = tid; i < count; i += 256) {
+      const uint64_t q = s_keys[i];
+      int place = 0;
+      for (int j = 0; j < count; ++j) place += s_keys[j] > q;
+      if (place < p.k) w.best[it * p.k + place] = q;
+    }
+    for (int i = count + tid; i < p.k; i += 256) w.best[it * p.k + i] = 0;
+    if (tid == 0) {
+      w.top[it] = top;
+      w.sum[it] = sum;
+    }
+  }
+}
+
+struct Key96 {
+  uint64_t s;   // score
+  uint32_t i;   // ~(beam V + token)
+  __device__ __forceinline__ bool operator>(const Key96& o) const { return s > o.s || (s == o.s && i > o.i); }
+  __device__ __forceinline__ Key96 from(int mask) const { return {from_lane(s, mask), from_lane(i, mask)}; }
+};
+
+__global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs w) {
+  __shared__ double s_top[64], s_log[64], s_score[64];
+  __shared__ bool s_none[64], s_done[64];
+  __shared__ Key96 s_group[64], s_keys[HOLD];
+  __shared__ int s_count[4], s_used;
+  const int tid = threadIdx.x, n = blockIdx.x, lane = tid & 63;
+  if (tid == 0) s_used = 0;
+  for (int b = tid >> 6; b < p.W; b += 4) {   // a wave: a beam's sum over its pieces
+    const int64_t row = (int64_t)n * p.W + b, at = row * w.pieces;
+    const bool done = p.finished && p.finished[row] != 0;
+    double top = -INFINITY, sum = 0.0;
+    bool bad = false;
+    if (!done) {
+      for (int i = lane; i < w.pieces; i += 64) {
+        const float t = w.top[at + i];
+        bad = bad || t != t;
+        top = t > top ? t : top;
+      }
+      for (int o = 1; o < 64; o <<= 1) {
+        const double t = from_lane(top, o);
+        top = t > top ? t : top;
+      }
+      bad = __any(bad) || top == -INFINITY;
+      if (!bad)
+        for (int i = lane; i < w.pieces; i += 64) {
+          const float t = w.top[at + i];
+          if (t != -INFINITY) sum += w.sum[at + i] * exp_below((double)t - top);
+        }
+      for (int o = 1; o < 64; o <<= 1) sum += from_lane(sum, o);
+    }
+    if (lane == 0) {
+      const float sc = p.scores[row];
+      s_top[b] = top;
+      s_log[b] = done || bad ? 0.0 : log(sum);
+      s_score[b] = (double)sc;
+      s_none[b] = bad || !(fabsf(sc) < INFINITY);
+      s_done[b] = done;
+    }
+  }
+  __syncthreads();
+  const int per = w.pieces * p.k, total = p.W * per;
+  auto key = [&](int i) -> Key96 {
+    const int b = i / per, j = i - b * per;
+    if (s_none[b]) return {0, 0};
+    if (s_done[b]) return j == 0 ? Key96{ordered(s_score[b]), ~((uint32_t)b * p.V + p.eos)} : Key96{0, 0};
+    const uint64_t q = w.best[((int64_t)n * p.W + b) * per + j];
+    if (q == 0) return {0, 0};
+    const double v = (((double)unordered((uint32_t)(q >> 32)) - s_top[b]) - s_log[b]) + s_score[b];
+    return {ordered(v), ~((uint32_t)b * p.V + ~(uint32_t)q)};
+  };
+  Key96 most{0, 0};
+  for (int i = tid; i < total; i += 256) {
+    const Key96 q = key(i);
+    if (q > most) most = q;
+  }
+  Key96 least = threshold(most, w.groups, s_group);
+  if (least.s == 0) least = {1, 0};
+  auto reach = [&](const Key96& t) {
+    int c = 0;
+    for (int i = tid; i < total; i += 256) c += !(t > key(i));
+    return wg_sum(c, s_count);
+  };
+  int count = reach(least);
+  if (count > HOLD) {   // reach(least) >= k > reach({high, 0}): first by the score, then by the index
+    uint64_t high = ~0ull;
+    while (count > HOLD && high - least.s > 1) {
+      const Key96 mid{least.s + (high - least.s) / 2, 0};
+      const int c = reach(mid);
+      if (c >= p.k) {
+        least = mid;
+        count = c;
+      } else {
+        high = mid.s;
+      }
+    }
+    uint64_t up = 1ull << 32;   // reach({least.s, up}) < k
+    while (count > HOLD) {
+      const Key96 mid{least.s, (uint32_t)(least.i + (up - least.i) / 2)};
+      const int c = reach(mid);
+      if (c >= p.k) {
+        least = mid;
+        count = c;
+      } else {
+        up = mid.i;
+      }
+    }
+  }
+  for (int i = tid; i < total; i += 256) {
+    const Key96 q = key(i);
+    if (!(least > q)) s_keys[atomicAdd(&s_used, 1)] = q;
+  }
+  __syncthreads();
+  for (int i = tid; i < count; i += 256) {
+    const Key96 q = s_keys[i];
+    int place = 0;
+    for (int j = 0; j < count; ++j) place += s_keys[j] > q;
+    if (place < p.k) {
+      const uint32_t at = ~q.i;
+      const int64_t to = (int64_t)n * p.k + place;
+      p.tokens[to] = (int32_t)(at % (uint32_t)p.V);
+      p.parents[to] = (int32_t)(at / (uint32_t)p.V);
+      p.new_scores[to] = (float)unordered(q.s);
+    }
+  }
+  for (int i = count + tid; i < p.k; i += 256) {
+    const int64_t to = (int64_t)n * p.k + i;
+    p.tokens[to] = p.parents[to] = -1;
+    p.new_scores[to] = -INFINITY;
+  }
+}
+
+template <typename F>
+void by_dtype(int dt, F f) {
+  if (dt == BF16) f(integral_constant<int, BF16>{});
+  else if (dt == FP32) f(integral_constant<int, FP32>{});
+  else f(integral_constant<int, FP16>{});
+}
+
+// Elements of a lane: many, or few where the GPU would not be filled so.
+int per_lane(int64_t rows, int64_t V) { return rows * ((V + 256 * 32 - 1) / (256 * 32)) >= 512 ? 32 : 8; }
+
+size_t lay_out(BeamWs& w, uint8_t* at, int64_t rows, int64_t V, int64_t k) {
+  const int per = per_lane(rows, V);
+  w.pieces = (int32_t)((V + 256 * per - 1) / (256 * per));
+  w.groups = 4;
+  while (w.groups < k) w.groups *= 2;
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* r = at ? at + used : nullptr;
+    used += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  const size_t items = (size_t)rows * w.pieces;
+  w.best = reinterpret_cast<uint64_t*>(take(items * k * sizeof(uint64_t)));
+  w.sum = reinterpret_cast<double*>(take(items * sizeof(double)));
+  w.top = reinterpret_cast<float*>(take(items * sizeof(float)));
+  return used;
+}
+
+}  // namespace
+
+size_t beam_workspace(int64_t N, int64_t W, int64_t V, int64_t k) {
+  BeamWs w{};
+  return lay_out(w, nullptr, N * W, V, k);
+}
+
+hipError_t launch_beam_select(const BeamParams& p, void* workspace, hipStream_t stream) {
+  if (p.N == 0) return hipSuccess;
+  BeamWs w{};
+  const int64_t rows = (int64_t)p.N * p.W;
+  lay_out(w, static_cast<uint8_t*>(workspace), rows, p.V, p.k);
+  const int64_t items = rows * w.pieces;
+  const unsigned blocks = (unsigned)(items < 65536 ? items : 65536);
+  by_dtype(p.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (per_lane(rows, p.V) == 32)
+      hipLaunchKernelGGL((kda_beam_piece_kernel<DT, 32>), dim3(blocks), dim3(256), 0, stream, p, w);
+    else
+      hipLaunchKernelGGL((kda_beam_piece_kernel<DT, 8>), dim3(blocks), dim3(256), 0, stream, p, w);
+  });
+  hipLaunchKernelGGL(kda_beam_join_kernel, dim3((unsigned)p.N), dim3(256), 0, stream, p, w);
+  return hipGetLastError();
+}
+
+}  // namespace kda

@@ -1,4 +1,4 @@
-// kda_cache.hip -- slots of a cache of states: copies, forks, frees, compaction (gfx950).
+// kda_cache.hip -- slots of a cache of states: copies, forks, frees, compaction, beams (gfx950).
 //
 // A plan kernel (one workgroup: S flags and n slot numbers are a few kilobytes) settles
 // which slot goes where, and a copy kernel moves the contents. Plans go by counts of free
@@ -177,6 +177,67 @@ hipError_t copy_slots(const CachePool& pool, const int32_t* src, const int32_t* 
   return hipGetLastError();
 }
 
+// The states of a sequence's W <= 64 beams after a step of beam search (rules in the header). A
+// workgroup takes a piece of one sequence's slots in one layer and makes all copies of it; each
+// settles for itself, in one wave, which slots become copies of which. No copy reads what another
+// writes: sources are slots that a beam continues in, targets slots of beams that no one continues.
+// Bound by memory where states are large.
+constexpr int BEAMS = 64;
+template <typename U>
+__global__ __launch_bounds__(256) void kda_cache_reorder_kernel(CachePool pool, size_t units, const int32_t* slots,
+                                                                const int32_t* parents, int32_t* new_slots, int64_t N, int W) {
+  __shared__ int from_s[BEAMS], to_s[BEAMS], n_s;
+  const int64_t pieces = (int64_t)((units + PIECE - 1) / PIECE), items = N * pool.layers * pieces;
+  const int tid = threadIdx.x;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t n = it / (pool.layers * pieces), r = it - n * (pool.layers * pieces);
+    const int64_t layer = r / pieces, piece = r - layer * pieces;
+    __syncthreads();   // the item before is done with the lists
+    if (tid < 64) {    // lane j: new beam j, and old beam j
+      const bool in = tid < W;
+      const int slot = in ? slots[n * W + tid] : -1;
+      int parent = in ? parents[n * W + tid] : -1;
+      if (parent < 0 || parent >= W) parent = -1;
+      bool first = parent >= 0, continued = false;
+      for (int j = 0; j < W; ++j) {
+        const int other = __builtin_amdgcn_readlane(parent, j);
+        if (other == parent && j < tid) first = false;
+        if (other == tid) continued = true;
+      }
+      const uint64_t below = ((uint64_t)1 << tid) - 1;
+      const uint64_t moved = __ballot(in && !first), free = __ballot(in && !continued);   // as many
+      // the free slots in ascending order of their beams
+      if (in && !continued) to_s[__popcll(free & below)] = slot;
+      const int rank = __popcll(moved & below);
+      const int old = __shfl(slot, parent < 0 ? 0 : parent, 64);
+      __builtin_amdgcn_wave_barrier();   // (a wave's accesses of shared memory are in order)
+      const int now = in && !first ? to_s[rank] : old;
+      if (in && !first) from_s[rank] = parent >= 0 ? old : -1;
+      if (tid == 0) n_s = __popcll(moved);
+      if (in && layer == 0 && piece == 0) new_slots[n * W + tid] = now;
+    }
+    __syncthreads();
+    U* base = static_cast<U*>(pool.base) + (size_t)layer * pool.slots * units;
+    const size_t u0 = (size_t)piece * PIECE + tid;
+    for (int i = 0; i < n_s; ++i) {
+      const int64_t from = from_s[i], to = to_s[i];
+      if (from < 0 || from >= pool.slots || to < 0 || to >= pool.slots || from == to) continue;
+      U v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const size_t u = u0 + 256 * j;
+        v[j] = U{};
+        if (u < units) v[j] = base[(size_t)from * units + u];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const size_t u = u0 + 256 * j;
+        if (u < units) __builtin_nontemporal_store(v[j], base + (size_t)to * units + u);
+      }
+    }
+  }
+}
+
 }  // namespace
 
 hipError_t launch_cache_copy(const CachePool& pool, const int32_t* src, const int32_t* dst, int64_t n, hipStream_t stream) {
@@ -204,6 +265,22 @@ hipError_t launch_cache_compact(const CachePool& pool, int32_t* used, int32_t* r
   hipLaunchKernelGGL(kda_cache_compact_plan_kernel, dim3(1), dim3(PLAN), 0, stream, used, S, remap, table, n, ws);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? copy_slots(pool, ws + 1, ws + 1 + S / 2 + 1, ws, S / 2, false, stream) : e;
+}
+
+hipError_t launch_cache_reorder(const CachePool& pool, const int32_t* slots, const int32_t* parents, int32_t* new_slots,
+                                int64_t N, int W, hipStream_t stream) {
+  if (N == 0) return hipSuccess;
+  const int unit = pool.slot_bytes % 16 == 0 ? 16 : pool.slot_bytes % 4 == 0 ? 4 : 1;
+  const size_t units = pool.slot_bytes / unit;
+  const double items = (double)N * pool.layers * (double)((units + PIECE - 1) / PIECE);
+  const dim3 grid(items < 8192.0 ? (unsigned)items : 8192u), wg(256);
+  if (unit == 16)
+    hipLaunchKernelGGL(kda_cache_reorder_kernel<u32x4>, grid, wg, 0, stream, pool, units, slots, parents, new_slots, N, W);
+  else if (unit == 4)
+    hipLaunchKernelGGL(kda_cache_reorder_kernel<uint32_t>, grid, wg, 0, stream, pool, units, slots, parents, new_slots, N, W);
+  else
+    hipLaunchKernelGGL(kda_cache_reorder_kernel<uint8_t>, grid, wg, 0, stream, pool, units, slots, parents, new_slots, N, W);
+  return hipGetLastError();
 }
 
 }  // namespace kda

@@ -4,7 +4,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
 #include "../../include/kda.h"
 #include "kda_api_util.h"
@@ -14,36 +13,16 @@
 namespace {
 
 using kda::aligned;
+using kda::any_unaligned;
+using kda::bad_dtype;
+using kda::check_pool;
+using kda::check_state;
+using kda::state_unaligned;
+using kda::status;
 
 using kda::MAX_SLOTS;
 constexpr int64_t MAX_D = (int64_t)1 << 24;          // of a row of layer norm
 constexpr int64_t MAX_CHANNELS = (int64_t)1 << 22;   // of the recurrence: 32-bit offsets inside a tile
-
-bool bad_state_code(int c) { return c != KDA_STATE_NONE && c != KDA_STATE_BF16 && c != KDA_STATE_FP32; }
-bool bad_dtype(int c) { return c != KDA_BF16 && c != KDA_FP32 && c != KDA_FP16; }
-
-// A state's pointer and its dtype code: both given or neither.
-int check_state(const void* p, int dtype) {
-  if (bad_state_code(dtype)) return KDA_ERR_DTYPE;
-  if ((dtype == KDA_STATE_NONE) != (p == nullptr)) return p ? KDA_ERR_DTYPE : KDA_ERR_NULL;
-  return KDA_OK;
-}
-
-bool any_unaligned(std::initializer_list<const void*> ps, size_t a) {
-  for (const void* p : ps)
-    if (p && !aligned(p, a)) return true;
-  return false;
-}
-
-// Whether a state of the recurrence is where the kernels can take it: an element at a time where
-// rows are no whole vectors of the token tensors (layers of a cache begin anywhere then), else as
-// many elements as such a vector holds.
-bool state_unaligned(const void* p, int state_dtype, int dtype, int64_t D) {
-  if (!p) return false;
-  const int64_t vec = dtype == KDA_FP32 ? 4 : 8;
-  const size_t elem = state_dtype == KDA_STATE_FP32 ? 4 : 2, all = (size_t)vec * elem;
-  return !aligned(p, D % vec != 0 ? elem : all < 16 ? all : 16);
-}
 
 // Checks that both directions of the recurrence share; a, b, c are its token tensors.
 int check_glr(const void* a, const void* b, const void* c, int dtype, const int64_t* cu, int64_t N, int64_t B, int64_t T,
@@ -71,16 +50,6 @@ kda::GlrParams glr_params(const void* x, const void* g, int dtype, const void* i
   p.tokens = (int32_t)(B * T);
   p.D = (int32_t)D;
   return p;
-}
-
-int status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
-
-int check_pool(const void* pool, int64_t L, int64_t S, size_t slot_bytes, int64_t n) {
-  if (!pool) return KDA_ERR_NULL;
-  if (L < 1 || S < 1 || S > MAX_SLOTS || slot_bytes < 1 || n < 0 || n > INT32_MAX) return KDA_ERR_SHAPE;
-  if (L > (int64_t)1 << 32 || (double)L * (double)S * (double)slot_bytes >= 4611686018427387904.0) return KDA_ERR_SHAPE;
-  if (!aligned(pool, 16)) return KDA_ERR_ALIGN;
-  return KDA_OK;
 }
 
 }  // namespace

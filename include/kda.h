@@ -1,8 +1,10 @@
 /*
  * kda.h -- C ABI of the MI355X (gfx950) Kimi Delta Attention forward library
  * (libkda.so), and of the operators beside it that a recurrent layer trains and
- * serves with: the gated linear recurrence (kda_glr_*), layer norm
- * (kda_layernorm_*), and caches of states in slots (kda_cache_*, kda_fwd_slots).
+ * serves with: the gated linear recurrence (kda_glr_*), the short convolution and
+ * the selective state space scan (kda_conv_*, kda_ssm_*), layer norm and the
+ * root-mean-square norm (kda_layernorm_*, kda_rmsnorm_*), caches of states in slots
+ * (kda_cache_*, kda_fwd_slots), and beam search over them (kda_beam_select).
  *
  * The operation (per sequence n and head h, state S of V x K, K contiguous):
  *   q^, k^ = L2-normalised q, k over K (x / sqrt(sum x^2 + 1e-6))
@@ -58,8 +60,8 @@ enum kda_status {
     KDA_OK = 0,
     KDA_ERR_NULL = 1,      /* a required pointer is NULL                           */
     KDA_ERR_SHAPE = 2,     /* K != 128, V != 128, H < 1, T < 0, B < 1, B != 1 with
-                              cu_seqlens, N < 1 with cu_seqlens, D, S, L, M or n
-                              out of range, size overflow                           */
+                              cu_seqlens, N < 1 with cu_seqlens, D, E, G, S, L, M, W, k,
+                              n or group out of range, size overflow                */
     KDA_ERR_DTYPE = 3,     /* unknown dtype or state dtype code, or initial and final
                               state given with different dtypes                     */
     KDA_ERR_VALUE = 4,     /* lower_bound outside [-5, 0] or not finite (safe gate),
@@ -276,8 +278,8 @@ size_t kda_noalloc_capacity(void);
  * the calls can be captured into a graph.
  *
  * Rules of every kda_cache_* call: S <= 2^24, L >= 1, slot_bytes >= 1; pool is
- * aligned to 16 bytes, used, src, dst, slots, remap and table to 4; the arrays do
- * not overlap each other (KDA_ERR_VALUE where one that is written is given twice).
+ * aligned to 16 bytes, used, src, dst, slots, remap, table, parents and new_slots to 4; the
+ * arrays do not overlap each other (KDA_ERR_VALUE where one that is written is given twice).
  * n may be 0 (nothing is done; the index arrays may then be NULL). A slot number
  * outside [0, S) is never followed: what it means is said at each call.
  *
@@ -306,6 +308,18 @@ size_t kda_noalloc_capacity(void);
  *   their new ones, -1 for free slots and numbers outside [0, S). workspace:
  *   kda_cache_workspace_size(S) bytes, 256-byte aligned.
  *
+ * kda_cache_reorder: the states of N sequences' W beams follow a step of beam
+ *   search, in which new beam j of sequence n continues beam parents[n][j] (as
+ *   kda_beam_select gives them). slots, parents and new_slots are int32 [N, W]; 1 <= W
+ *   <= 64. slots[n][b] is beam b's slot, no slot twice. Of the new beams that continue
+ *   the same beam the first keeps its slot, and the others, in their order, get the
+ *   slots of the beams that no one continues, in ascending order of b, as copies in
+ *   every layer: new_slots[n] (OUTPUT) is slots[n] in another order, and only what is
+ *   needed twice is copied. A new beam with a parent outside [0, W) gets such a slot too,
+ *   with its contents as they were; a slot number outside [0, S) is given on and nothing is
+ *   copied from or to it. N may be 0. Pools under the same slot numbers each take a call
+ *   with the same slots and parents.
+ *
  * A pool has slots of one size. Two of them under the same slot numbers (the states
  * of KDA and those of a recurrence) are forked by kda_cache_fork on one and
  * kda_cache_copy with the same src and dst on the other, which leaves the slots of
@@ -321,6 +335,8 @@ int kda_cache_fork(void *pool, int64_t L, int64_t S, size_t slot_bytes, int32_t 
 int kda_cache_free(int32_t *used, int64_t S, const int32_t *slots, int64_t n, void *stream);
 int kda_cache_compact(void *pool, int64_t L, int64_t S, size_t slot_bytes, int32_t *used, int32_t *remap,
                       int32_t *table, int64_t n, void *workspace, size_t workspace_bytes, void *stream);
+int kda_cache_reorder(void *pool, int64_t L, int64_t S, size_t slot_bytes, const int32_t *slots,
+                      const int32_t *parents, int32_t *new_slots, int64_t N, int64_t W, void *stream);
 
 /*
  * kda_fwd_slots -- kda_fwd_recurrent_ex with the states in the slots of a cache's
@@ -343,7 +359,8 @@ int kda_fwd_slots(const void *q, const void *k, const void *v, const void *g, co
 enum kda_dtype {
     KDA_BF16 = 1,
     KDA_FP32 = 2,
-    KDA_FP16 = 3
+    KDA_FP16 = 3,
+    KDA_E4M3 = 4   /* 8 bits, 3 of them mantissa, +-448 at most: y of kda_rmsnorm_fwd only */
 };
 
 /* ---- gated linear recurrence -----------------------------------------------
@@ -449,6 +466,172 @@ int kda_layernorm_fwd(const void *x, const float *weight, const float *bias, flo
 int kda_layernorm_bwd(const void *dy, const void *x, const float *weight, const float *mean, const float *rstd,
                       void *dx, int dtype, float *d_weight, float *d_bias, int64_t M, int64_t D, void *workspace,
                       size_t workspace_bytes, void *stream);
+
+/* ---- root-mean-square norm ------------------------------------------------------
+ *
+ * Per row of D elements, with the sum s = x + residual (x alone without one) and
+ * r = 1 / sqrt(mean(s^2) + eps):
+ *     y = s r weight,   residual_out = s
+ * and from dy, with a = dy weight and d_residual, the gradient of residual_out:
+ *     dx = r (a - s r^2 mean(a s)) + d_residual     (of x and of the residual alike)
+ *     d_weight = sum over rows of dy s r
+ * Statistics and sums are fp32 (the square of an |s| beyond 1.8e19 overflows: r is then 0);
+ * every output is rounded once, y and r from the sum before it is rounded to residual_out.
+ *
+ *   x, residual, residual_out, dy, d_residual, dx
+ *                     [M, D] in `dtype` (KDA_BF16, KDA_FP32 or KDA_FP16), M >= 0,
+ *                     1 <= D <= 2^24. residual, residual_out and d_residual may be NULL.
+ *                     kda_rmsnorm_bwd's x is the sum: residual_out where there was a residual.
+ *   y, y_dtype        [M, D] in `dtype`, or in KDA_E4M3 with scales
+ *   scales, group     fp32 [M, ceil(D / group)] with KDA_E4M3, else NULL and 0: y holds what
+ *                     the values are in units of their scale, the largest of the group's
+ *                     |values| / 448 (1 where that is 0; NaN, or infinity with infinite
+ *                     values among finite ones, where it is). A group is 128 neighbouring
+ *                     elements (the row's last one the rest), or the row: group is 128 or D.
+ *   weight            fp32 [D], or NULL (ones)
+ *   eps               finite, >= 0
+ *   rstd              fp32 [M]: written by kda_rmsnorm_fwd where not NULL, read by
+ *                     kda_rmsnorm_bwd (needed there where M > 0)
+ *   d_weight          fp32 [D] or NULL, overwritten (zeros where M = 0), its sums in an order
+ *                     of their own that no timing changes
+ *   dx                may be NULL (only the weight's gradient is wanted)
+ *   workspace         caller-owned, kda_rmsnorm_workspace_size(M, D) bytes, 256-byte aligned,
+ *                     needed where d_weight is given
+ * y (of `dtype`) and residual_out may each be x or residual, but not the same; dx may be dy, x
+ * or d_residual; other outputs do not overlap inputs.
+ */
+size_t kda_rmsnorm_workspace_size(int64_t M, int64_t D);
+int kda_rmsnorm_fwd(const void *x, const void *residual, const float *weight, float eps, void *y, int y_dtype,
+                    float *scales, int64_t group, void *residual_out, int dtype, float *rstd, int64_t M, int64_t D,
+                    void *stream);
+int kda_rmsnorm_bwd(const void *dy, const void *x, const float *weight, const float *rstd, const void *d_residual,
+                    void *dx, int dtype, float *d_weight, int64_t M, int64_t D, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* ---- short causal convolution ---------------------------------------------------
+ *
+ * Per sequence and channel, over the last W tokens (before the first one: the initial
+ * state's, or zeros):
+ *     u_t = bias + sum over j of weight[j] x_{t - W + 1 + j},   y_t = u_t or SiLU(u_t)
+ * where SiLU(u) = u / (1 + exp(-u)), with KDA_CONV_SILU. Sums are fp32; every output is
+ * rounded once.
+ *
+ *   x, y, dy, dx      [B, T, D] in `dtype`; T may be 0 (they may then be NULL)
+ *   weight            fp32 [D, W], W = 2, 3 or 4
+ *   bias              fp32 [D], or NULL (zeros)
+ *   flags             KDA_CONV_SILU or 0
+ *   initial_state, final_state, their dtypes, cu_seqlens, N, B, T
+ *                     as for kda_glr_fwd, alignment and uncovered tokens included, with states
+ *                     [B|N, W - 1, D]: the W - 1 inputs before the sequence's next token, the
+ *                     oldest first. final_state may be initial_state.
+ *   d_weight, d_bias  fp32 [D, W], [D], or NULL; overwritten, their sums in an order of their
+ *                     own that no timing changes
+ *   d_final, d_initial and their dtypes
+ *                     as for kda_glr_bwd, [B|N, W - 1, D]
+ *   workspace         caller-owned, kda_conv_workspace_size(B, T, D, W) bytes, 256-byte
+ *                     aligned, needed where d_weight or d_bias is given
+ * Outputs do not overlap inputs, except as said. D is 1 to 2^22.
+ *
+ * kda_conv_step: one token for each of N sequences, x, y [N, D], states in the slots of a
+ * cache's layer [S, W - 1, D] by the rules of kda_glr_step.
+ */
+enum kda_conv_flags { KDA_CONV_SILU = 1 };
+size_t kda_conv_workspace_size(int64_t B, int64_t T, int64_t D, int64_t W);
+int kda_conv_fwd(const void *x, const float *weight, const float *bias, void *y, int dtype, int64_t W, uint32_t flags,
+                 const void *initial_state, int initial_dtype, void *final_state, int final_dtype,
+                 const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t D, void *stream);
+int kda_conv_bwd(const void *x, const float *weight, const float *bias, const void *dy, int dtype, int64_t W,
+                 uint32_t flags, const void *initial_state, int initial_dtype, const void *d_final, int d_final_dtype,
+                 void *dx, float *d_weight, float *d_bias, void *d_initial, int d_initial_dtype,
+                 const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t D, void *workspace,
+                 size_t workspace_bytes, void *stream);
+int kda_conv_step(const void *x, const float *weight, const float *bias, void *y, int dtype, int64_t W, uint32_t flags,
+                  void *state, int state_dtype, int64_t S, const int32_t *in_slots, const int32_t *out_slots,
+                  int64_t N, int64_t D, void *stream);
+
+/* ---- selective state space scan ---------------------------------------------------
+ *
+ * Per sequence and channel d, with E states h (of before its first token: the initial
+ * state's, or zeros), d in group c = d / (D / G), and s_t = dt_t + dt_bias, or
+ * log(1 + exp(dt_t + dt_bias)) with KDA_SSM_SOFTPLUS:
+ *     h_t[e] = exp(s_t A[e]) h_{t-1}[e] + s_t x_t B_t[c][e]
+ *     y_t = (sum over e of C_t[c][e] h_t[e] + skip x_t) SiLU(z_t)
+ * (without skip, z or dt_bias: without their term or factor). The backward pass gives the
+ * gradients of all of them from dy and d_final. States and sums are fp32 throughout, every
+ * output is rounded once. Once a state is infinite or NaN, what its channel gives for the
+ * rest of its sequence is unspecified.
+ *
+ *   x, dt, z, y, dy, dx, d_dt, d_z
+ *                     [B, T, D] in `dtype`; T may be 0 (all tokens' tensors may then be NULL)
+ *   A, dA             fp32 [D, E], 1 <= E <= 64; A < 0 forgets
+ *   Bm, Cm, dB, dC    [B, T, G, E] in `dtype`; G >= 1 divides D
+ *   skip, dt_bias, d_skip, d_dt_bias
+ *                     fp32 [D], or NULL; a gradient is given only where its input is
+ *                     (KDA_ERR_VALUE otherwise; d_z likewise), and may be NULL
+ *   flags             KDA_SSM_SOFTPLUS or 0
+ *   initial_state, final_state, their dtypes, cu_seqlens, N, B, T
+ *                     as for kda_glr_fwd, uncovered tokens included, with states [B|N, D, E]
+ *                     aligned to 4 of their elements where E is a multiple of 4, else to one.
+ *                     final_state may be initial_state.
+ *   carry             fp32 [kda_ssm_carry_rows(B, T), D, E]: the state that enters every 64th
+ *                     of the B * T packed tokens. kda_ssm_fwd writes it where it is not NULL;
+ *                     kda_ssm_bwd needs the one of the same inputs and boundaries. Its
+ *                     contents where a sequence begins are unspecified.
+ *   d_final, d_initial and their dtypes
+ *                     as for kda_glr_bwd, [B|N, D, E]
+ *   dx, d_dt, dA, dB, dC
+ *                     all given, overwritten; the sums over channels and tokens are in an order
+ *                     of their own that no timing changes
+ *   workspace         caller-owned, kda_ssm_workspace_size(B, T, D, E, G, N, backward) bytes (N = 0
+ *                     without cu_seqlens; backward: 0 or 1, the direction), 256-byte aligned;
+ *                     contents need no initialisation and are clobbered
+ * Outputs do not overlap inputs, except as said. D is 1 to 2^20.
+ *
+ * kda_ssm_step: one token for each of N sequences, x, dt, z, y [N, D], Bm, Cm [N, G, E],
+ * states in the slots of a cache's layer [S, D, E] by the rules of kda_glr_step.
+ */
+enum kda_ssm_flags { KDA_SSM_SOFTPLUS = 1 };
+int64_t kda_ssm_carry_rows(int64_t B, int64_t T);   /* 0 for invalid sizes */
+size_t kda_ssm_workspace_size(int64_t B, int64_t T, int64_t D, int64_t E, int64_t G, int64_t N, int backward);
+int kda_ssm_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *skip,
+                const void *z, const float *dt_bias, void *y, int dtype, uint32_t flags, const void *initial_state,
+                int initial_dtype, void *final_state, int final_dtype, float *carry, const int64_t *cu_seqlens,
+                int64_t N, int64_t B, int64_t T, int64_t D, int64_t E, int64_t G, void *workspace,
+                size_t workspace_bytes, void *stream);
+int kda_ssm_bwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *skip,
+                const void *z, const float *dt_bias, const void *dy, int dtype, uint32_t flags, const float *carry,
+                const void *initial_state, int initial_dtype, const void *d_final, int d_final_dtype, void *dx,
+                void *d_dt, float *dA, void *dB, void *dC, float *d_skip, void *d_z, float *d_dt_bias, void *d_initial,
+                int d_initial_dtype, const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t D, int64_t E,
+                int64_t G, void *workspace, size_t workspace_bytes, void *stream);
+int kda_ssm_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *skip,
+                 const void *z, const float *dt_bias, void *y, int dtype, uint32_t flags, void *state, int state_dtype,
+                 int64_t S, const int32_t *in_slots, const int32_t *out_slots, int64_t N, int64_t D, int64_t E,
+                 int64_t G, void *stream);
+
+/* ---- beam search ------------------------------------------------------------------
+ *
+ * kda_beam_select -- the k best continuations of every sequence's W beams. Continuation v of
+ * beam b of sequence n has the score
+ *     scores[n][b] + logits[n][b][v] - log(sum over v' of exp(logits[n][b][v']))
+ * computed in 64 bits; the best come first, equal ones in the order of b, then v. A beam with
+ * finished[n][b] != 0 has one continuation, v = eos, at its score as it is (its logits are
+ * not read). Only finite scores count: a logit of -infinity is no continuation, and a beam
+ * with a NaN or +infinite logit, or whose score is infinite or NaN, has none.
+ *   logits            [N, W, V] in `dtype`; N >= 0, 1 <= W <= 64, 1 <= V <= 2^24, N W < 2^24
+ *   scores            fp32 [N, W]
+ *   finished          int32 [N, W], or NULL: none is
+ *   eos               0 <= eos < V (of use with finished only)
+ *   tokens, parents   int32 [N, k]: v and b of the continuations; -1 where there are fewer than
+ *                     k. 1 <= k <= 64.
+ *   new_scores        fp32 [N, k]: their scores, rounded once; -infinity there. May be scores
+ *                     where k = W.
+ *   workspace         caller-owned, kda_beam_workspace_size(N, W, V, k) bytes, 256-byte aligned
+ */
+size_t kda_beam_workspace_size(int64_t N, int64_t W, int64_t V, int64_t k);
+int kda_beam_select(const void *logits, int dtype, const float *scores, const int32_t *finished, int64_t eos,
+                    int32_t *tokens, int32_t *parents, float *new_scores, int64_t N, int64_t W, int64_t V, int64_t k,
+                    void *workspace, size_t workspace_bytes, void *stream);
 
 /* kda_status_string -- static description of a status code (never NULL). */
 const char *kda_status_string(int status);

@@ -1,0 +1,231 @@
+"""Refusals of a state space layer's operators, without a GPU: every argument that the header
+rules out is reported with its status before anything is launched (fake device pointers are
+never dereferenced), sizes are as documented, and the Python wrappers check what they can."""
+import os
+import re
+
+import pytest
+import torch
+
+import gated_delta_rule_87_amd as kda
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, ENULL, ESHAPE, EDTYPE, EVALUE, EALIGN, EWS, EHIP, ECAP = range(9)
+BIG = 1 << 50
+
+
+def fake(i):
+    return 0x10000000 + (i << 24)
+
+
+def call(name, defaults, **kw):
+    a = dict(defaults)
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    return getattr(kda.lib(), name)(*a.values())
+
+
+def test_signatures_match_the_header():
+    """As many arguments as the header declares, in the types that it declares."""
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "kda.h")).read(), flags=re.S)
+    L = kda.lib()
+    from gated_delta_rule_87_amd._layer import F, I, I64, P, SZ, U32
+    kinds = {"int": I, "int64_t": I64, "size_t": SZ, "float": F, "uint32_t": U32}
+    for name in ("kda_rmsnorm_workspace_size", "kda_rmsnorm_fwd", "kda_rmsnorm_bwd", "kda_conv_workspace_size", "kda_conv_fwd",
+                 "kda_conv_bwd", "kda_conv_step", "kda_ssm_carry_rows", "kda_ssm_workspace_size", "kda_ssm_fwd", "kda_ssm_bwd",
+                 "kda_ssm_step", "kda_beam_workspace_size", "kda_beam_select", "kda_cache_reorder"):
+        m = re.search(r"(\w+)\s+%s\s*\(([^)]*)\)" % name, src)
+        assert m, name
+        want = [P if "*" in a else kinds[a.split()[-2]] for a in m.group(2).split(",")]
+        assert want == getattr(L, name).argtypes, name
+        assert kinds[m.group(1)] is getattr(L, name).restype, name
+
+
+RF = dict(x=fake(1), res=fake(2), w=fake(3), eps=1e-6, y=fake(4), yd=1, scales=None, group=0, ro=fake(5), dtype=1, rstd=fake(6),
+          M=10, D=200, stream=None)
+RB = dict(dy=fake(1), x=fake(2), w=fake(3), rstd=fake(4), dres=fake(5), dx=fake(6), dtype=1, dw=fake(7), M=10, D=200, ws=fake(9),
+          wsb=BIG, stream=None)
+
+
+def test_rmsnorm_refusals():
+    go = lambda **kw: call("kda_rmsnorm_fwd", RF, **kw)  # noqa: E731
+    for k in ("x", "y"):
+        assert go(**{k: None}) == ENULL, k
+    for k in ("x", "res", "w", "y", "ro", "rstd"):
+        assert go(**{k: RF[k] + 4}) == EALIGN, k
+    for bad in (dict(M=-1), dict(D=0), dict(D=(1 << 24) + 1), dict(M=1 << 55), dict(group=128), dict(group=200)):
+        assert go(**bad) == ESHAPE, bad
+    assert go(dtype=0) == EDTYPE and go(dtype=4, yd=4) == EDTYPE and go(yd=2) == EDTYPE and go(yd=5) == EDTYPE
+    assert go(scales=fake(8)) == EVALUE and go(eps=-1.0) == EVALUE and go(eps=float("nan")) == EVALUE
+    assert go(ro=RF["y"]) == EVALUE
+    e8 = dict(yd=4, scales=fake(8), group=128)
+    assert go(**{**e8, "scales": None}) == ENULL and go(**{**e8, "group": 64}) == ESHAPE and go(**{**e8, "group": 0}) == ESHAPE
+    assert go(**{**e8, "y": RF["x"]}) == EVALUE and go(**{**e8, "y": RF["res"]}) == EVALUE
+    assert go(**{**e8, "scales": fake(8) + 4}) == EALIGN
+    assert go(M=0, x=None, y=None, res=None, ro=None) == OK
+    go = lambda **kw: call("kda_rmsnorm_bwd", RB, **kw)  # noqa: E731
+    for k in ("dy", "x", "rstd"):
+        assert go(**{k: None}) == ENULL, k
+    for k in ("dy", "x", "w", "rstd", "dres", "dx", "dw"):
+        assert go(**{k: RB[k] + 4}) == EALIGN, k
+    assert go(M=-1) == ESHAPE and go(D=0) == ESHAPE and go(dtype=4) == EDTYPE
+    need = kda.rmsnorm_workspace_size(10, 200)
+    assert need >= 800 and go(ws=None) == EWS and go(wsb=need - 1) == EWS and go(ws=fake(9) + 16) == EALIGN
+    assert go(dx=None, dw=None) == OK and kda.rmsnorm_workspace_size(3, 0) == 0
+
+
+CF = dict(x=fake(1), w=fake(2), b=fake(3), y=fake(4), dtype=1, W=4, flags=1, h0=None, h0d=0, hT=None, hTd=0, cu=None, N=0, B=2,
+          T=100, D=64, stream=None)
+CB = dict(x=fake(1), w=fake(2), b=fake(3), dy=fake(4), dtype=1, W=4, flags=1, h0=None, h0d=0, df=None, dfd=0, dx=fake(5), dw=fake(6),
+          db=fake(7), d0=None, d0d=0, cu=None, N=0, B=2, T=100, D=64, ws=fake(9), wsb=BIG, stream=None)
+CS = dict(x=fake(1), w=fake(2), b=fake(3), y=fake(4), dtype=1, W=4, flags=1, state=fake(5), sd=2, S=8, src=fake(6), dst=fake(7), N=3,
+          D=64, stream=None)
+TOKENS = (dict(B=0), dict(T=-1), dict(D=0), dict(cu=fake(11), N=2), dict(cu=fake(11), N=0, B=1), dict(B=1 << 20, T=1 << 20),
+          dict(T=1 << 62), dict(B=1 << 62, T=4), dict(cu=fake(11), N=1 << 40, B=1))
+
+
+@pytest.mark.parametrize("name,d,null,align", [
+    ("kda_conv_fwd", CF, ("x", "w", "y"), ("x", "w", "b", "y")),
+    ("kda_conv_bwd", CB, ("x", "w", "dy", "dx"), ("x", "w", "b", "dy", "dx", "dw", "db")),
+], ids=["fwd", "bwd"])
+def test_conv_refusals(name, d, null, align):
+    go = lambda **kw: call(name, d, **kw)  # noqa: E731
+    for k in null:
+        assert go(**{k: None}) == ENULL, k
+    for k in align:
+        assert go(**{k: d[k] + 4}) == EALIGN, k
+    for bad in TOKENS + (dict(W=1), dict(W=5), dict(D=(1 << 22) + 1), dict(T=1 << 24, D=1 << 22)):
+        assert go(**bad) == ESHAPE, bad
+    assert go(dtype=4) == EDTYPE and go(flags=2) == EVALUE and go(cu=fake(11) + 4, N=2, B=1) == EALIGN
+    states = [("h0", "h0d"), ("hT", "hTd")] if name == "kda_conv_fwd" else [("h0", "h0d"), ("df", "dfd"), ("d0", "d0d")]
+    for p, c in states:
+        assert go(**{p: fake(8), c: 0}) == EDTYPE and go(**{p: fake(8), c: 3}) == EDTYPE and go(**{p: None, c: 2}) == ENULL
+        assert go(**{p: fake(8) + 4, c: 2}) == EALIGN
+    if name == "kda_conv_fwd":
+        assert go(y=d["x"]) == EVALUE and go(h0=fake(8), h0d=1, hT=fake(8), hTd=2) == EDTYPE
+        return
+    assert go(dx=d["x"]) == EVALUE and go(dx=d["dy"]) == EVALUE
+    assert go(df=fake(8), dfd=2, d0=fake(8), d0d=2) == EVALUE and go(h0=fake(8), h0d=2, d0=fake(8), d0d=2) == EVALUE
+    need = kda.conv_workspace_size(2, 100, 64, 4)
+    assert need > 0 and go(ws=None) == EWS and go(wsb=need - 1) == EWS and go(ws=fake(9) + 16) == EALIGN
+
+
+def test_conv_step_refusals():
+    go = lambda **kw: call("kda_conv_step", CS, **kw)  # noqa: E731
+    for k in ("x", "w", "y", "state", "src", "dst"):
+        assert go(**{k: None}) == ENULL, k
+        assert go(**{k: CS[k] + 2}) == EALIGN, k
+    for bad in (dict(N=-1), dict(N=1 << 40), dict(D=0), dict(W=5), dict(S=0), dict(S=(1 << 24) + 1)):
+        assert go(**bad) == ESHAPE, bad
+    assert go(dtype=5) == EDTYPE and go(sd=0) == EDTYPE and go(sd=3) == EDTYPE and go(flags=4) == EVALUE
+    assert go(N=0, x=None, y=None, src=None, dst=None) == OK
+
+
+def test_conv_sizes():
+    for bad in ((0, 5, 4, 4), (1, -1, 4, 4), (1, 5, 0, 4), (1, 5, 4, 1), (1, 5, 4, 5), (1 << 40, 1 << 40, 4, 4), (1, 1 << 24, 1 << 22, 4)):
+        assert kda.conv_workspace_size(*bad) == 0, bad
+    assert kda.conv_workspace_size(1, 0, 4, 4) == 0 and kda.conv_workspace_size(1, 1, 1, 2) >= 12
+
+
+SF = dict(x=fake(1), dt=fake(2), A=fake(3), Bm=fake(4), Cm=fake(5), skip=fake(6), z=fake(7), bias=fake(8), y=fake(9), dtype=1, flags=1,
+          h0=None, h0d=0, hT=None, hTd=0, carry=None, cu=None, N=0, B=2, T=100, D=64, E=16, G=2, ws=fake(30), wsb=BIG, stream=None)
+SB = dict(x=fake(1), dt=fake(2), A=fake(3), Bm=fake(4), Cm=fake(5), skip=fake(6), z=fake(7), bias=fake(8), dy=fake(9), dtype=1, flags=1,
+          carry=fake(10), h0=None, h0d=0, df=None, dfd=0, dx=fake(12), ddt=fake(13), dA=fake(14), dB=fake(15), dC=fake(16),
+          dskip=fake(17), dz=fake(18), dbias=fake(19), d0=None, d0d=0, cu=None, N=0, B=2, T=100, D=64, E=16, G=2, ws=fake(30),
+          wsb=BIG, stream=None)
+SS = dict(x=fake(1), dt=fake(2), A=fake(3), Bm=fake(4), Cm=fake(5), skip=fake(6), z=fake(7), bias=fake(8), y=fake(9), dtype=1, flags=1,
+          state=fake(10), sd=2, S=8, src=fake(12), dst=fake(13), N=3, D=64, E=16, G=2, stream=None)
+SIZES = (dict(D=0), dict(D=(1 << 20) + 2), dict(E=0), dict(E=65), dict(G=0), dict(G=3), dict(G=128))
+
+
+@pytest.mark.parametrize("name,d", [("kda_ssm_fwd", SF), ("kda_ssm_bwd", SB)], ids=["fwd", "bwd"])
+def test_ssm_refusals(name, d):
+    go = lambda **kw: call(name, d, **kw)  # noqa: E731
+    fwd = name == "kda_ssm_fwd"
+    must = ("x", "dt", "A", "Bm", "Cm") + (("y",) if fwd else ("dy", "carry", "dx", "ddt", "dA", "dB", "dC"))
+    for k in must:
+        assert go(**{k: None}) == ENULL, k
+    for k in must + ("skip", "z", "bias") + (() if fwd else ("dskip", "dz", "dbias")):
+        assert go(**{k: d[k] + 4}) == EALIGN, k
+    for bad in TOKENS + SIZES:
+        assert go(**bad) == ESHAPE, bad
+    assert go(dtype=4) == EDTYPE and go(flags=2) == EVALUE and go(cu=fake(20) + 4, N=2, B=1) == EALIGN
+    for p, c in ([("h0", "h0d"), ("hT", "hTd")] if fwd else [("h0", "h0d"), ("df", "dfd"), ("d0", "d0d")]):
+        assert go(**{p: fake(21), c: 0}) == EDTYPE and go(**{p: fake(21), c: 3}) == EDTYPE and go(**{p: None, c: 2}) == ENULL
+        assert go(**{p: fake(21) + 8, c: 2}) == EALIGN and go(**{p: fake(21) + 4, c: 1}) == EALIGN
+    if fwd:
+        assert go(h0=fake(21), h0d=1, hT=fake(21), hTd=2) == EDTYPE and go(carry=fake(21) + 4) == EALIGN
+        assert all(go(y=d[k]) == EVALUE for k in ("x", "dt", "z"))
+    else:
+        assert go(df=fake(21), dfd=2, d0=fake(21), d0d=2) == EVALUE and go(h0=fake(21), h0d=2, d0=fake(21), d0d=2) == EVALUE
+        assert go(skip=None) == EVALUE and go(z=None) == EVALUE and go(bias=None) == EVALUE
+        assert all(go(**{o: d[k]}) == EVALUE for o in ("dx", "ddt", "dz") for k in ("x", "dt", "z", "dy"))
+    need = kda.ssm_workspace_size(2, 100, 64, 16, 2, 0, not fwd)
+    assert need > 0 and go(ws=None) == EWS and go(wsb=need - 1) == EWS and go(ws=fake(30) + 16) == EALIGN
+
+
+def test_ssm_step_refusals():
+    go = lambda **kw: call("kda_ssm_step", SS, **kw)  # noqa: E731
+    for k in ("x", "dt", "A", "Bm", "Cm", "y", "state", "src", "dst"):
+        assert go(**{k: None}) == ENULL, k
+        assert go(**{k: SS[k] + 2}) == EALIGN, k
+    for bad in SIZES + (dict(N=-1), dict(N=1 << 40), dict(S=0), dict(S=(1 << 24) + 1)):
+        assert go(**bad) == ESHAPE, bad
+    assert go(dtype=5) == EDTYPE and go(sd=0) == EDTYPE and go(sd=3) == EDTYPE and go(flags=4) == EVALUE
+    assert go(state=SS["state"] + 8) == EALIGN
+    assert go(N=0, x=None, dt=None, Bm=None, Cm=None, y=None, src=None, dst=None) == OK
+
+
+def test_ssm_sizes():
+    assert kda.ssm_carry_shape(2, 100, 5, 7) == (4, 5, 7) and kda.ssm_carry_shape(1, 64, 5, 7)[0] == 1
+    assert kda.ssm_carry_shape(0, 5, 1, 1)[0] == 0 and kda.ssm_carry_shape(1, -1, 1, 1)[0] == 0
+    for bad in ((0, 5, 4, 4, 1), (1, -1, 4, 4, 1), (1, 5, 0, 4, 1), (1, 5, 4, 65, 1), (1, 5, 4, 4, 3), (1 << 40, 1 << 40, 4, 4, 1),
+                (2, 5, 4, 4, 1, 3), (1, 5, 4, 4, 1, -1)):
+        assert kda.ssm_workspace_size(*bad) == 0 and kda.ssm_workspace_size(*bad, backward=True) == 0, bad
+
+
+BS = dict(logits=fake(1), dtype=1, scores=fake(2), fin=None, eos=0, tokens=fake(3), parents=fake(4), new=fake(5), N=2, W=4, V=1000,
+          k=4, ws=fake(6), wsb=BIG, stream=None)
+
+
+def test_beam_refusals():
+    go = lambda **kw: call("kda_beam_select", BS, **kw)  # noqa: E731
+    for k in ("logits", "scores", "tokens", "parents", "new"):
+        assert go(**{k: None}) == ENULL, k
+        assert go(**{k: BS[k] + 2}) == EALIGN, k
+    for bad in (dict(N=-1), dict(W=0), dict(W=65), dict(V=0), dict(V=(1 << 24) + 1), dict(k=0), dict(k=65), dict(N=1 << 22),
+                dict(N=1 << 62)):
+        assert go(**bad) == ESHAPE, bad
+    assert go(dtype=4) == EDTYPE and go(fin=fake(7), eos=1000) == EVALUE and go(fin=fake(7), eos=-1) == EVALUE
+    assert go(parents=BS["tokens"]) == EVALUE and go(new=BS["scores"], k=3) == EVALUE and go(fin=BS["tokens"]) == EVALUE
+    need = kda.beam_workspace_size(2, 4, 1000, 4)
+    assert need > 0 and go(ws=None) == EWS and go(wsb=need - 1) == EWS and go(ws=fake(6) + 16) == EALIGN
+    assert go(N=0, logits=None, scores=None, tokens=None, parents=None, new=None) == OK
+    assert kda.beam_workspace_size(2, 65, 1000, 4) == 0
+
+
+def test_reorder_refusals():
+    d = dict(pool=fake(1), L=2, S=8, size=64, slots=fake(2), parents=fake(3), new=fake(4), N=2, W=4, stream=None)
+    go = lambda **kw: call("kda_cache_reorder", d, **kw)  # noqa: E731
+    for k in ("pool", "slots", "parents", "new"):
+        assert go(**{k: None}) == ENULL, k
+        assert go(**{k: d[k] + 2}) == EALIGN, k
+    for bad in (dict(L=0), dict(S=0), dict(size=0), dict(N=-1), dict(N=1 << 25), dict(W=0), dict(W=65)):
+        assert go(**bad) == ESHAPE, bad
+    assert go(new=d["slots"]) == EVALUE and go(new=d["parents"]) == EVALUE and go(N=0, slots=None, parents=None, new=None) == OK
+
+
+def test_wrappers_check_before_the_device():
+    x = torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.rmsnorm_fwd(x, None, 1e-5, x)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.conv_fwd(x, torch.zeros(8, 4), None, x)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.ssm_fwd(x, x, torch.zeros(8, 4), x, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.beam_select(x, x, x, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.cache_reorder(x, x, x, x)
+    with pytest.raises(TypeError):
+        kda.conv_step([1.0], None, None, None, None, None, None)
