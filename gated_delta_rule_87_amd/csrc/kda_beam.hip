@@ -41,8 +41,8 @@ __device__ __forceinline__ double unordered(uint64_t u) {
   return __builtin_bit_cast(double, u >> 63 ? u & ~(1ull << 63) : ~u);
 }
 
-// exp(t), t <= 0: 2^n 2^f, |f| <= 1/2, a Taylor series of nine terms (7e-12). Below -40 it is
-// nothing beside the sum, which is at least 1.
+// exp(t), t <= 0 or NaN: 2^n 2^f, |f| <= 1/2, a Taylor series of nine terms (7e-12). Below -40 it is
+// nothing beside the sum, which is at least 1 (2^24 of them are 7e-11).
 __device__ __forceinline__ double exp_below(double t) {
   t = t < -40.0 ? -40.0 : t;
   const double y = t * 1.4426950408889634074, n = __builtin_rint(y), f = (y - n) * 0.69314718055994530942;
@@ -111,7 +111,7 @@ struct Key64 {
 
 // PER elements of a lane. A workgroup takes a piece of 256 PER elements of a beam's logits.
 template <int DT, int PER>
-__global__ __launch_bounds__(256) void kda_beam_piece_kernel(BeamParams p, BeamWs w) {
+__global__ __launch_bounds__(256, 4) void kda_beam_piece_kernel(BeamParams p, BeamWs w) {
   constexpr int VEC = 16 / elem_size(DT), NV = PER / VEC;
   __shared__ Key64 s_group[64];
   __shared__ uint64_t s_keys[HOLD];
@@ -131,77 +131,100 @@ __global__ __launch_bounds__(256) void kda_beam_piece_kernel(BeamParams p, BeamW
       raw[i].clear();
       if (at < p.V) load_part<false>(raw[i], p.logits, (size_t)row * p.V + at, p.V - at < VEC ? p.V - at : VEC);
     }
-    float x[PER], top = -INFINITY;
-    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      raw[i].unpack(x + i * VEC);
+    for (int i = 0; i < NV; ++i) {   // nothing behind the last element
+      const int at = first + (i * 256 + tid) * VEC;
+      if (at + VEC > p.V) {
+        float f[VEC];
+        raw[i].unpack(f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float& f = x[i * VEC + e];
-        if (first + (i * 256 + tid) * VEC + e >= p.V) f = -INFINITY;
-        bad = bad || !(f < INFINITY);
-        top = fmaxf(top, f);
+        for (int e = 0; e < VEC; ++e) f[e] = at + e < p.V ? f[e] : -INFINITY;
+        raw[i].pack(f);
       }
     }
+    // f(value, index) for the lane's elements in order of their index. They are kept as they lie in
+    // memory and taken apart again each time: kept as fp32, or as keys, they would take the registers
+    // of all but one wave.
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[VEC];
+        raw[i].opaque();
+        raw[i].unpack(x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f(x[e], first + (i * 256 + tid) * VEC + e);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    float own = -INFINITY;
+    int own_at = 0;
+    each([&](float x, int at) {
+      if (x > own) {
+        own = x;
+        own_at = at;
+      }
+    });
+    float top = own;
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, from_lane(top, o));
-    if (__any(bad)) top = __uint_as_float(0x7fc00000u);
     __syncthreads();   // the item before has been read
     if (lane == 0) s_top[wave] = top;
     if (tid == 0) s_used = 0;
     __syncthreads();
-    bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      bad = bad || s_top[i] != s_top[i];
-      top = i == 0 ? s_top[0] : fmaxf(top, s_top[i]);
-    }
-    if (bad || top == -INFINITY) {   // no continuation here
+    top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+    double sum = 0.0;   // NaN where an element is NaN or +infinity
+    const double dtop = (double)top;
+    each([&](float x, int) { sum += exp_below((double)x - dtop); });
+    sum = wg_sum(sum, s_sum);
+    if (!(top > -INFINITY) || sum != sum) {   // no continuation here: all masked, or one is no number
+      bool bad = false;
+      each([&](float x, int) { bad = bad || !(x < INFINITY); });
+      const bool any = __syncthreads_or(bad);
       if (tid == 0) {
-        w.top[it] = bad ? __uint_as_float(0x7fc00000u) : -INFINITY;
+        w.top[it] = any ? __uint_as_float(0x7fc00000u) : -INFINITY;
         w.sum[it] = 0.0;
       }
       for (int i = tid; i < p.k; i += 256) w.best[it * p.k + i] = 0;
       continue;
     }
-    double sum = 0.0;
-    uint64_t most = 0;
-    auto key = [&](int j) -> uint64_t {   // element j of the lane's
-      const int at = first + ((j / VEC) * 256 + tid) * VEC + j % VEC;
-      return x[j] == -INFINITY ? 0ull : ((uint64_t)ordered(x[j]) << 32) | (uint32_t)~at;
-    };
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      if (x[j] != -INFINITY) sum += exp_below((double)x[j] - (double)top);
-      const uint64_t q = key(j);
-      most = q > most ? q : most;
-    }
-    sum = wg_sum(sum, s_sum);
-    uint64_t least = threshold(Key64{most}, w.groups, s_group).v;
+    auto key_of = [](float x, int at) { return x == -INFINITY ? 0ull : ((uint64_t)ordered(x) << 32) | (uint32_t)~at; };
+    uint64_t least = threshold(Key64{key_of(own, own_at)}, w.groups, s_group).v;
     if (least == 0) least = 1;
-    auto reach = [&](uint64_t t) {   // elements of the workgroup with keys of t and more
-      int n = 0;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) n += key(j) >= t;
-      return wg_sum(n, s_count);
+    // those that reach it to shared memory; returns how many there are, held or not
+    auto gather = [&]() {
+      const float from = least == 1 ? -INFINITY : unordered((uint32_t)(least >> 32));
+      each([&](float x, int at) {
+        if (x >= from) {
+          const uint64_t q = key_of(x, at);
+          if (q >= least) {
+            const int to = atomicAdd(&s_used, 1);
+            if (to < HOLD) s_keys[to] = q;
+          }
+        }
+      });
+      __syncthreads();
+      return s_used;
     };
-    int count = reach(least);
-    for (uint64_t high = ~0ull; count > HOLD;) {   // reach(least) >= k > reach(high)
-      const uint64_t mid = least + (high - least) / 2;
-      const int n = reach(mid);
-      if (n >= p.k) {
-        least = mid;
-        count = n;
-      } else {
-        high = mid;
+    int count = gather();
+    if (count > HOLD) {
+      auto reach = [&](uint64_t t) {   // elements with keys of t and more
+        int n = 0;
+        each([&](float x, int at) { n += key_of(x, at) >= t; });
+        return wg_sum(n, s_count);
+      };
+      for (uint64_t high = ~0ull; count > HOLD;) {   // reach(least) >= k > reach(high)
+        const uint64_t mid = least + (high - least) / 2;
+        const int n = reach(mid);
+        if (n >= p.k) {
+          least = mid;
+          count = n;
+        } else {
+          high = mid;
+        }
       }
+      if (tid == 0) s_used = 0;
+      __syncthreads();
+      gather();
     }
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const uint64_t q = key(j);
-      if (q >= least) s_keys[atomicAdd(&s_used, 1)] = q;
-    }
-    __syncthreads();
     for (int i = tid; i < count; i += 256) {
       const uint64_t q = s_keys[i];
       int place = 0;

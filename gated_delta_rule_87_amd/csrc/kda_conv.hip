@@ -39,8 +39,12 @@ __device__ __forceinline__ void load_any(Pack<DT, V>& q, const void* p, size_t i
 }
 template <int DT, int V>
 __device__ __forceinline__ void store_any(const Pack<DT, V>& q, void* p, size_t i) {
-  if constexpr (V == 1) q.store(p, i);
-  else store_part<true>(q, p, i, V);   // past the caches
+  if constexpr (V == 1) {
+    q.store(p, i);
+  } else {   // past the caches
+    using Any = typename Pack<DT, V>::Raw __attribute__((aligned(2)));
+    __builtin_nontemporal_store(q.r, reinterpret_cast<Any*>(static_cast<uint8_t*>(p) + i * elem_size(DT)));
+  }
 }
 template <int DT, int V>
 __device__ __forceinline__ void load_any_f32(const void* p, size_t i, float* f) {
@@ -380,8 +384,10 @@ __global__ __launch_bounds__(1024) void kda_conv_sum_kernel(ConvParams p, int pa
   const int run = threadIdx.x >> 6;
   const int64_t width = (int64_t)(W + 1) * p.D;
   float v = 0.0f;
-  if (col < width)
+  if (col < width) {
+#pragma unroll 8
     for (int i = run; i < parts; i += 16) v += p.partial[(size_t)i * width + col];
+  }
   buf[run][threadIdx.x & 63] = v;
   __syncthreads();
   if (run != 0 || col >= width) return;
@@ -474,10 +480,12 @@ Grid grid_of(int64_t tokens, int64_t D, int V, int most_run) {
 }
 
 constexpr int64_t FWD_RUN = 32, BWD_RUN = 32;
+// Channels of a lane backward: with 8 of 16 bits each it takes 256 registers, one wave to a SIMD
+constexpr int BWD_VEC = 4;
 
 int64_t parts_of(int64_t tokens, int64_t D, int V) {
   const Grid g = grid_of(tokens, D, V, BWD_RUN);
-  const int64_t most = (2048 + g.cols - 1) / g.cols;
+  const int64_t most = (1024 + g.cols - 1) / g.cols;
   return g.blocks < most ? g.blocks : most;
 }
 
@@ -493,7 +501,7 @@ bool conv_fits(int64_t tokens, int64_t D) {
 size_t conv_workspace(int64_t tokens, int64_t D, int64_t W) {
   if (tokens == 0) return 0;
   int64_t most = 0;   // whatever the type
-  for (int V : {1, 4, 8}) {
+  for (int V : {1, BWD_VEC}) {
     const int64_t n = parts_of(tokens, D, V);
     if ((V == 1 || D >= V) && n > most) most = n;
   }
@@ -546,7 +554,7 @@ hipError_t launch_conv_bwd(const ConvParams& p, hipStream_t stream) {
                          p.D / N);
     };
     if (p.tokens > 0) {
-      if (p.D >= V) tokens(integral_constant<int, V>{});
+      if (p.D >= BWD_VEC) tokens(integral_constant<int, BWD_VEC>{});
       else tokens(integral_constant<int, 1>{});
     }
     if (p.dw || p.db)

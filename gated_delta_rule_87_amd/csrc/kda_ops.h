@@ -159,6 +159,7 @@ struct SsmWs {
   float* sums;                // [chunks - 1][D] sum of s
   int32_t* resets;            // [chunks - 1] whether a sequence begins in the chunk
   float* stage;               // forward: [chunks - 1][D][E] initial states that final_state overwrites, or NULL
+  float* table;               // [G][tokens][2][EP] B and C in fp32
   float* dA;                  // backward: [chunks][D][E]
   float* dvec;                // [chunks][2][D] of d_skip and d_dt_bias
   float* bc;                  // [tiles][tokens][2][E] of dB and dC

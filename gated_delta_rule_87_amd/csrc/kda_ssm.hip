@@ -34,8 +34,9 @@ namespace {
 using std::integral_constant;
 
 constexpr int SUB = 16;     // tokens that a workgroup stages at once
+constexpr int RUN = 8;      // tokens whose states the backward pass holds in registers
 constexpr int BLK = SSM_BLOCK;
-static_assert(BLK == 4 * SUB, "");
+static_assert(BLK == 8 * RUN && SUB == 2 * RUN, "");
 
 __device__ __forceinline__ Seqs seqs_of(const SsmParams& p) { return {p.cu, p.nseq, p.T, p.tokens}; }
 
@@ -85,6 +86,19 @@ __device__ __forceinline__ float softplus(float u) {
 __device__ __forceinline__ float sigmoid(float u) {
   const float e = fast_exp2(-fabsf(u) * LOG2E), r = fast_rcp(1.0f + e);
   return u < 0.0f ? e * r : r;
+}
+
+// the same in every lane, and said so to the compiler
+__device__ __forceinline__ size_t uniform(size_t v) {
+  return (size_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// v, of which the compiler does not know that it stays the same: an address formed of it is formed
+// of a scalar base and 32 bits a lane, not kept in two registers a lane
+__device__ __forceinline__ uint32_t hidden(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
 // N elements of a token tensor from element i on, the first c of them; `vec`: all, aligned
@@ -220,146 +234,306 @@ struct StageBC {
   }
 };
 
+// ---- B and C in fp32 ----------------------------------------------------------------
+//
+// [G][tokens][2][EP]: B, then C, E rounded up to EP = 4 S with zeros, and zeros for tokens that no
+// sequence covers (their values are not used, and may be NaN)
+template <int DT>
+__global__ __launch_bounds__(256) void kda_ssm_table_kernel(SsmParams p, float* table, int EP) {
+  const Seqs seqs = seqs_of(p);
+  const int32_t lo = seqs.begin(0), hi = seqs.begin(seqs.n);
+  const int64_t n = (int64_t)p.G * p.tokens * 2 * EP;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int e = (int)(i % EP);
+    const int64_t r = i / EP;
+    const bool is_c = r & 1;
+    const int64_t gt = r >> 1, g = gt / p.tokens, t = gt - g * p.tokens;
+    float v = 0.0f;
+    if (e < p.E && t >= lo && t < hi) load_f32<DT, 1>(is_c ? p.Cm : p.Bm, ((size_t)t * p.G + g) * p.E + e, &v);
+    table[i] = v;
+  }
+}
+
+// ---- a wave's channels ----------------------------------------------------------------
+//
+// A wave takes 64 channels of one group, four to a quad of lanes. Lane p of a quad has the states
+// S p .. S p + S - 1 of all four, and is besides the owner of channel p: it loads that channel's
+// x, dt and z and computes what all its states share, which the other three take over by lane
+// permutes. So B and C, the same for all channels, are read once for four channels' states. Lanes
+// beyond the last channel work on that one too, so that nothing of the tokens needs a condition.
+template <int S>
+struct Quad {
+  static constexpr int EP = 4 * S;
+  int g, d0, dn;        // group, first channel, channels
+  int lane, part, own;  // own: the lane's channel (the last one again beyond dn)
+  int e0, ec;           // its states e0 .. e0 + ec - 1
+  bool mine;            // owns a channel
+
+  __device__ __forceinline__ Quad(const SsmParams& p, int tile, int per_group) {
+    const int Dg = p.D / p.G;
+    g = tile / per_group;
+    const int at = (tile - g * per_group) * 64;
+    d0 = g * Dg + at;
+    dn = Dg - at < 64 ? Dg - at : 64;
+    lane = threadIdx.x & 63;
+    part = lane & 3;
+    mine = lane < dn;
+    own = d0 + (mine ? lane : dn - 1);
+    e0 = S * part;
+    ec = p.E - e0 < 0 ? 0 : p.E - e0 < S ? p.E - e0 : S;
+  }
+  __device__ __forceinline__ bool has(int c) const { return (lane & ~3) + c < dn; }
+  __device__ __forceinline__ int channel(int c) const { return d0 + (has(c) ? (lane & ~3) + c : dn - 1); }
+  // The lane's states of the quad's channels, of row `row` of [rows, D, E]: f(channel of the quad,
+  // state, byte of the row, the lane's own offset) for V of them each
+  template <int DT, bool ALL, typename F>
+  __device__ __forceinline__ void each(const SsmParams& p, size_t row, F f) const {
+    constexpr int V = S < 4 ? S : 4, SIZE = elem_size(DT);
+    const bool whole = ec == S && p.E % 4 == 0;
+    const size_t at = uniform(row * p.D * p.E * SIZE);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (!ALL && !has(c)) continue;
+      const uint32_t off = hidden((uint32_t)(channel(c) * p.E + e0) * SIZE);
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < S; j += V) f(integral_constant<int, V>{}, c, j, at + j * SIZE, off);
+      } else {
+#pragma unroll
+        for (int j = 0; j < S; ++j)
+          if (j < ec) f(integral_constant<int, 1>{}, c, j, at + j * SIZE, off);
+      }
+    }
+  }
+  template <int DT>
+  __device__ __forceinline__ void load_as(const SsmParams& p, const void* a, size_t row, float (&h)[4][S]) const {
+    each<DT, true>(p, row, [&](auto v, int c, int j, size_t at, uint32_t off) {
+      Pack<DT, decltype(v)::value> q;
+      q.load_at(a, at, off);
+      q.unpack(&h[c][j]);
+    });
+  }
+  template <int DT>
+  __device__ __forceinline__ void store_as(const SsmParams& p, void* a, size_t row, const float (&h)[4][S]) const {
+    each<DT, false>(p, row, [&](auto v, int c, int j, size_t at, uint32_t off) {
+      Pack<DT, decltype(v)::value> q;
+      q.pack(&h[c][j]);
+      q.store_at(a, at, off);
+    });
+  }
+  __device__ __forceinline__ void load(const SsmParams& p, const void* a, int dtype, size_t row, float (&h)[4][S]) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < S; ++j) h[c][j] = 0.0f;
+    if (dtype == FP32) load_as<FP32>(p, a, row, h);
+    else if (dtype == BF16) load_as<BF16>(p, a, row, h);
+  }
+  __device__ __forceinline__ void store(const SsmParams& p, void* a, int dtype, size_t row, const float (&h)[4][S]) const {
+    if (dtype == FP32) store_as<FP32>(p, a, row, h);
+    else if (dtype == BF16) store_as<BF16>(p, a, row, h);
+  }
+};
+
+// x of lane C of the quad
+template <int C>
+__device__ __forceinline__ float of_lane(float x) {
+  int r = __builtin_amdgcn_mov_dpp(__float_as_int(x), C * 0x55, 0xf, 0xf, true);
+  asm("" : "+v"(r));   // an instruction of its own: as an operand it halves the rate of each that uses it
+  return __int_as_float(r);
+}
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// v[p] summed over the quad, in lane p
+__device__ __forceinline__ float quad_sums(const float (&v)[4], bool odd, bool high) {
+  const float a = (odd ? v[1] : v[0]) + moved<0xB1>(odd ? v[0] : v[1]);
+  const float b = (odd ? v[3] : v[2]) + moved<0xB1>(odd ? v[2] : v[3]);
+  return (high ? b : a) + moved<0x4E>(high ? a : b);
+}
+
+// SUB tokens' rows of the table in shared memory, two of them in turn; one wave, so no barriers
+template <int S, int SUB>
+struct Rows {
+  static constexpr int EP = 4 * S, N = SUB * 2 * EP / 4, K = (N + 63) / 64;   // 16-byte pieces, of a lane
+  f32x4 r[K];
+  __device__ __forceinline__ void load(const float* table, int32_t t, int32_t end, int lane) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = lane + 64 * k;
+      r[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (i < N && t + i * 4 / (2 * EP) < end) r[k] = *reinterpret_cast<const f32x4*>(table + (size_t)t * 2 * EP + i * 4);
+    }
+  }
+  __device__ __forceinline__ void store(float* to, int lane) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = lane + 64 * k;
+      if (i < N) *reinterpret_cast<f32x4*>(to + i * 4) = r[k];
+    }
+  }
+};
+template <int S>
+__device__ __forceinline__ void row_of(const float* s, float (&f)[S]) {
+  if constexpr (S >= 4) {
+#pragma unroll
+    for (int j = 0; j < S; j += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(s + j);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[j + k] = v[k];
+    }
+  } else if constexpr (S == 2) {
+    const f32x2 v = *reinterpret_cast<const f32x2*>(s);
+    f[0] = v[0];
+    f[1] = v[1];
+  } else {
+    f[0] = *s;
+  }
+}
+
 // ---- forward ----------------------------------------------------------------------
 
-// FINAL: the outputs; else the chunk's map.
-template <int DT, int LPC, bool FINAL>
-__global__ __launch_bounds__(256) void kda_ssm_fwd_kernel(SsmParams p, SsmWs w) {
-  using TileT = Tile<LPC>;
-  constexpr int CW = TileT::CW, EPT = TileT::EPT;
-  __shared__ f32x2 s_d[2][SUB][CW];   // s, s x
-  __shared__ Shared2<LPC> s_bc[2];
-  __shared__ float s_y[FINAL ? 2 : 1][FINAL ? SUB : 1][CW];
+// h = exp(s A) h + w B for the channels of the quad; AL = A log2 e; y[c] += C . h where wanted
+template <int S, bool Y>
+__device__ __forceinline__ void advance(float (&h)[4][S], const float (&AL)[4][S], float s, float w, const float* b, const float* c,
+                                        float (&y)[4]) {
+  auto channel = [&](auto ch) {
+    constexpr int N = decltype(ch)::value;
+    const float sc = of_lane<N>(s), wc = of_lane<N>(w);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      h[N][j] = fmaf(fast_exp2(sc * AL[N][j]), h[N][j], wc * b[j]);
+      if (Y) y[N] = j == 0 ? c[0] * h[N][0] : fmaf(c[j], h[N][j], y[N]);
+    }
+  };
+  channel(integral_constant<int, 0>{});
+  channel(integral_constant<int, 1>{});
+  channel(integral_constant<int, 2>{});
+  channel(integral_constant<int, 3>{});
+}
+
+// Tokens loaded at once, and waves to a SIMD that the registers are to leave room for
+constexpr int FSUB = 4;
+constexpr int waves_of(int S) { return S >= 16 ? 1 : S >= 8 ? 2 : 4; }
+
+// FINAL: the outputs; else the chunk's map. A workgroup is one wave.
+template <int DT, int S, bool FINAL>
+__global__ __launch_bounds__(64, waves_of(S)) void kda_ssm_fwd_kernel(SsmParams p, SsmWs w) {
+  constexpr int EP = 4 * S;
+  __shared__ alignas(16) float s_bc[2][FSUB][2][EP];
+  __shared__ float s_own[3][FSUB][64];   // x, dt, z where tokens are taken one by one
   const Seqs seqs = seqs_of(p);
   const int tile = blockIdx.x % w.tiles, chunk = blockIdx.x / w.tiles;
-  const TileT T(p, tile, w.per_group);
-  const bool vec = (p.D / p.G) % EPT == 0 && p.D % EPT == 0;
+  const Quad<S> T(p, tile, w.per_group);
   const int32_t t_lo = chunk * w.len, t_hi = p.tokens - t_lo < w.len ? p.tokens : t_lo + w.len;
   const int32_t lo = seqs.begin(0), hi = seqs.begin(seqs.n) < t_hi ? seqs.begin(seqs.n) : t_hi;
-  float A[4], h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
-  T.load4(p, p.A, 0, A);
+  const float* table = w.table + (size_t)T.g * p.tokens * 2 * EP;
+  const bool odd = T.lane & 1, high = T.lane & 2;
+  float AL[4][S], h[4][S], sum = 0.0f;
+  T.load(p, p.A, FP32, 0, AL);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) A[j] *= LOG2E;
-  float bias[EPT], skip[EPT];
-  load_vec<EPT>(p.dt_bias, T.d0 + T.c0, T.cn, 0.0f, bias);
-  if (FINAL) load_vec<EPT>(p.skip, T.d0 + T.c0, T.cn, 0.0f, skip);
-  if (FINAL && chunk > 0) T.load4(p, w.maps, chunk - 1, h);
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      AL[c][j] *= LOG2E;
+      h[c][j] = 0.0f;
+    }
+  const float bias = p.dt_bias ? p.dt_bias[T.own] : 0.0f, skip = FINAL && p.skip ? p.skip[T.own] : 0.0f;
+  if (FINAL && chunk > 0) T.load(p, w.maps, FP32, chunk - 1, h);
   bool reset = false;
 
-  float x[EPT], dt[EPT], z[EPT], ox[EPT], oz[EPT];
-  StageBC<DT, LPC, true, FINAL> bc;
-  auto load = [&](int32_t t) {
-    const int32_t tt = t + T.row;
-    const int c = tt >= lo && tt < hi ? T.cn : 0;
-    const size_t i = (size_t)tt * p.D + T.d0 + T.c0;
-    load_some<DT, EPT>(p.x, i, c, vec, x);
-    load_some<DT, EPT>(p.dt, i, c, vec, dt);
-    if (FINAL && p.z) load_some<DT, EPT>(p.z, i, c, vec, z);
-    bc.load(p, T.g, t, lo, hi);
-  };
-  auto stage = [&](int32_t t, int buf) {
-    const bool in = t + T.row >= lo && t + T.row < hi;   // others leave the state as it is: s = 0
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const float u = dt[i] + bias[i];
-      const float s = in && i < T.cn ? (p.softplus ? softplus(u) : u) : 0.0f;
-      s_d[buf][T.row][T.c0 + i] = f32x2{s, in && i < T.cn ? s * x[i] : 0.0f};
-      ox[i] = x[i];
-      oz[i] = z[i];
-    }
-    bc.store(&s_bc[buf].b[0][0], &s_bc[buf].c[0][0]);
-  };
-  auto step = [&](int buf, int r) {   // one token; the lane's part of its y
-    const f32x2 d = s_d[buf][r][T.ch];
-    const f32x4 b = *reinterpret_cast<const f32x4*>(&s_bc[buf].b[r][T.e0]);
-    f32x4 c = {};
-    if (FINAL) c = *reinterpret_cast<const f32x4*>(&s_bc[buf].c[r][T.e0]);
-    float y = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = fmaf(fast_exp2(d.x * A[j]), h[j], d.y * b[j]);
-      if (FINAL) y = fmaf(c[j], h[j], y);
-    }
-    if (!FINAL) sum += d.x;
-    return y;
+  const uint32_t off = (uint32_t)T.own * elem_size(DT);
+  const size_t line = (size_t)p.D * elem_size(DT);
+  Pack<DT, 1> x[FSUB], d[FSUB], z[FSUB];   // of the next FSUB tokens: each is loaded as soon as the one before has been used
+  Rows<S, FSUB> rows;
+  auto load = [&](int r, int32_t t) {   // (tokens beyond the covered ones are read as the last of them and not used)
+    const size_t at = uniform((t < lo ? lo : t < hi ? t : hi - 1) * line);
+    const uint32_t o = hidden(off);
+    x[r].load_at(p.x, at, o);
+    d[r].load_at(p.dt, at, o);
+    if (FINAL) z[r].load_at(p.z ? p.z : p.x, at, o);
   };
   SeqWalk q;
   q.start(seqs, t_lo);
-  if (t_lo < t_hi) {
-    load(t_lo);
-    stage(t_lo, 0);
+  const bool any = t_lo < hi && t_hi > lo;   // tokens of a sequence
+  if (any) {
+#pragma unroll
+    for (int r = 0; r < FSUB; ++r) load(r, t_lo + r);
+    rows.load(table, t_lo, t_hi, T.lane);
+    rows.store(&s_bc[0][0][0][0], T.lane);
   }
-  __syncthreads();
   int buf = 0;
-  for (int32_t t = t_lo; t < t_hi; t += SUB, buf ^= 1) {
-    float px[EPT], pz[EPT];
+  for (int32_t t = t_lo; any && t < t_hi; t += FSUB, buf ^= 1) {
+    if (t + FSUB < t_hi) rows.load(table, t + FSUB, t_hi, T.lane);
+    if (FINAL && p.carry && t % BLK == 0) T.store(p, p.carry, FP32, t / BLK, h);
+    // one token; in: it belongs to a sequence (others leave the state as it is)
+    auto step = [&](int r, bool in, float xv, float dv, float zv) {
+      float b[S], c[S], y[4];
+      row_of<S>(&s_bc[buf][r][0][T.e0], b);
+      if (FINAL) row_of<S>(&s_bc[buf][r][1][T.e0], c);
+      const float u = dv + bias;
+      const float sp = softplus(u);   // (selects, no branches: they would cut up the code of a token)
+      const float s = !in ? 0.0f : p.softplus ? sp : u, v = in ? s * xv : 0.0f;
+      advance<S, FINAL>(h, AL, s, v, b, c, y);
+      if (!FINAL) sum += s;
+      if (FINAL) {
+        float out = fmaf(skip, xv, quad_sums(y, odd, high));
+        const float gate = zv * sigmoid(zv);
+        out *= p.z ? gate : 1.0f;
+        Pack<DT, 1> o;
+        o.pack(&out);
+        if (in) o.store_at(p.y, uniform((t + r) * line), hidden(off));
+      }
+    };
+    if (q.b < t && q.e > t + FSUB) {   // no sequence begins or ends here
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      px[i] = ox[i];
-      pz[i] = oz[i];
-    }
-    if (t + SUB < t_hi) load(t + SUB);
-    if (FINAL && p.carry && t % BLK == 0) T.store4(p, p.carry, t / BLK, h);
-    if (q.b < t && q.e > t + SUB) {   // no sequence begins or ends here
-#pragma unroll
-      for (int r = 0; r < SUB; r += 4) {
-        float y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) y[u] = step(buf, r + u);
-        if (FINAL) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) y[u] = part_sum<LPC>(y[u]);
-          if constexpr (LPC >= 4) {
-            if (T.part < 4) s_y[buf][r + T.part][T.ch] = T.part == 0 ? y[0] : T.part == 1 ? y[1] : T.part == 2 ? y[2] : y[3];
-          } else {
-            s_y[buf][r + T.part][T.ch] = T.part ? y[1] : y[0];
-            s_y[buf][r + 2 + T.part][T.ch] = T.part ? y[3] : y[2];
-          }
-        }
+      for (int r = 0; r < FSUB; ++r) {
+        float xv, dv, zv;
+        x[r].unpack(&xv);
+        d[r].unpack(&dv);
+        z[r].unpack(&zv);
+        load(r, t + FSUB + r);
+        step(r, true, xv, dv, zv);
+        __builtin_amdgcn_sched_barrier(0);   // (more tokens at once would only take registers)
       }
     } else {
+#pragma unroll
+      for (int r = 0; r < FSUB; ++r) {
+        x[r].unpack(&s_own[0][r][T.lane]);
+        d[r].unpack(&s_own[1][r][T.lane]);
+        z[r].unpack(&s_own[2][r][T.lane]);
+        load(r, t + FSUB + r);
+      }
 #pragma unroll 1
-      for (int r = 0; r < SUB && t + r < t_hi; ++r) {
+      for (int r = 0; r < FSUB && t + r < t_hi; ++r) {
         if (t + r >= q.e) q.forward(seqs, t + r);
-        if (t + r == q.b && q.holds(t + r)) {
+        const bool in = q.holds(t + r);
+        if (t + r == q.b && in) {
           // the last sequence that goes on after this chunk has its final state written elsewhere,
           // perhaps over its initial state: that is put aside
           const bool goes_on = w.stage && q.e > t_hi;
-          if (FINAL && goes_on) T.load4(p, w.stage, chunk, h);
-          else T.load_state4(p, p.init, p.init_dtype, q.i, h);
-          if (!FINAL && goes_on) T.store4(p, w.stage, chunk, h);
+          if (FINAL && goes_on) T.load(p, w.stage, FP32, chunk, h);
+          else T.load(p, p.init, p.init_dtype, q.i, h);
+          if (!FINAL && goes_on) T.store(p, w.stage, FP32, chunk, h);
           reset = true;
         }
-        const float y = part_sum<LPC>(step(buf, r));
-        if (FINAL && T.part == 0) s_y[buf][r][T.ch] = y;
-        if (FINAL && p.fin && t + r == q.e - 1 && q.holds(t + r)) T.store_state4(p, p.fin, p.fin_dtype, q.i, h);
+        step(r, in, s_own[0][r][T.lane], s_own[1][r][T.lane], s_own[2][r][T.lane]);
+        if (FINAL && p.fin && t + r == q.e - 1 && in) T.store(p, p.fin, p.fin_dtype, q.i, h);
       }
     }
-    if (t + SUB < t_hi) stage(t + SUB, buf ^ 1);
-    __syncthreads();
-    if (FINAL) {
-      const int32_t tt = t + T.row;
-      if (tt >= lo && tt < hi) {
-        float y[EPT];
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          y[i] = fmaf(skip[i], px[i], s_y[buf][T.row][T.c0 + i]);
-          if (p.z) y[i] *= pz[i] * sigmoid(pz[i]);
-        }
-        store_some<DT, EPT>(p.y, (size_t)tt * p.D + T.d0 + T.c0, T.cn, vec, y);
-      }
-    }
+    if (t + FSUB < t_hi) rows.store(&s_bc[buf ^ 1][0][0][0], T.lane);
   }
   if (FINAL) {   // sequences without tokens
     if (p.fin)
       for (int n = chunk; n < p.nseq; n += w.chunks)
         if (seqs.begin(n) >= seqs.begin(n + 1)) {
-          T.load_state4(p, p.init, p.init_dtype, n, h);
-          T.store_state4(p, p.fin, p.fin_dtype, n, h);
+          T.load(p, p.init, p.init_dtype, n, h);
+          T.store(p, p.fin, p.fin_dtype, n, h);
         }
   } else {
-    T.store4(p, w.maps, chunk, h);
-    if (T.part == 0 && T.ch < T.dn) w.sums[(size_t)chunk * p.D + T.d] = sum;
+    T.store(p, w.maps, FP32, chunk, h);
+    if (T.mine) w.sums[(size_t)chunk * p.D + T.own] = sum;
     if (tile == 0 && threadIdx.x == 0) w.resets[chunk] = reset;
   }
 }
@@ -404,24 +578,31 @@ __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmParams p, SsmWs w)
   float A[4];
   T.load4(p, p.A, 0, A);
   const float bias = p.dt_bias ? p.dt_bias[T.d] : 0.0f, skip = p.skip ? p.skip[T.d] : 0.0f;
+  #pragma unroll 2
   for (int n = blockIdx.x / w.tiles; n < p.nseq; n += gridDim.x / w.tiles) {
     const int from = p.in_slots[n], to = p.out_slots[n];
     const size_t i = (size_t)n * p.D + T.d, bc = ((size_t)n * p.G + T.g) * p.E + T.e0;
-    float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x, dt, z = 0.0f, y = 0.0f;
+    float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {}, c[4] = {}, x, dt, z = 0.0f, y = 0.0f;
     if (from >= 0 && from < p.n_slots) T.load_state4(p, p.init, p.init_dtype, from, h);
     load_f32<DT, 1>(p.x, i, &x);
     load_f32<DT, 1>(p.dt, i, &dt);
     if (p.z) load_f32<DT, 1>(p.z, i, &z);
+    if (T.ec == 4 && p.E % 4 == 0) {
+      load_f32<DT, 4>(p.Bm, bc, b);
+      load_f32<DT, 4>(p.Cm, bc, c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < T.ec) {
+          load_f32<DT, 1>(p.Bm, bc + j, b + j);
+          load_f32<DT, 1>(p.Cm, bc + j, c + j);
+        }
+    }
     const float s = p.softplus ? softplus(dt + bias) : dt + bias;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float b = 0.0f, c = 0.0f;
-      if (j < T.ec) {
-        load_f32<DT, 1>(p.Bm, bc + j, &b);
-        load_f32<DT, 1>(p.Cm, bc + j, &c);
-      }
-      h[j] = fmaf(fast_exp2(s * A[j] * LOG2E), h[j], s * x * b);
-      y = fmaf(c, h[j], y);
+      h[j] = fmaf(fast_exp2(s * A[j] * LOG2E), h[j], s * x * b[j]);
+      y = fmaf(c[j], h[j], y);
     }
     if (to >= 0 && to < p.n_slots) T.store_state4(p, p.fin, p.fin_dtype, to, h);
     y = fmaf(skip, x, part_sum<LPC>(y));
@@ -574,8 +755,8 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
       bc.store(&s_b[s][0], &s_c[s][0]);
     }
     __syncthreads();
-    // the state that enters each SUB tokens
-    float h[4], in4[BLK / SUB][4];
+    // the state that enters each RUN tokens
+    float h[4], in4[BLK / RUN][4];
     T.load4(p, p.carry, t_blk / BLK, h);
     q.start(seqs, t_blk);
     auto begins = [&](int32_t t) {   // token t, next in order, is a sequence's first
@@ -583,41 +764,46 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
       if (t == q.b && q.holds(t)) T.load_state4(p, p.init, p.init_dtype, q.i, h);
     };
 #pragma unroll 1
-    for (int s = 0; s < BLK / SUB; ++s) {
-      const int32_t t = t_blk + s * SUB;
+    for (int s = 0; s < BLK / RUN; ++s) {
+      const int32_t t = t_blk + s * RUN;
 #pragma unroll
-      for (int k = 0; k < BLK / SUB; ++k)
+      for (int k = 0; k < BLK / RUN; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) in4[k][j] = k == s || s == 0 ? h[j] : in4[k][j];
-      if (s + 1 == BLK / SUB) break;
+      if (s + 1 == BLK / RUN) break;
       auto sweep = [&](auto plain) {
 #pragma unroll 4
-        for (int r = 0; r < SUB; ++r) {
+        for (int r = 0; r < RUN; ++r) {
           if (!decltype(plain)::value) begins(t + r);
-          const f32x2 d = s_d[s * SUB + r][T.ch];
-          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_b[s * SUB + r][T.e0]);
+          const f32x2 d = s_d[s * RUN + r][T.ch];
+          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_b[s * RUN + r][T.e0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[j] = fmaf(fast_exp2(d.x * AL[j]), h[j], d.y * b[j]);
         }
       };
-      if (q.b < t && q.e >= t + SUB) sweep(std::true_type{});
+      if (q.b < t && q.e >= t + RUN) sweep(std::true_type{});
       else sweep(std::false_type{});
     }
 #pragma unroll 1
-    for (int s = BLK / SUB - 1; s >= 0; --s) {
-      const int32_t t = t_blk + s * SUB;
+    for (int s = BLK / RUN - 1; s >= 0; --s) {
+      const int32_t t = t_blk + s * RUN;
       if (t >= t_hi) continue;
+      const int at0 = (s & 1) * RUN;   // two runs share what follows
       q.start(seqs, t);
-      float hb[SUB][4], a[SUB][4];
+      float hb[RUN][4], a[RUN][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = s == 0 ? in4[0][j] : s == 1 ? in4[1][j] : s == 2 ? in4[2][j] : in4[3][j];
+      for (int j = 0; j < 4; ++j) {
+        h[j] = in4[0][j];
+#pragma unroll
+        for (int k = 1; k < BLK / RUN; ++k) h[j] = s == k ? in4[k][j] : h[j];
+      }
       auto sweep = [&](auto plain) {
         constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-        for (int r = 0; r < SUB; ++r) {
+        for (int r = 0; r < RUN; ++r) {
           if (!PLAIN) begins(t + r);
-          const f32x2 d = s_d[s * SUB + r][T.ch];
-          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_b[s * SUB + r][T.e0]);
+          const f32x2 d = s_d[s * RUN + r][T.ch];
+          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_b[s * RUN + r][T.e0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             hb[r][j] = h[j];
@@ -625,9 +811,9 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
             h[j] = fmaf(a[r][j], h[j], d.y * b[j]);
           }
         }
-        if (!PLAIN) q.start(seqs, t + SUB - 1 < p.tokens ? t + SUB - 1 : p.tokens - 1);
+        if (!PLAIN) q.start(seqs, t + RUN - 1 < p.tokens ? t + RUN - 1 : p.tokens - 1);
 #pragma unroll
-        for (int r = SUB - 1; r >= 0; --r) {
+        for (int r = RUN - 1; r >= 0; --r) {
           if (!PLAIN && t + r < t_hi) {
             if (t + r < q.b) q.back(seqs, t + r);
             if (p.dfin && t + r == q.e - 1 && q.holds(t + r)) {
@@ -637,10 +823,10 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
               for (int j = 0; j < 4; ++j) G[j] += f[j];
             }
           }
-          const f32x2 d = s_d[s * SUB + r][T.ch];
-          const float g = s_g[s * SUB + r][T.ch];
-          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_b[s * SUB + r][T.e0]);
-          const f32x4 c = *reinterpret_cast<const f32x4*>(&s_c[s * SUB + r][T.e0]);
+          const f32x2 d = s_d[s * RUN + r][T.ch];
+          const float g = s_g[s * RUN + r][T.ch];
+          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_b[s * RUN + r][T.e0]);
+          const f32x4 c = *reinterpret_cast<const f32x4*>(&s_c[s * RUN + r][T.e0]);
           float bg = 0.0f, ahg = 0.0f, chs = 0.0f, v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -658,11 +844,11 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
           bg = part_sum<LPC>(bg);
           ahg = part_sum<LPC>(ahg);
           chs = part_sum<LPC>(chs);
-          if (T.part < 3) s_o[T.part][r][T.ch] = T.part == 0 ? bg : T.part == 1 ? ahg : chs;
+          if (T.part < 3) s_o[T.part][at0 + r][T.ch] = T.part == 0 ? bg : T.part == 1 ? ahg : chs;
           // over channels: bit 5 of the lane B or C, bit 4 (and 3) the state, the rest of them summed
           const float u0 = halves16(v[0], v[1]), u1 = halves16(v[2], v[3]);
           if constexpr (LPC == 16) {
-            float* to = &s_r[wave][r][lane >> 5][T.e0 + ((lane >> 4) & 1)];
+            float* to = &s_r[wave][at0 + r][lane >> 5][T.e0 + ((lane >> 4) & 1)];
             to[0] = u0;
             to[2] = u1;
           } else {
@@ -670,7 +856,7 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
             const float keep = up ? u1 : u0, give = up ? u0 : u1;
             float u = keep + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(give), 0x128, 0xf, 0xf, false));   // row_ror 8
             if constexpr (LPC == 4) u = xor4_add(u);
-            if (LPC != 4 || !(lane & 4)) s_r[wave][r][lane >> 5][T.e0 + ((lane >> 4) & 1) + (up ? 2 : 0)] = u;
+            if (LPC != 4 || !(lane & 4)) s_r[wave][at0 + r][lane >> 5][T.e0 + ((lane >> 4) & 1) + (up ? 2 : 0)] = u;
           }
           if (!PLAIN && t + r == q.b && q.holds(t + r)) {
             if (p.dinit && t + r < t_hi) T.store_state4(p, p.dinit, p.dinit_dtype, q.i, G);
@@ -679,10 +865,11 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
           }
         }
       };
-      if (q.b < t && q.e > t + SUB) sweep(std::true_type{});
+      if (q.b < t && q.e > t + RUN) sweep(std::true_type{});
       else sweep(std::false_type{});
+      if (s & 1) continue;
       __syncthreads();
-      // outputs of these tokens
+      // outputs of these SUB tokens
       const int32_t tt = t + T.row;
       if (tt >= lo && tt < hi && T.cn > 0) {
         const size_t i0 = (size_t)tt * p.D + T.d0 + T.c0;
@@ -695,7 +882,7 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
         }
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-          const float g = s_g[s * SUB + T.row][T.c0 + i], sp = s_d[s * SUB + T.row][T.c0 + i].x;
+          const float g = s_g[s * RUN + T.row][T.c0 + i], sp = s_d[s * RUN + T.row][T.c0 + i].x;
           const float bg = s_o[0][T.row][T.c0 + i], ahg = s_o[1][T.row][T.c0 + i], ch = s_o[2][T.row][T.c0 + i];
           odx[i] = fmaf(skip[i], g, sp * bg);
           odt[i] = fmaf(x[i], bg, ahg);
@@ -793,16 +980,18 @@ __global__ __launch_bounds__(256) void kda_ssm_empty_kernel(SsmParams p) {
 int lanes_of(int64_t E, bool backward) {
   return E <= 8 && !backward ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : 16;
 }
+int states_of(int64_t E) { return E <= 4 ? 1 : E <= 8 ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : 16; }
 
-// Chunks of a multiple of BLK tokens: as many as give the GPU 4 workgroups a compute unit (waves
-// hide each other's waits), 64 at most.
+// Chunks of a multiple of BLK tokens: as many as give the GPU enough waves to hide each other's
+// waits (forward four to a SIMD, backward workgroups of four of them, 4 to a compute unit).
 SsmWs shape_of(int64_t tokens, int64_t D, int64_t E, int64_t G, bool backward) {
   SsmWs w{};
-  const int64_t cw = 256 / lanes_of(E, backward), Dg = D / G;
+  const int64_t cw = backward ? 256 / lanes_of(E, true) : 64, Dg = D / G;
   w.per_group = (int32_t)((Dg + cw - 1) / cw);
   w.tiles = (int32_t)(w.per_group * G);
-  int64_t want = (1024 + w.tiles - 1) / w.tiles;
-  if (want > 64) want = 64;
+  const int64_t fill = backward ? 1024 : 4096, most = backward ? 64 : 256;
+  int64_t want = (fill + w.tiles - 1) / w.tiles;
+  if (want > most) want = most;
   const int64_t blocks = (tokens + BLK - 1) / BLK;
   int64_t len = (blocks + want - 1) / want;
   if (len < 1) len = 1;
@@ -813,7 +1002,7 @@ SsmWs shape_of(int64_t tokens, int64_t D, int64_t E, int64_t G, bool backward) {
 }
 
 // The parts of a workspace, each aligned to 256 bytes; at: its start, or NULL for the size alone
-size_t lay_out(SsmWs& w, uint8_t* at, int64_t tokens, int64_t D, int64_t E, bool backward) {
+size_t lay_out(SsmWs& w, uint8_t* at, int64_t tokens, int64_t D, int64_t E, int64_t G, bool backward) {
   size_t used = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = at ? at + used : nullptr;
@@ -826,6 +1015,7 @@ size_t lay_out(SsmWs& w, uint8_t* at, int64_t tokens, int64_t D, int64_t E, bool
   w.resets = reinterpret_cast<int32_t*>(take(links * sizeof(int32_t)));
   if (!backward) {
     w.stage = reinterpret_cast<float*>(take(links * states));
+    w.table = reinterpret_cast<float*>(take((size_t)G * tokens * 2 * 4 * states_of(E) * sizeof(float)));
   } else {
     w.dA = reinterpret_cast<float*>(take(w.chunks * states));
     w.dvec = reinterpret_cast<float*>(take((size_t)w.chunks * 2 * D * sizeof(float)));
@@ -834,6 +1024,14 @@ size_t lay_out(SsmWs& w, uint8_t* at, int64_t tokens, int64_t D, int64_t E, bool
   return used;
 }
 
+template <typename F>
+void by_states(int S, F f) {
+  if (S == 1) f(integral_constant<int, 1>{});
+  else if (S == 2) f(integral_constant<int, 2>{});
+  else if (S == 4) f(integral_constant<int, 4>{});
+  else if (S == 8) f(integral_constant<int, 8>{});
+  else f(integral_constant<int, 16>{});
+}
 template <int DT, typename F>
 void by_lanes(int lpc, F f) {
   if (lpc == 2) f(integral_constant<int, 2>{});
@@ -858,23 +1056,26 @@ bool ssm_fits(int64_t tokens, int64_t D, int64_t E, int64_t G) {
 
 size_t ssm_workspace(int64_t tokens, int64_t D, int64_t E, int64_t G, bool backward) {
   SsmWs w = shape_of(tokens, D, E, G, backward);
-  return lay_out(w, nullptr, tokens, D, E, backward);
+  return lay_out(w, nullptr, tokens, D, E, G, backward);
 }
 
 hipError_t launch_ssm_fwd(const SsmParams& p, void* workspace, hipStream_t stream) {
   SsmWs w = shape_of(p.tokens, p.D, p.E, p.G, false);
-  lay_out(w, static_cast<uint8_t*>(workspace), p.tokens, p.D, p.E, false);
+  lay_out(w, static_cast<uint8_t*>(workspace), p.tokens, p.D, p.E, p.G, false);
   if (p.fin != p.init || !p.fin) w.stage = nullptr;
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    by_lanes<DT>(lanes_of(p.E, false), [&](auto lpc) {
-      constexpr int L = decltype(lpc)::value;
+    by_states(states_of(p.E), [&](auto states) {
+      constexpr int S = decltype(states)::value;
+      if (p.tokens > 0)
+        hipLaunchKernelGGL(kda_ssm_table_kernel<DT>, dim3(blocks_of((int64_t)p.G * p.tokens * 8 * S, 4096)), dim3(256), 0, stream, p,
+                           w.table, 4 * S);
       if (w.chunks > 1) {
-        hipLaunchKernelGGL((kda_ssm_fwd_kernel<DT, L, false>), dim3((unsigned)w.tiles * (w.chunks - 1)), dim3(256), 0, stream, p, w);
+        hipLaunchKernelGGL((kda_ssm_fwd_kernel<DT, S, false>), dim3((unsigned)w.tiles * (w.chunks - 1)), dim3(64), 0, stream, p, w);
         hipLaunchKernelGGL(kda_ssm_pass_kernel<false>, dim3(blocks_of((int64_t)p.D * p.E, INT32_MAX)), dim3(256), 0, stream, p, w,
                            w.chunks - 1);
       }
-      hipLaunchKernelGGL((kda_ssm_fwd_kernel<DT, L, true>), dim3((unsigned)w.tiles * w.chunks), dim3(256), 0, stream, p, w);
+      hipLaunchKernelGGL((kda_ssm_fwd_kernel<DT, S, true>), dim3((unsigned)w.tiles * w.chunks), dim3(64), 0, stream, p, w);
     });
   });
   return hipGetLastError();
@@ -882,8 +1083,11 @@ hipError_t launch_ssm_fwd(const SsmParams& p, void* workspace, hipStream_t strea
 
 hipError_t launch_ssm_step(const SsmParams& p, hipStream_t stream) {
   if (p.nseq == 0) return hipSuccess;
-  const SsmWs w = shape_of(0, p.D, p.E, p.G, false);
-  const int64_t rows = p.nseq < 65536 / w.tiles + 1 ? p.nseq : 65536 / w.tiles + 1;
+  SsmWs w{};
+  const int cw = 256 / lanes_of(p.E, false);
+  w.per_group = (p.D / p.G + cw - 1) / cw;
+  w.tiles = w.per_group * p.G;
+  const int64_t most = 4096 / w.tiles + 1, rows = p.nseq < most ? p.nseq : most;   // the others in turn: A is loaded once
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     by_lanes<DT>(lanes_of(p.E, false), [&](auto lpc) {
@@ -895,7 +1099,7 @@ hipError_t launch_ssm_step(const SsmParams& p, hipStream_t stream) {
 
 hipError_t launch_ssm_bwd(const SsmParams& p, void* workspace, hipStream_t stream) {
   SsmWs w = shape_of(p.tokens, p.D, p.E, p.G, true);
-  lay_out(w, static_cast<uint8_t*>(workspace), p.tokens, p.D, p.E, true);
+  lay_out(w, static_cast<uint8_t*>(workspace), p.tokens, p.D, p.E, p.G, true);
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     if (p.tokens > 0) {
