@@ -146,13 +146,15 @@ __global__ __launch_bounds__(256, 4) void kda_beam_piece_kernel(BeamParams p, Be
     // memory and taken apart again each time: kept as fp32, or as keys, they would take the registers
     // of all but one wave.
     auto each = [&](auto f) {
+      int from = first + tid * VEC;
+      asm volatile("" : "+v"(from));   // indices are formed anew each time as well
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float x[VEC];
         raw[i].opaque();
         raw[i].unpack(x);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f(x[e], first + (i * 256 + tid) * VEC + e);
+        for (int e = 0; e < VEC; ++e) f(x[e], from + i * 256 * VEC + e);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -296,20 +298,44 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
     const double v = (((double)unordered((uint32_t)(q >> 32)) - s_top[b]) - s_log[b]) + s_score[b];
     return {ordered(v), ~((uint32_t)b * p.V + ~(uint32_t)q)};
   };
-  Key96 most{0, 0};
-  for (int i = tid; i < total; i += 256) {
-    const Key96 q = key(i);
-    if (q > most) most = q;
+  constexpr int HELD = 8;   // keys of a lane that are kept, where that is all of them: formed once
+  const bool held = total <= 256 * HELD;
+  Key96 own[HELD];
+  auto each = [&](auto f) {
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < HELD; ++j) f(own[j]);
+    } else {
+      for (int i = tid; i < total; i += 256) f(key(i));
+    }
+  };
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) own[j] = tid + 256 * j < total ? key(tid + 256 * j) : Key96{0, 0};
   }
+  Key96 most{0, 0};
+  each([&](const Key96& q) {
+    if (q > most) most = q;
+  });
   Key96 least = threshold(most, w.groups, s_group);
   if (least.s == 0) least = {1, 0};
-  auto reach = [&](const Key96& t) {
-    int c = 0;
-    for (int i = tid; i < total; i += 256) c += !(t > key(i));
-    return wg_sum(c, s_count);
+  auto gather = [&]() {   // as in a piece
+    each([&](const Key96& q) {
+      if (!(least > q)) {
+        const int to = atomicAdd(&s_used, 1);
+        if (to < HOLD) s_keys[to] = q;
+      }
+    });
+    __syncthreads();
+    return s_used;
   };
-  int count = reach(least);
+  int count = gather();
   if (count > HOLD) {   // reach(least) >= k > reach({high, 0}): first by the score, then by the index
+    auto reach = [&](const Key96& t) {
+      int c = 0;
+      each([&](const Key96& q) { c += !(t > q); });
+      return wg_sum(c, s_count);
+    };
     uint64_t high = ~0ull;
     while (count > HOLD && high - least.s > 1) {
       const Key96 mid{least.s + (high - least.s) / 2, 0};
@@ -332,12 +358,10 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
         up = mid.i;
       }
     }
+    if (tid == 0) s_used = 0;
+    __syncthreads();
+    gather();
   }
-  for (int i = tid; i < total; i += 256) {
-    const Key96 q = key(i);
-    if (!(least > q)) s_keys[atomicAdd(&s_used, 1)] = q;
-  }
-  __syncthreads();
   for (int i = tid; i < count; i += 256) {
     const Key96 q = s_keys[i];
     int place = 0;
