@@ -601,8 +601,7 @@ __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmParams p, SsmWs w)
   float A[4];
   T.load4(p, p.A, 0, A);
   const float bias = p.dt_bias ? p.dt_bias[T.d] : 0.0f, skip = p.skip ? p.skip[T.d] : 0.0f;
-  #pragma unroll 2
-  for (int n = blockIdx.x / w.tiles; n < p.nseq; n += gridDim.x / w.tiles) {
+    for (int n = blockIdx.x / w.tiles; n < p.nseq; n += gridDim.x / w.tiles) {
     const int from = p.in_slots[n], to = p.out_slots[n];
     const size_t i = (size_t)n * p.D + T.d, bc = ((size_t)n * p.G + T.g) * p.E + T.e0;
     float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {}, c[4] = {}, x, dt, z = 0.0f, y = 0.0f;
@@ -782,9 +781,10 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_bwd_kernel(SsmParams p, SsmWs 
     float h[4], in4[BLK / RUN][4];
     T.load4(p, p.carry, t_blk / BLK, h);
     q.start(seqs, t_blk);
-    auto begins = [&](int32_t t) {   // token t, next in order, is a sequence's first
+    auto begins = [&](int32_t t) {   // before token t, next in order
       if (t >= q.e) q.forward(seqs, t);
-      if (t == q.b && q.holds(t)) T.load_state4(p, p.init, p.init_dtype, q.i, h);
+      if (!q.holds(t)) h[0] = h[1] = h[2] = h[3] = 0.0f;   // (of no sequence: nothing was saved there)
+      else if (t == q.b) T.load_state4(p, p.init, p.init_dtype, q.i, h);
     };
 #pragma unroll 1
     for (int s = 0; s < BLK / RUN; ++s) {

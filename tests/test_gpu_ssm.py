@@ -13,7 +13,9 @@ RAGGED = [0, 1, 1, 17, 20, 81, 145, 145, 210]
 SHAPES = [(1, 1, 1, 1, 1, None), (2, 5, 7, 3, 1, None), (1, 64, 64, 16, 1, None), (1, 65, 66, 16, 2, None), (3, 130, 24, 8, 3, None),
           (1, 200, 130, 16, 1, None), (1, 100, 40, 33, 1, None), (2, 70, 35, 20, 5, None), (1, 300, 16, 64, 1, None),
           (1, 210, 72, 16, 1, RAGGED), (1, 210, 33, 13, 1, RAGGED), (1, 210, 20, 40, 2, RAGGED), (1, 210, 130, 6, 1, RAGGED),
-          (1, 150, 12, 16, 1, [9, 30, 30, 31, 140]), (3, 0, 8, 4, 1, None), (1, 0, 8, 4, 1, [0, 0]), (1, 128, 128, 16, 1, [0, 64, 128])]
+          (1, 150, 12, 16, 1, [9, 30, 30, 31, 140]), (3, 0, 8, 4, 1, None), (1, 0, 8, 4, 1, [0, 0]), (1, 128, 128, 16, 1, [0, 64, 128]),
+          (1, 400, 20, 16, 1, [200, 201, 330]), (1, 300, 70, 8, 1, [0, 10, 64]), (1, 90, 300, 4, 4, [0, 0, 90]),
+          (1, 70, 6, 2, 6, None)]
 
 
 def make(B, T, D, E, G, bounds, dtype, state, seed=0):
@@ -217,6 +219,43 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         got = [t.clone() for t in outs]
         assert all(same(a, b) for a, b in zip(got, step())), k
+
+
+def test_gradients_that_are_not_wanted():
+    i, n = make(1, 100, 40, 16, 1, None, BF, F, 9)
+    j = {a: gpu(t) for a, t in i.items()}
+    carry = forward(j, None, 1, F)[2]
+    want = backward(j, None, 1, carry)
+    x = j["x"]
+    dx, ddt, dA, dB, dC = (blank(t.shape, t.dtype) for t in (x, x, j["A"], j["B"], j["B"]))
+    kda.ssm_bwd(x, j["dt"], j["A"], j["B"], j["C"], j["dy"], carry, dx, ddt, dA, dB, dC, D=j["skip"], z=j["z"], dt_bias=j["bias"],
+                initial_state=j["h0"], d_final=j["df"])
+    for a, b in zip((dx, ddt, dA, dB, dC), ("dx", "ddt", "dA", "dB", "dC")):
+        assert same(a, want[b]), b
+
+
+def test_values_behind_a_sequence_are_not_used():
+    """NaN in tokens that no sequence covers, and in a state beside them."""
+    bounds = [70, 75, 200]
+    i, n = make(1, 330, 40, 16, 1, bounds, F, F, 10)
+    cu = cu_of(bounds)
+    j = {a: gpu(t) for a, t in i.items()}
+    bad = {a: None if t is None else t.clone() for a, t in j.items()}
+    for k in ("x", "dt", "B", "C", "z", "dy"):
+        bad[k][:, :70], bad[k][:, 200:] = float("nan"), float("inf")
+    out = []
+    for v in (j, bad):
+        y, fin, carry = forward(v, cu, n, F)
+        out.append({"y": y, "final": fin, **backward(v, cu, n, carry)})
+    for k in out[0]:
+        assert same(out[0][k], out[1][k]), k
+    # the last token's state alone is infinite: no sum over tokens uses it
+    j["x"][0, 199] = float("inf")
+    y, fin, carry = forward(j, cu, n, F)
+    j["df"] = None
+    j["dy"][0, 199] = 0
+    got = backward({**j, "z": None, "skip": None}, cu, n, carry)
+    assert bool(torch.isfinite(got["dA"]).all())
 
 
 def test_two_calls_at_once():
