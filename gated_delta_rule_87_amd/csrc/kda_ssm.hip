@@ -4,24 +4,26 @@
 //     y_t = (sum_e C_t[e] h_t[e] + skip x_t) SiLU(z_t)
 //
 // per channel, s_t = softplus(dt_t + bias). Bound by the vector units: each of the T D E updates
-// takes an exponential (16 cycles of a wave) and four operations (16). The states of a channel
-// are four to a lane (LPC lanes a channel, E rounded up to LPC 4), so that the sum over e stays
-// in a few neighbouring lanes; everything that is the same for a channel's states (s_t, s_t x_t,
-// SiLU(z_t)) is computed once, by the lanes that load it, 16 tokens at a time, and handed over
-// in shared memory together with B and C.
+// takes an exponential (8.4 cycles of a SIMD, measured) and four operations (2.6 to 3 each, with
+// more than one wave; 4.4 where an operand is scalar or comes from another lane). At 8192 tokens x
+// 8192 channels x 16 states, bf16, those alone are 140 us of the outputs' pass, where the memory
+// traffic takes 105; it measures 300 us, and the pass before it 230.
 //
-// A sequence's tokens follow each other; where channels and states alone do not fill the GPU the
-// packed tokens are cut into chunks. A chunk acts on the state entering it as h -> P h + R with
-// P = exp(A sum s_t): one launch computes R and the sum of s of all chunks but the last, a second
-// one runs through the chunks for the state that enters each, the third computes the outputs. A
-// sequence's first token puts its initial state in the place of h; a chunk with one passes no state
-// on (reset), whatever is before it.
+// A sequence's tokens follow each other, so the packed tokens are cut into chunks until the GPU is
+// filled. A chunk acts on the state entering it as h -> P h + R with P = exp(A sum s_t): one launch
+// computes R and the sum of s of all chunks but the last, a second one passes the states from chunk
+// to chunk, the third computes the outputs. (The exponentials are so taken twice; storing them
+// would be 16 times the inputs.) A sequence's first token puts its initial state in the place of h;
+// a chunk with one passes no state on (reset), whatever is before it.
 //
 // Backward, with g = dy SiLU(z): G_t = C_t g_t + exp(s_{t+1} A) G_{t+1} runs from the last token to
 // the first, by chunks in the same manner. The states h are recomputed from those that the forward
-// pass has saved every 64 tokens, 16 tokens at a time in registers. The sums over channels (dB,
-// dC) are halved from lane to lane with two values at once, added up over a workgroup, and over
-// workgroups by a kernel after it, as the sums over chunks (dA, d_skip, d_bias) are.
+// pass has saved every 64 tokens: once through the 64 for the state that enters every 8th, then 8
+// tokens at a time, their states and decays in registers. The sums over channels (dB, dC) are
+// halved from lane to lane with two values at once, added up over a workgroup, and over workgroups
+// by a kernel after it, as the sums over chunks (dA, d_skip, d_bias) are. There the states of a
+// channel are four to a lane, and what they share is computed by the lanes that load it and handed
+// over in shared memory (8192 tokens x 4096 channels x 16 states 830 us, 35 operations an update).
 #include <type_traits>
 
 #include "kda_elem.h"
@@ -135,7 +137,9 @@ __device__ __forceinline__ void load_vec(const float* p, size_t i, int c, float 
   for (int e = 0; e < N; ++e) f[e] = p && e < c ? p[i + e] : none;
 }
 
-// ---- a workgroup's part of the channels, and its lanes' ------------------------------
+// ---- a workgroup's part of the channels, and its lanes' (single tokens, backward) -----
+//
+// LPC lanes a channel, four states each; E rounded up to 4 LPC.
 
 template <int LPC>
 struct Tile {
@@ -189,6 +193,18 @@ struct Tile {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j < ec) load_state<1>(a, dtype, at(p, row_) + j, h + j);
+    }
+  }
+  // past the caches (states of 256 sequences x 8192 channels x 16: a step 74 -> 70 us)
+  __device__ __forceinline__ void store_past4(const SsmParams& p, void* a, int dtype, size_t row_, const float* h) const {
+    if (ec != 4 || p.E % 4 != 0) {
+      store_state4(p, a, dtype, row_, h);
+    } else if (dtype == FP32) {
+      __builtin_nontemporal_store(f32x4{h[0], h[1], h[2], h[3]}, reinterpret_cast<f32x4*>(static_cast<float*>(a) + at(p, row_)));
+    } else {
+      Pack<BF16, 4> q;
+      q.pack(h);
+      __builtin_nontemporal_store(q.r, reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a) + at(p, row_)));
     }
   }
   __device__ __forceinline__ void store_state4(const SsmParams& p, void* a, int dtype, size_t row_, const float* h) const {
@@ -626,7 +642,7 @@ __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmParams p, SsmWs w)
       h[j] = fmaf(fast_exp2(s * A[j] * LOG2E), h[j], s * x * b[j]);
       y = fmaf(c[j], h[j], y);
     }
-    if (to >= 0 && to < p.n_slots) T.store_state4(p, p.fin, p.fin_dtype, to, h);
+    if (to >= 0 && to < p.n_slots) T.store_past4(p, p.fin, p.fin_dtype, to, h);
     y = fmaf(skip, x, part_sum<LPC>(y));
     if (p.z) y *= z * sigmoid(z);
     if (T.part == 0) store_f32<DT, 1>(p.y, i, &y);
@@ -1111,7 +1127,9 @@ hipError_t launch_ssm_step(const SsmParams& p, hipStream_t stream) {
   const int cw = 256 / lanes_of(p.E, false);
   w.per_group = (p.D / p.G + cw - 1) / cw;
   w.tiles = w.per_group * p.G;
-  const int64_t most = 4096 / w.tiles + 1, rows = p.nseq < most ? p.nseq : most;   // the others in turn: A is loaded once
+  // Sequences at once; the others in turn, so that A is loaded once for some (16384 workgroups 69 us
+  // at 256 sequences of 8192 channels, 4096 71, one for each sequence 80).
+  const int64_t most = 16384 / w.tiles + 1, rows = p.nseq < most ? p.nseq : most;
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     by_lanes<DT>(lanes_of(p.E, false), [&](auto lpc) {
