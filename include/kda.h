@@ -37,7 +37,8 @@
  *     clamp every sequence into [0, T] so malformed contents cannot make them
  *     access memory out of bounds (results are then unspecified). Setting the
  *     environment variable KDA_VALIDATE=1 makes kda_fwd synchronise the stream
- *     and check the contents on the host (KDA_ERR_VALUE if violated).
+ *     and check the contents on the host (KDA_ERR_VALUE if violated); kda_glr_*,
+ *     kda_conv_* and kda_ssm_* with cu_seqlens likewise.
  *   - Other environment variables: KDA_LOG=1 prints each kda_fwd call's sizes
  *     and chain segment count to stderr; KDA_CHAIN_SEGMENTS=n caps the number
  *     of segments of the segment-parallel state chain (see
@@ -485,8 +486,9 @@ int kda_layernorm_bwd(const void *dy, const void *x, const float *weight, const 
  *   y, y_dtype        [M, D] in `dtype`, or in KDA_E4M3 with scales
  *   scales, group     fp32 [M, ceil(D / group)] with KDA_E4M3, else NULL and 0: y holds what
  *                     the values are in units of their scale, the largest of the group's
- *                     |values| / 448 (1 where that is 0; NaN, or infinity with infinite
- *                     values among finite ones, where it is). A group is 128 neighbouring
+ *                     |values| / 448, or 1 where that is 0. (A NaN in a group makes its scale
+ *                     NaN; an infinity makes it infinite, and finite values 0 beside it.) A
+ *                     group is 128 neighbouring
  *                     elements (the row's last one the rest), or the row: group is 128 or D.
  *   weight            fp32 [D], or NULL (ones)
  *   eps               finite, >= 0
