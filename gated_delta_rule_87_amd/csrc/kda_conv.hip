@@ -14,8 +14,8 @@
 // past its run. The weight's sums stay in registers over all of a lane's runs, are added up over
 // the workgroup, and a second kernel adds the workgroups' sums in a fixed order.
 //
-// States are written by kernels of their own: a lane has read all of a sequence's state before
-// it writes (final_state may be initial_state), and every run has been read by then.
+// States are written by workgroups of their own, a lane all of a sequence's state after it has read
+// all of it; where final_state is initial_state, in a launch after the one that reads it.
 #include <type_traits>
 
 #include "kda_elem.h"
@@ -133,11 +133,41 @@ struct Where {
 
 // ---- forward ----------------------------------------------------------------------
 
+// The last W - 1 inputs of every sequence, the state before it included: the share of workgroup
+// `block` of `blocks`. A lane: a sequence's V channels.
 template <int DT, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_fwd_kernel(ConvParams p, int lr_log, int cols, int run) {
+__device__ __forceinline__ void final_states(const ConvParams& p, int block, int blocks) {
   const Seqs s = seqs_of(p);
-  const Where at(lr_log, blockIdx.x % cols, p.D, V);
-  const int64_t first = ((int64_t)(blockIdx.x / cols) * (256 >> lr_log) + at.grp) * run;
+  const int vecs = p.D / V;
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < (int64_t)p.nseq * vecs; i += (int64_t)blocks * 256) {
+    const int n = (int)(i / vecs), d = (int)(i - (int64_t)n * vecs) * V;
+    const int32_t b = s.begin(n), e = s.begin(n + 1);
+    float old[W - 1][V];
+    load_before<DT, W, V>(p, n, b, e > b ? e : b, d, old);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store_state<V>(p.fin, p.fin_dtype, ((size_t)n * (W - 1) + j) * p.D + d, old[j]);
+  }
+}
+template <int DT, int W, int V>
+__device__ __forceinline__ void any_final_states(const ConvParams& p, int block, int blocks) {
+  if (p.D % V == 0) final_states<DT, W, V>(p, block, blocks);
+  else final_states<DT, W, 1>(p, block, blocks);
+}
+template <int DT, int W, int V>
+__global__ __launch_bounds__(256) void kda_conv_final_kernel(ConvParams p) {
+  any_final_states<DT, W, V>(p, blockIdx.x, gridDim.x);
+}
+
+template <int DT, int W, int V>
+__global__ __launch_bounds__(256) void kda_conv_fwd_kernel(ConvParams p, int lr_log, int cols, int run, int states) {
+  if ((int)blockIdx.x < states) {
+    any_final_states<DT, W, V>(p, blockIdx.x, states);
+    return;
+  }
+  const int block = blockIdx.x - states;
+  const Seqs s = seqs_of(p);
+  const Where at(lr_log, block % cols, p.D, V);
+  const int64_t first = ((int64_t)(block / cols) * (256 >> lr_log) + at.grp) * run;
   if (!at.any || first >= p.tokens) return;
   const int32_t t0 = (int32_t)first, t1 = p.tokens - t0 < run ? p.tokens : t0 + run;
   const int d = at.d;
@@ -177,22 +207,6 @@ __global__ __launch_bounds__(256) void kda_conv_fwd_kernel(ConvParams p, int lr_
       y.pack(u);
       store_any(y, p.out, (size_t)(t + r) * p.D + d);
     }
-  }
-}
-
-// The last W - 1 inputs of every sequence, the state before it included. A lane: a sequence's
-// V channels.
-template <int DT, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_final_kernel(ConvParams p, int vecs) {
-  const Seqs s = seqs_of(p);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.nseq * vecs; i += (int64_t)gridDim.x * 256) {
-    const int n = (int)(i / vecs), d = (int)(i - (int64_t)n * vecs) * V;
-    const int32_t b = s.begin(n), e = s.begin(n + 1);
-    float old[W - 1][V];
-    load_before<DT, W, V>(p, n, b, e > b ? e : b, d, old);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      store_state<V>(p.fin, p.fin_dtype, ((size_t)n * (W - 1) + j) * p.D + d, old[j]);
   }
 }
 
@@ -239,12 +253,60 @@ __device__ __forceinline__ float grad_of(float u, float dy) {
   return dy * (sg * fmaf(u, 1.0f - sg, 1.0f));
 }
 
+// Gradient of the initial states: from the first W - 1 tokens, and from the final state where a
+// sequence is shorter than that
 template <int DT, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvParams p, int lr_log, int cols, int run, int parts) {
+__device__ __forceinline__ void initial_grads(const ConvParams& p, int block, int blocks) {
+  const int vecs = p.D / V;
+  const Seqs s = seqs_of(p);
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < (int64_t)p.nseq * vecs; i += (int64_t)blocks * 256) {
+    const int n = (int)(i / vecs), d = (int)(i - (int64_t)n * vecs) * V;
+    const int32_t b = s.begin(n), len = s.begin(n + 1) - b;
+    Taps<W, V> taps;
+    taps.load(p, d);
+    float old[W - 1][V], out[W - 1][V];
+    load_before<DT, W, V>(p, n, b, b, d, old);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int row = j - (len > 0 ? len : 0);   // of the final state
+      load_state_any<V>(p.dfin, row >= 0 ? p.dfin_dtype : 0, ((size_t)n * (W - 1) + (row >= 0 ? row : 0)) * p.D + d, out[j]);
+    }
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) {
+      if (r >= len) break;
+      float f[V], g[V], u[V];
+      load_any_f32<DT, V>(p.x, (size_t)(b + r) * p.D + d, f);
+      load_any_f32<DT, V>(p.dy, (size_t)(b + r) * p.D + d, g);
+      taps.apply(old, f, u);
+      if (p.silu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] = grad_of(u[e], g[e]);
+      }
+      shift<V, W - 1>(old, f);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)   // state row j is input r - (W - 1) + j - r of this output, tap j - r
+        if (j >= r) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) out[j][e] = fmaf(taps.w[j - r][e], g[e], out[j][e]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      store_state<V>(p.dinit, p.dinit_dtype, ((size_t)n * (W - 1) + j) * p.D + d, out[j]);
+  }
+}
+
+template <int DT, int W, int V>
+__global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvParams p, int lr_log, int cols, int run, int parts, int states) {
   constexpr int K = V * (W + 1);
   __shared__ float sums[256 * (K + 1)];
+  if ((int)blockIdx.x < states) {
+    if (p.D % V == 0) initial_grads<DT, W, V>(p, blockIdx.x, states);
+    else initial_grads<DT, W, 1>(p, blockIdx.x, states);
+    return;
+  }
   const Seqs s = seqs_of(p);
-  const int col = blockIdx.x % cols, part = blockIdx.x / cols, groups = 256 >> lr_log;
+  const int col = (blockIdx.x - states) % cols, part = (blockIdx.x - states) / cols, groups = 256 >> lr_log;
   const Where at(lr_log, col, p.D, V);
   const int d = at.d;
   const int32_t lo = s.begin(0), hi = s.begin(s.n);   // tokens of any sequence
@@ -402,48 +464,6 @@ __global__ __launch_bounds__(1024) void kda_conv_sum_kernel(ConvParams p, int pa
   }
 }
 
-// Gradient of the initial states: from the first W - 1 tokens, and from the final state where a
-// sequence is shorter than that
-template <int DT, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_dinit_kernel(ConvParams p, int vecs) {
-  const Seqs s = seqs_of(p);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.nseq * vecs; i += (int64_t)gridDim.x * 256) {
-    const int n = (int)(i / vecs), d = (int)(i - (int64_t)n * vecs) * V;
-    const int32_t b = s.begin(n), len = s.begin(n + 1) - b;
-    Taps<W, V> taps;
-    taps.load(p, d);
-    float old[W - 1][V], out[W - 1][V];
-    load_before<DT, W, V>(p, n, b, b, d, old);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-      const int row = j - (len > 0 ? len : 0);   // of the final state
-      load_state_any<V>(p.dfin, row >= 0 ? p.dfin_dtype : 0, ((size_t)n * (W - 1) + (row >= 0 ? row : 0)) * p.D + d, out[j]);
-    }
-#pragma unroll
-    for (int r = 0; r < W - 1; ++r) {
-      if (r >= len) break;
-      float f[V], g[V], u[V];
-      load_any_f32<DT, V>(p.x, (size_t)(b + r) * p.D + d, f);
-      load_any_f32<DT, V>(p.dy, (size_t)(b + r) * p.D + d, g);
-      taps.apply(old, f, u);
-      if (p.silu) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = grad_of(u[e], g[e]);
-      }
-      shift<V, W - 1>(old, f);
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)   // state row j is input r - (W - 1) + j - r of this output, tap j - r
-        if (j >= r) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) out[j][e] = fmaf(taps.w[j - r][e], g[e], out[j][e]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      store_state<V>(p.dinit, p.dinit_dtype, ((size_t)n * (W - 1) + j) * p.D + d, out[j]);
-  }
-}
-
 // ---- launches ---------------------------------------------------------------------
 
 // f(type, W)
@@ -495,7 +515,7 @@ unsigned state_blocks(int64_t n) { return (unsigned)((n + 255) / 256 < 16384 ? (
 
 bool conv_fits(int64_t tokens, int64_t D) {
   const Grid g = grid_of(tokens, D, D < 8 ? 1 : 4, FWD_RUN);   // (the most workgroups of all types)
-  return g.blocks < (1 << 24) && g.blocks * g.cols < (1 << 24);
+  return g.blocks < (1 << 24) && g.blocks * g.cols < (1 << 24) - 16384;   // (and 16384 for the states)
 }
 
 size_t conv_workspace(int64_t tokens, int64_t D, int64_t W) {
@@ -510,59 +530,48 @@ size_t conv_workspace(int64_t tokens, int64_t D, int64_t W) {
 
 // Token tensors are taken in vectors of 16 bytes at any alignment, rows of fewer channels one by
 // one. States in vectors only where they are whole ones: what overlaps would be read by one lane
-// after another has written it.
+// after another has written it. The first workgroups write the states beside the others (a launch
+// of their own took 5 us, 7 backward), except where final states overwrite the initial ones that
+// the others read.
 hipError_t launch_conv_fwd(const ConvParams& p, hipStream_t stream) {
   dispatch(p, [&](auto dt, auto w) {
     constexpr int DT = decltype(dt)::value, W = decltype(w)::value, V = vec_of<DT>();
-    auto tokens = [&](auto v) {
+    auto go = [&](auto v) {
       constexpr int N = decltype(v)::value;
-      const Grid g = grid_of(p.tokens, p.D, N, FWD_RUN);
-      hipLaunchKernelGGL((kda_conv_fwd_kernel<DT, W, N>), dim3((unsigned)(g.blocks * g.cols)), dim3(256), 0, stream, p, g.lr_log,
-                         g.cols, g.run);
+      const unsigned states = p.fin ? state_blocks((int64_t)p.nseq * p.D / (p.D % N == 0 ? N : 1)) : 0;
+      const bool apart = p.fin == p.init || p.tokens == 0;
+      if (p.tokens > 0) {
+        const Grid g = grid_of(p.tokens, p.D, N, FWD_RUN);
+        const unsigned beside = apart ? 0 : states;
+        hipLaunchKernelGGL((kda_conv_fwd_kernel<DT, W, N>), dim3((unsigned)(g.blocks * g.cols) + beside), dim3(256), 0, stream, p,
+                           g.lr_log, g.cols, g.run, (int)beside);
+      }
+      if (apart && states > 0) hipLaunchKernelGGL((kda_conv_final_kernel<DT, W, N>), dim3(states), dim3(256), 0, stream, p);
     };
-    auto states = [&](auto v) {
-      constexpr int N = decltype(v)::value;
-      hipLaunchKernelGGL((kda_conv_final_kernel<DT, W, N>), dim3(state_blocks((int64_t)p.nseq * p.D / N)), dim3(256), 0, stream, p,
-                         p.D / N);
-    };
-    if (p.tokens > 0) {
-      if (p.D >= V) tokens(integral_constant<int, V>{});
-      else tokens(integral_constant<int, 1>{});
-    }
-    if (p.fin) {
-      if (p.D % V == 0) states(integral_constant<int, V>{});
-      else states(integral_constant<int, 1>{});
-    }
+    if (p.D >= V) go(integral_constant<int, V>{});
+    else go(integral_constant<int, 1>{});
   });
   return hipGetLastError();
 }
 
 hipError_t launch_conv_bwd(const ConvParams& p, hipStream_t stream) {
   dispatch(p, [&](auto dt, auto w) {
-    constexpr int DT = decltype(dt)::value, W = decltype(w)::value, V = vec_of<DT>();
+    constexpr int DT = decltype(dt)::value, W = decltype(w)::value;
     int parts = 0;
-    auto tokens = [&](auto v) {
+    auto go = [&](auto v) {
       constexpr int N = decltype(v)::value;
+      const unsigned states = p.dinit ? state_blocks((int64_t)p.nseq * p.D / (p.D % N == 0 ? N : 1)) : 0;
       const Grid g = grid_of(p.tokens, p.D, N, BWD_RUN);
-      parts = (int)parts_of(p.tokens, p.D, N);
-      hipLaunchKernelGGL((kda_conv_bwd_kernel<DT, W, N>), dim3((unsigned)parts * g.cols), dim3(256), 0, stream, p, g.lr_log, g.cols,
-                         g.run, parts);
+      if (p.tokens > 0) parts = (int)parts_of(p.tokens, p.D, N);
+      const unsigned blocks = (unsigned)parts * g.cols + states;
+      if (blocks > 0)
+        hipLaunchKernelGGL((kda_conv_bwd_kernel<DT, W, N>), dim3(blocks), dim3(256), 0, stream, p, g.lr_log, g.cols, g.run, parts,
+                           (int)states);
     };
-    auto states = [&](auto v) {
-      constexpr int N = decltype(v)::value;
-      hipLaunchKernelGGL((kda_conv_dinit_kernel<DT, W, N>), dim3(state_blocks((int64_t)p.nseq * p.D / N)), dim3(256), 0, stream, p,
-                         p.D / N);
-    };
-    if (p.tokens > 0) {
-      if (p.D >= BWD_VEC) tokens(integral_constant<int, BWD_VEC>{});
-      else tokens(integral_constant<int, 1>{});
-    }
+    if (p.D >= BWD_VEC) go(integral_constant<int, BWD_VEC>{});
+    else go(integral_constant<int, 1>{});
     if (p.dw || p.db)
       hipLaunchKernelGGL((kda_conv_sum_kernel<W>), dim3((unsigned)(((int64_t)(W + 1) * p.D + 63) / 64)), dim3(1024), 0, stream, p, parts);
-    if (p.dinit) {
-      if (p.D % V == 0) states(integral_constant<int, V>{});
-      else states(integral_constant<int, 1>{});
-    }
   });
   return hipGetLastError();
 }
