@@ -11,9 +11,10 @@ from typing import Optional
 import torch
 
 import gated_delta_rule_87_amd as _kda
-from ._ops import (F, I, I64, P, SZ, _bytes, _done, _dtype, _glr_sizes, _gpu, _on, _pool, _ptr, _rows, _slots, _space, _state,
+from ._ops import (F, I, I64, P, SZ, _bytes, _done, _dtype, _glr_sizes, _gpu, _on, _pool, _ptr, _rows, _space, _state,
                    _stream, _vector)
 
+_check = _kda._check
 U32 = ctypes.c_uint32
 E4M3 = 4
 CONV_SILU = 1
@@ -44,9 +45,8 @@ def _setup(L):
 
 
 def _fp32(name, t, shape, dev, optional=False):
-    if t is None and optional:
-        return
-    _kda._check(name, t, torch.float32, shape, dev)
+    if t is not None or not optional:
+        _check(name, t, torch.float32, shape, dev)
 
 
 # ---- root-mean-square norm ------------------------------------------------------------
@@ -65,20 +65,20 @@ def rmsnorm_fwd(x, weight, eps: float, y, residual=None, residual_out=None, scal
     each row's 1 / sqrt(mean square + eps) into ``rstd`` (fp32, one per row) where given. y (of
     x's type) and residual_out may be x or residual (kda_rmsnorm_fwd)."""
     dev, M, D, dt = _rows(x)
-    _kda._check("x", x, x.dtype, x.shape, dev)
+    _check("x", x, x.dtype, x.shape, dev)
     for name, t in (("residual", residual), ("residual_out", residual_out)):
         if t is not None:
-            _kda._check(name, t, x.dtype, x.shape, dev)
+            _check(name, t, x.dtype, x.shape, dev)
     group, y_dt = 0, dt
     if isinstance(y, torch.Tensor) and y.dtype == torch.float8_e4m3fn:
-        _kda._check("y", y, torch.float8_e4m3fn, x.shape, dev)
+        _check("y", y, torch.float8_e4m3fn, x.shape, dev)
         y_dt, blocks = E4M3, (D + 127) // 128
         if not isinstance(scales, torch.Tensor) or scales.dim() != x.dim() or scales.shape[-1] not in (1, blocks):
             raise ValueError(f"scales must be [..., {blocks}] or [..., 1] for an 8-bit y")
         _fp32("scales", scales, (*x.shape[:-1], scales.shape[-1]), dev)
         group = D if scales.shape[-1] == 1 else 128
     else:
-        _kda._check("y", y, x.dtype, x.shape, dev)
+        _check("y", y, x.dtype, x.shape, dev)
         if scales is not None:
             raise ValueError("scales go with a float8_e4m3fn y only")
     _vector("weight", weight, D, dev)
@@ -95,11 +95,11 @@ def rmsnorm_bwd(dy, x, weight, rstd, dx, d_weight=None, d_residual=None, workspa
     or d_residual, or None), with ``d_residual``, the gradient of residual_out, added to it;
     ``d_weight`` fp32 [D] or None (kda_rmsnorm_bwd)."""
     dev, M, D, dt = _rows(x)
-    _kda._check("x", x, x.dtype, x.shape, dev)
-    _kda._check("dy", dy, x.dtype, x.shape, dev)
+    _check("x", x, x.dtype, x.shape, dev)
+    _check("dy", dy, x.dtype, x.shape, dev)
     for name, t in (("dx", dx), ("d_residual", d_residual)):
         if t is not None:
-            _kda._check(name, t, x.dtype, x.shape, dev)
+            _check(name, t, x.dtype, x.shape, dev)
     if rstd is None:
         raise ValueError("rstd of the forward pass is required")
     for name, t, n in (("weight", weight, D), ("rstd", rstd, M), ("d_weight", d_weight, D)):
@@ -118,8 +118,9 @@ def _conv_weights(weight, bias, D, dev) -> int:
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a 2-D tensor [D, W]")
     W = weight.shape[1]
-    _fp32("weight", weight, (D, W), dev)
-    _fp32("bias", bias, (D,), dev, optional=True)
+    _check("weight", weight, torch.float32, (D, W), dev)
+    if bias is not None:
+        _check("bias", bias, torch.float32, (D,), dev)
     return W
 
 
@@ -138,8 +139,8 @@ def conv_fwd(x, weight, bias, y, initial_state=None, final_state=None, cu_seqlen
     dev = _gpu("x", x, 3)
     B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
     dt = _dtype("x", x)
-    _kda._check("x", x, x.dtype, x.shape, dev)
-    _kda._check("y", y, x.dtype, x.shape, dev)
+    _check("x", x, x.dtype, x.shape, dev)
+    _check("y", y, x.dtype, x.shape, dev)
     W = _conv_weights(weight, bias, D, dev)
     shape = (N if cu_seqlens is not None else B, W - 1, D)
     ic = _state("initial_state", initial_state, shape, dev)
@@ -161,7 +162,7 @@ def conv_bwd(x, weight, bias, dy, dx, d_weight=None, d_bias=None, initial_state=
     B, T, D, N = _glr_sizes(x, cu_seqlens, dev)
     dt = _dtype("x", x)
     for name, t in (("x", x), ("dy", dy), ("dx", dx)):
-        _kda._check(name, t, x.dtype, x.shape, dev)
+        _check(name, t, x.dtype, x.shape, dev)
     W = _conv_weights(weight, bias, D, dev)
     _fp32("d_weight", d_weight, (D, W), dev, optional=True)
     _fp32("d_bias", d_bias, (D,), dev, optional=True)
@@ -186,14 +187,14 @@ def conv_step(x, weight, bias, y, state, in_slots, out_slots, silu: bool = True)
     dev = _gpu("x", x, 2)
     N, D = x.shape
     dt = _dtype("x", x)
-    _kda._check("x", x, x.dtype, x.shape, dev)
-    _kda._check("y", y, x.dtype, x.shape, dev)
+    _check("x", x, x.dtype, x.shape, dev)
+    _check("y", y, x.dtype, x.shape, dev)
     W = _conv_weights(weight, bias, D, dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a 3-D tensor [slots, W - 1, D]")
-    _kda._check("state", state, state.dtype, (state.shape[0], W - 1, D), dev)
-    _slots("in_slots", in_slots, dev, N)
-    _slots("out_slots", out_slots, dev, N)
+    _check("state", state, state.dtype, (state.shape[0], W - 1, D), dev)
+    _check("in_slots", in_slots, torch.int32, (N,), dev)
+    _check("out_slots", out_slots, torch.int32, (N,), dev)
     with _on(dev):
         _done(_kda.lib().kda_conv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), dt, W, CONV_SILU if silu else 0,
                                        state.data_ptr(), _kda._state_code(state), state.shape[0], in_slots.data_ptr(),
@@ -206,10 +207,10 @@ def conv_step(x, weight, bias, y, state, in_slots, out_slots, silu: bool = True)
 def _ssm_inputs(x, dt, A, B, C, skip, z, dt_bias, dev):
     """E and G, after checking the operator's inputs against x [..., D]."""
     D = x.shape[-1]
-    _kda._check("x", x, x.dtype, x.shape, dev)
-    _kda._check("dt", dt, x.dtype, x.shape, dev)
+    _check("x", x, x.dtype, x.shape, dev)
+    _check("dt", dt, x.dtype, x.shape, dev)
     if z is not None:
-        _kda._check("z", z, x.dtype, x.shape, dev)
+        _check("z", z, x.dtype, x.shape, dev)
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a 2-D tensor [D, E]")
     E = A.shape[1]
@@ -218,7 +219,7 @@ def _ssm_inputs(x, dt, A, B, C, skip, z, dt_bias, dev):
         raise ValueError(f"B must be a tensor [{'B, T' if x.dim() == 3 else 'N'}, G, E]")
     G = B.shape[-2]
     for name, t in (("B", B), ("C", C)):
-        _kda._check(name, t, x.dtype, (*x.shape[:-1], G, E), dev)
+        _check(name, t, x.dtype, (*x.shape[:-1], G, E), dev)
     if G < 1 or D % G:
         raise ValueError(f"G must divide D (got D={D}, G={G})")
     _fp32("D", skip, (D,), dev, optional=True)
@@ -250,7 +251,7 @@ def ssm_fwd(x, dt, A, B, C, y, D=None, z=None, dt_bias=None, softplus: bool = Tr
     Bn, T, Dn, N = _glr_sizes(x, cu_seqlens, dev)
     code = _dtype("x", x)
     E, G = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dev)
-    _kda._check("y", y, x.dtype, x.shape, dev)
+    _check("y", y, x.dtype, x.shape, dev)
     shape = (N if cu_seqlens is not None else Bn, Dn, E)
     ic = _state("initial_state", initial_state, shape, dev)
     fc = _state("final_state", final_state, shape, dev)
@@ -278,16 +279,16 @@ def ssm_bwd(x, dt, A, B, C, dy, carry, dx, d_dt, dA, dB, dC, D=None, d_D=None, z
     code = _dtype("x", x)
     E, G = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dev)
     for name, t in (("dy", dy), ("dx", dx), ("d_dt", d_dt)):
-        _kda._check(name, t, x.dtype, x.shape, dev)
+        _check(name, t, x.dtype, x.shape, dev)
     for name, t in (("dB", dB), ("dC", dC)):
-        _kda._check(name, t, x.dtype, B.shape, dev)
+        _check(name, t, x.dtype, B.shape, dev)
     _fp32("dA", dA, (Dn, E), dev)
     for name, t, of, given in (("d_D", d_D, "D", D), ("d_z", d_z, "z", z), ("d_dt_bias", d_dt_bias, "dt_bias", dt_bias)):
         if t is None:
             continue
         if given is None:
             raise ValueError(f"{name} without {of}")
-        _kda._check(name, t, given.dtype, given.shape, dev)
+        _check(name, t, given.dtype, given.shape, dev)
     shape = (N if cu_seqlens is not None else Bn, Dn, E)
     ic = _state("initial_state", initial_state, shape, dev)
     fc = _state("d_final", d_final, shape, dev)
@@ -311,12 +312,12 @@ def ssm_step(x, dt, A, B, C, y, state, in_slots, out_slots, D=None, z=None, dt_b
     N, Dn = x.shape
     code = _dtype("x", x)
     E, G = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dev)
-    _kda._check("y", y, x.dtype, x.shape, dev)
+    _check("y", y, x.dtype, x.shape, dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a 3-D tensor [slots, D, E]")
-    _kda._check("state", state, state.dtype, (state.shape[0], Dn, E), dev)
-    _slots("in_slots", in_slots, dev, N)
-    _slots("out_slots", out_slots, dev, N)
+    _check("state", state, state.dtype, (state.shape[0], Dn, E), dev)
+    _check("in_slots", in_slots, torch.int32, (N,), dev)
+    _check("out_slots", out_slots, torch.int32, (N,), dev)
     ptr = _ptr
     with _on(dev):
         _done(_kda.lib().kda_ssm_step(ptr(x), ptr(dt), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(dt_bias), ptr(y), code,
@@ -328,7 +329,7 @@ def ssm_step(x, dt, A, B, C, y, state, in_slots, out_slots, D=None, z=None, dt_b
 
 
 def _int32(name, t, shape, dev):
-    _kda._check(name, t, torch.int32, shape, dev)
+    _check(name, t, torch.int32, shape, dev)
 
 
 def beam_workspace_size(N: int, W: int, V: int, k: int) -> int:
@@ -347,7 +348,7 @@ def beam_select(logits, scores, tokens, parents, new_scores, finished=None, eos:
     dev = _gpu("logits", logits, 3)
     N, W, V = logits.shape
     dt = _dtype("logits", logits)
-    _kda._check("logits", logits, logits.dtype, logits.shape, dev)
+    _check("logits", logits, logits.dtype, logits.shape, dev)
     _fp32("scores", scores, (N, W), dev)
     if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
         raise ValueError("tokens must be a 2-D tensor [N, k]")

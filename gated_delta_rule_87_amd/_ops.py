@@ -21,6 +21,8 @@ _NULL = contextlib.nullcontext()
 # the current stream's handle without a Stream object (2 us less on every call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _changed = torch.autograd.graph.increment_version
+# the current device's number without torch's check that the GPU is initialised: the tensors are on it
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _setup(L):
@@ -47,7 +49,7 @@ def _setup(L):
 
 def _on(device):
     """The device of the call's tensors as the current one (its context only where it is another)."""
-    return _NULL if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _NULL if _current_device() == device.index else torch.cuda.device(device)
 
 
 def _stream(device) -> int:
