@@ -27,7 +27,7 @@ namespace {
 
 using std::integral_constant;
 
-constexpr int BATCH = 8;   // tokens loaded at once
+constexpr int BATCH = 8, BWD_BATCH = 4;   // tokens loaded at once
 
 template <int DT>
 constexpr int vec_of() { return 16 / elem_size(DT); }
@@ -357,19 +357,19 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvParams p, int lr_
       shift<V, W - 1>(pend, last);
     };
     const float none[V] = {};
-    Pack<DT, V> nx[BATCH], ny[BATCH];
+    Pack<DT, V> nx[BWD_BATCH], ny[BWD_BATCH];
     auto load = [&](int32_t t) {
 #pragma unroll
-      for (int r = 0; r < BATCH; ++r)
+      for (int r = 0; r < BWD_BATCH; ++r)
         if (t + r < t1) {
           load_any(nx[r], p.x, (size_t)(t + r) * p.D + d);
           load_any(ny[r], p.dy, (size_t)(t + r) * p.D + d);
         }
     };
-    for (int32_t t = t0; t < t1; t += BATCH) {
+    for (int32_t t = t0; t < t1; t += BWD_BATCH) {
       load(t);
 #pragma unroll
-      for (int r = 0; r < BATCH; ++r) {
+      for (int r = 0; r < BWD_BATCH; ++r) {
         if (t + r >= t1) break;
         if (t + r >= q.e) q.forward(s, t + r);
         if (t + r == q.b) load_before<DT, W, V>(p, q.i, q.b, q.b, d, old);
