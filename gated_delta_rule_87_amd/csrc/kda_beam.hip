@@ -74,17 +74,21 @@ struct BeamWs {
 };
 
 // Least of the groups' largest keys, as KEY has them (an operator > and a zero); the same in all
-// lanes. buf: 64 keys
+// lanes. A group is every groups-th lane, so that elements that fill only some of the lanes, as a
+// vocabulary's last ones, reach all groups. buf: 256 keys
 template <typename KEY>
 __device__ __forceinline__ KEY threshold(KEY most, int groups, KEY* buf) {
-  const int size = 256 / groups, lane = threadIdx.x & 63;   // lanes of a group: 4 .. 64
-  for (int o = 1; o < size; o <<= 1) {
+  const int lane = threadIdx.x & 63;
+  for (int o = groups; o < 64; o <<= 1) {
     const KEY other = most.from(o);
     if (other > most) most = other;
   }
-  if (threadIdx.x % size == 0) buf[threadIdx.x / size] = most;
+  buf[threadIdx.x] = most;
   __syncthreads();
-  KEY least = buf[lane % groups];
+  KEY least = buf[lane];
+#pragma unroll
+  for (int w = 1; w < 4; ++w)
+    if (buf[w * 64 + lane] > least) least = buf[w * 64 + lane];
   for (int o = 1; o < groups; o <<= 1) {
     const KEY other = least.from(o);
     if (least > other) least = other;
@@ -113,7 +117,7 @@ struct Key64 {
 template <int DT, int PER>
 __global__ __launch_bounds__(256, 4) void kda_beam_piece_kernel(BeamParams p, BeamWs w) {
   constexpr int VEC = 16 / elem_size(DT), NV = PER / VEC;
-  __shared__ Key64 s_group[64];
+  __shared__ Key64 s_group[256];
   __shared__ uint64_t s_keys[HOLD];
   __shared__ double s_sum[4];
   __shared__ int s_count[4], s_used;
@@ -251,7 +255,7 @@ struct Key96 {
 __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs w) {
   __shared__ double s_top[64], s_log[64], s_score[64];
   __shared__ bool s_none[64], s_done[64];
-  __shared__ Key96 s_group[64], s_keys[HOLD];
+  __shared__ Key96 s_group[256], s_keys[HOLD];
   __shared__ int s_count[4], s_used;
   const int tid = threadIdx.x, n = blockIdx.x, lane = tid & 63;
   if (tid == 0) s_used = 0;
@@ -288,12 +292,15 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
     }
   }
   __syncthreads();
-  const int per = w.pieces * p.k, total = p.W * per;
+  // the pieces' best ones first, then their second ones: neighbouring lanes, and so all groups of a
+  // threshold, have candidates of the same rank (in the order of the pieces, where a lane's group was
+  // the rank, the kernel took 31 us at 32 x 8 beams and not 14)
+  const int lists = p.W * w.pieces, total = lists * p.k;
   auto key = [&](int i) -> Key96 {
-    const int b = i / per, j = i - b * per;
+    const int j = i / lists, list = i - j * lists, b = list / w.pieces;
     if (s_none[b]) return {0, 0};
-    if (s_done[b]) return j == 0 ? Key96{ordered(s_score[b]), ~((uint32_t)b * p.V + p.eos)} : Key96{0, 0};
-    const uint64_t q = w.best[((int64_t)n * p.W + b) * per + j];
+    if (s_done[b]) return j == 0 && list == b * w.pieces ? Key96{ordered(s_score[b]), ~((uint32_t)b * p.V + p.eos)} : Key96{0, 0};
+    const uint64_t q = w.best[((int64_t)n * lists + list) * p.k + j];
     if (q == 0) return {0, 0};
     const double v = (((double)unordered((uint32_t)(q >> 32)) - s_top[b]) - s_log[b]) + s_score[b];
     return {ordered(v), ~((uint32_t)b * p.V + ~(uint32_t)q)};

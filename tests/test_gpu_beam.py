@@ -32,7 +32,8 @@ def check(logits, scores, k, finished=None, eos=0):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("N,W,V,k", [(1, 1, 1, 1), (1, 1, 1, 5), (2, 3, 7, 4), (1, 4, 2048, 4), (3, 4, 2049, 8), (2, 5, 5003, 16),
-                                     (1, 64, 100, 64), (2, 2, 20000, 64), (9, 8, 60000, 8), (1, 1, 100001, 33), (70, 4, 9001, 2)])
+                                     (1, 64, 100, 64), (2, 2, 20000, 64), (9, 8, 60000, 8), (1, 1, 100001, 33), (70, 4, 9001, 2),
+                                     (54, 11, 586, 11), (1, 2, 2996, 2), (2, 3, 600, 64), (130, 4, 8200, 40)])
 def test_select(N, W, V, k, dtype):
     say("beam", N, W, V, k, dtype)
     g = torch.Generator().manual_seed(V)
