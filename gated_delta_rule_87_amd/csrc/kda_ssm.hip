@@ -7,7 +7,7 @@
 // takes an exponential (8.4 cycles of a SIMD, measured) and four operations (2.6 to 3 each, with
 // more than one wave; 4.4 where an operand is scalar or comes from another lane). At 8192 tokens x
 // 8192 channels x 16 states, bf16, those alone are 140 us of the outputs' pass, where the memory
-// traffic takes 105; it measures 300 us, and the pass before it 230.
+// traffic takes 105; it measures 320 us, and the pass before it 235.
 //
 // A sequence's tokens follow each other, so the packed tokens are cut into chunks until the GPU is
 // filled. A chunk acts on the state entering it as h -> P h + R with P = exp(A sum s_t): one launch
