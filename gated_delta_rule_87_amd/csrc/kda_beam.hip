@@ -6,9 +6,9 @@
 // is read once for the largest value, the sum of exponentials and the best k values. A second
 // kernel, one workgroup a sequence, joins the beams' sums and picks the best k of all pieces'.
 // Their time goes to the exponentials and to the steps that a workgroup takes one after the other
-// (256 beams of 131072 bf16 logits: 54 us, of which reading is 13). Scores of different beams lie close together and their order is the
-// result, so sums and scores are 64 bits (an fp64 operation takes as long as an fp32 one here; the
-// exponential of 13 operations is good to 1e-11).
+// (256 beams of 131072 bf16 logits: 54 us, of which reading is 13). Scores of different beams lie
+// close together and their order is the result, so sums and scores are 64 bits (an fp64 operation
+// takes twice an fp32 one's time here; the exponential of 18 of them is good to 1e-11).
 //
 // The best k are found by counting, not by sorting: the 256 lanes form k' >= k groups, each with
 // its best element, and the least of those k' is a threshold that at least k elements reach, about
