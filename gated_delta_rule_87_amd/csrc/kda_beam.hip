@@ -42,10 +42,11 @@ __device__ __forceinline__ double unordered(uint64_t u) {
   return __builtin_bit_cast(double, u >> 63 ? u & ~(1ull << 63) : ~u);
 }
 
-// exp(t), t <= 0 or NaN: 2^n 2^f, |f| <= 1/2, a Taylor series of nine terms (7e-12). Below -40 it is
-// nothing beside the sum, which is at least 1 (2^24 of them are 7e-11).
+// exp(t), t <= 0 or NaN: 2^n 2^f, |f| <= 1/2, a Taylor series of nine terms (7e-12). It is 0 below
+// -745, as in 64 bits: masked elements add nothing, and a beam with one other element keeps its
+// score to the last bit, which a finished beam's equals. (n stays a number of 32 bits.)
 __device__ __forceinline__ double exp_below(double t) {
-  t = t < -40.0 ? -40.0 : t;
+  t = t < -1100.0 ? -1100.0 : t;
   const double y = t * 1.4426950408889634074, n = __builtin_rint(y), f = (y - n) * 0.69314718055994530942;
   double s = 1.0 / 362880.0;
   s = fma(s, f, 1.0 / 40320.0);

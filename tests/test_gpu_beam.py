@@ -186,3 +186,25 @@ def test_refusals():
         kda.cache_reorder(pool, i, i.clone(), i)
     with pytest.raises(ValueError):
         kda.cache_reorder(pool, i, i[:1], i.clone())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("V", [50, 9000, 200000])
+def test_masked_tokens_add_nothing(V, dtype):
+    """A beam that has one token left (a forced one) goes on at its score as it is, as a finished beam
+    does: of equal scores the lowest beam comes first, wherever its token is."""
+    say("forced", V, dtype)
+    for low in (float("-inf"), torch.finfo(dtype).min, -2.0 ** 15):
+        x = torch.full((3, 6, V), low)
+        for n in range(3):
+            for b, v in enumerate((V // 2, V - 1, 0, 7, V // 3, V // 5)):
+                x[n, b, v] = (0.0, 5.0, -3.0)[n]
+        scores = torch.tensor([-1.5, -0.25, -7.0])[:, None].expand(3, 6).contiguous()
+        check(x.to(dtype), scores, 6)
+        for fin in ([0, 0, 0, 0, 0, 1], [0, 0, 1, 0, 1, 0], [1, 0, 0, 0, 0, 0]):
+            check(x.to(dtype), scores, 6, torch.tensor([fin] * 3, dtype=torch.int32), eos=V // 7)
+        # two tokens left, alike: half of the beam's probability each
+        for n in range(3):
+            for b, v in enumerate((3, 11, V - 2, 21, 20, 30)):
+                x[n, b, v] = (0.0, 5.0, -3.0)[n]
+        check(x.to(dtype), scores, 12)
