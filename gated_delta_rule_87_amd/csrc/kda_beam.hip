@@ -28,14 +28,14 @@ using std::integral_constant;
 
 constexpr int HOLD = 512;   // elements that may reach the threshold
 
-// bits that grow with the number; 0 is below all of them
+// bits that grow with the number, the same for both zeros (-0.0 + 0.0 is +0.0); 0 is below all of them
 __device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(f + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
 __device__ __forceinline__ uint64_t ordered(double f) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, f);
+  const uint64_t u = __builtin_bit_cast(uint64_t, f + 0.0);
   return u >> 63 ? ~u : u | (1ull << 63);
 }
 __device__ __forceinline__ double unordered(uint64_t u) {

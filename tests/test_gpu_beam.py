@@ -208,3 +208,27 @@ def test_masked_tokens_add_nothing(V, dtype):
             for b, v in enumerate((3, 11, V - 2, 21, 20, 30)):
                 x[n, b, v] = (0.0, 5.0, -3.0)[n]
         check(x.to(dtype), scores, 12)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("V", [2, 3000, 70000])
+def test_zeros_of_both_signs_are_equal(V, dtype):
+    """-0.0 and +0.0 are one value: within a piece, across pieces, for either way of cutting a row into
+    pieces (few rows and many), and as a finished beam's score."""
+    say("zeros", V, dtype)
+    g = torch.Generator().manual_seed(V)
+    x = torch.zeros(2, 4, V)
+    x[..., :5] = -0.0
+    check(x.to(dtype), torch.zeros(2, 4), min(4, V))
+    x = torch.where(torch.rand(2, 4, V, generator=g) < 0.5, -0.0, 0.0)
+    check(x.to(dtype), torch.zeros(2, 4), 16)
+    x = torch.where(torch.rand(1, 20, V, generator=g) < 0.01, 0.0, -0.0)   # mostly negative ones
+    check(x.to(dtype), torch.zeros(1, 20), 64)
+    scores = torch.zeros(2, 4)
+    scores[:, 0], scores[1, 2] = -0.0, -0.0
+    x = torch.full((2, 4, V), float("-inf"))
+    x[..., V // 2] = -0.0                # a sure token: its score is the beam's
+    for fin in ([1, 1, 1, 1], [1, 0, 1, 0], [0, 1, 0, 1]):
+        check(x.to(dtype), scores, 4, torch.tensor([fin] * 2, dtype=torch.int32), eos=V - 1)
+    if V == 3000:
+        check(torch.where(torch.rand(72, 8, V, generator=g) < 0.5, -0.0, 0.0).to(dtype), torch.zeros(72, 8), 4)
