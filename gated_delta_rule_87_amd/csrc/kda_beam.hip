@@ -72,6 +72,7 @@ struct BeamWs {
   double* sum;      // of exp(value - top)
   float* top;       // largest value; NaN where one is NaN or +infinity
   int32_t pieces;
+  int32_t size;     // elements of a piece
   int32_t groups;   // k': a power of two from 4 to 64, at least k
 };
 
@@ -254,13 +255,34 @@ struct Key96 {
   __device__ __forceinline__ Key96 from(int mask) const { return {from_lane(s, mask), from_lane(i, mask)}; }
 };
 
+// A logit of a tensor of any type
+__device__ __forceinline__ float logit_of(const BeamParams& p, size_t i) {
+  float x;
+  if (p.dtype == BF16) load_f32<BF16, 1>(p.logits, i, &x);
+  else if (p.dtype == FP32) load_f32<FP32, 1>(p.logits, i, &x);
+  else load_f32<FP16, 1>(p.logits, i, &x);
+  return x;
+}
+
+// The pieces' best ones go by their logits. Where different logits have one score (64 bits of a beam's
+// score of -1e30, or of the sum, swallow what tells them apart), a piece may so have kept larger logits
+// in the place of lower tokens. That matters at the k-th score alone: fewer than k are above it, and
+// those are all in their pieces' lists. A list that ends with that score, and whose last logit has a
+// neighbour in fp32 of the same score, is the sign of it (no list ends above the k-th score): the
+// continuations with the k-th score are then taken from the logits themselves, in order, until there
+// are k. (32 x 8 beams of 131072 bf16 tokens, of which all but one do not count: 76 us a call, 60 where all do.)
 __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs w) {
   __shared__ double s_top[64], s_log[64], s_score[64];
   __shared__ bool s_none[64], s_done[64];
   __shared__ Key96 s_group[256], s_keys[HOLD];
-  __shared__ int s_count[4], s_used;
+  __shared__ unsigned long long s_kth, s_lost;
+  __shared__ int s_count[4], s_used, s_above;
   const int tid = threadIdx.x, n = blockIdx.x, lane = tid & 63;
-  if (tid == 0) s_used = 0;
+  if (tid == 0) {
+    s_used = 0;
+    s_kth = s_lost = 0;
+    s_above = 0;
+  }
   for (int b = tid >> 6; b < p.W; b += 4) {   // a wave: a beam's sum over its pieces
     const int64_t row = (int64_t)n * p.W + b, at = row * w.pieces;
     const bool done = p.finished && p.finished[row] != 0;
@@ -298,14 +320,19 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
   // threshold, have candidates of the same rank (in the order of the pieces, where a lane's group was
   // the rank, the kernel took 31 us at 32 x 8 beams and not 14)
   const int lists = p.W * w.pieces, total = lists * p.k;
-  auto key = [&](int i) -> Key96 {
+  auto score = [&](int b, float x) { return ordered((((double)x - s_top[b]) - s_log[b]) + s_score[b]); };
+  uint64_t lost = 0;   // best score at the end of a list that may have left out others with it
+  auto key = [&](int i, auto first) -> Key96 {   // first: its list's end is looked at
     const int j = i / lists, list = i - j * lists, b = list / w.pieces;
     if (s_none[b]) return {0, 0};
     if (s_done[b]) return j == 0 && list == b * w.pieces ? Key96{ordered(s_score[b]), ~((uint32_t)b * p.V + p.eos)} : Key96{0, 0};
     const uint64_t q = w.best[((int64_t)n * lists + list) * p.k + j];
     if (q == 0) return {0, 0};
-    const double v = (((double)unordered((uint32_t)(q >> 32)) - s_top[b]) - s_log[b]) + s_score[b];
-    return {ordered(v), ~((uint32_t)b * p.V + ~(uint32_t)q)};
+    const uint32_t x = (uint32_t)(q >> 32);
+    const uint64_t v = score(b, unordered(x));
+    if (decltype(first)::value && j == p.k - 1 && v > lost &&
+        (score(b, unordered(x - 1)) == v || score(b, unordered(x + 1)) == v)) lost = v;
+    return {v, ~((uint32_t)b * p.V + ~(uint32_t)q)};
   };
   constexpr int HELD = 8;   // keys of a lane that are kept, where that is all of them: formed once
   const bool held = total <= 256 * HELD;
@@ -315,17 +342,21 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
 #pragma unroll
       for (int j = 0; j < HELD; ++j) f(own[j]);
     } else {
-      for (int i = tid; i < total; i += 256) f(key(i));
+      for (int i = tid; i < total; i += 256) f(key(i, std::false_type{}));
     }
   };
   if (held) {
 #pragma unroll
-    for (int j = 0; j < HELD; ++j) own[j] = tid + 256 * j < total ? key(tid + 256 * j) : Key96{0, 0};
+    for (int j = 0; j < HELD; ++j) own[j] = tid + 256 * j < total ? key(tid + 256 * j, std::true_type{}) : Key96{0, 0};
   }
   Key96 most{0, 0};
-  each([&](const Key96& q) {
+  auto better = [&](const Key96& q) {
     if (q > most) most = q;
-  });
+  };
+  if (held) each(better);
+  else
+    for (int i = tid; i < total; i += 256) better(key(i, std::true_type{}));
+  if (lost != 0) atomicMax(&s_lost, (unsigned long long)lost);
   Key96 least = threshold(most, w.groups, s_group);
   if (least.s == 0) least = {1, 0};
   auto gather = [&]() {   // as in a piece
@@ -371,22 +402,63 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
     __syncthreads();
     gather();
   }
+  auto put = [&](int place, const Key96& q) {
+    const uint32_t at = ~q.i;
+    const int64_t to = (int64_t)n * p.k + place;
+    p.tokens[to] = (int32_t)(at % (uint32_t)p.V);
+    p.parents[to] = (int32_t)(at / (uint32_t)p.V);
+    p.new_scores[to] = (float)unordered(q.s);
+  };
   for (int i = tid; i < count; i += 256) {
     const Key96 q = s_keys[i];
     int place = 0;
     for (int j = 0; j < count; ++j) place += s_keys[j] > q;
-    if (place < p.k) {
-      const uint32_t at = ~q.i;
-      const int64_t to = (int64_t)n * p.k + place;
-      p.tokens[to] = (int32_t)(at % (uint32_t)p.V);
-      p.parents[to] = (int32_t)(at / (uint32_t)p.V);
-      p.new_scores[to] = (float)unordered(q.s);
-    }
+    if (place < p.k) put(place, q);
+    if (place == p.k - 1) s_kth = q.s;
   }
   for (int i = count + tid; i < p.k; i += 256) {
     const int64_t to = (int64_t)n * p.k + i;
     p.tokens[to] = p.parents[to] = -1;
     p.new_scores[to] = -INFINITY;
+  }
+  if (s_lost == 0) return;
+  __syncthreads();
+  const uint64_t kth = s_kth;
+  if (s_lost != kth) return;   // (0 where there are fewer than k: none was left out)
+  int above = 0;
+  for (int i = tid; i < count; i += 256) above += s_keys[i].s > kth;
+  if (above > 0) atomicAdd(&s_above, above);
+  __syncthreads();
+  int place = s_above;   // of the next one, the same in all lanes
+  for (int list = 0; list < lists && place < p.k; ++list) {
+    const int b = list / w.pieces, first = (list - b * w.pieces) * w.size;
+    if (s_none[b]) continue;
+    if (s_done[b]) {
+      if (first != 0 || ordered(s_score[b]) != kth) continue;
+      if (tid == 0) put(place, {kth, ~((uint32_t)b * p.V + p.eos)});
+      ++place;
+      continue;
+    }
+    bool some = false;   // (a piece without one in its list has none)
+    for (int j = tid; j < p.k; j += 256) some = some || key(j * lists + list, std::false_type{}).s == kth;
+    if (!__syncthreads_or(some)) continue;
+    const int end = p.V - first < w.size ? p.V : first + w.size;
+    for (int v0 = first; v0 < end && place < p.k; v0 += 256) {
+      const int v = v0 + tid;
+      const float x = v < end ? logit_of(p, ((size_t)n * p.W + b) * p.V + v) : -INFINITY;
+      const bool hit = x > -INFINITY && score(b, x) == kth;
+      const uint64_t hits = __ballot(hit);
+      __syncthreads();   // the counts before have been read
+      if (lane == 0) s_count[tid >> 6] = __popcll(hits);
+      __syncthreads();
+      int to = place + __popcll(hits & (((uint64_t)1 << lane) - 1));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < tid >> 6) to += s_count[i];
+        place += s_count[i];
+      }
+      if (hit && to < p.k) put(to, {kth, ~((uint32_t)b * p.V + (uint32_t)v)});
+    }
   }
 }
 
@@ -402,7 +474,8 @@ int per_lane(int64_t rows, int64_t V) { return rows * ((V + 256 * 32 - 1) / (256
 
 size_t lay_out(BeamWs& w, uint8_t* at, int64_t rows, int64_t V, int64_t k) {
   const int per = per_lane(rows, V);
-  w.pieces = (int32_t)((V + 256 * per - 1) / (256 * per));
+  w.size = 256 * per;
+  w.pieces = (int32_t)((V + w.size - 1) / w.size);
   w.groups = 4;
   while (w.groups < k) w.groups *= 2;
   size_t used = 0;

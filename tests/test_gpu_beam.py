@@ -232,3 +232,37 @@ def test_zeros_of_both_signs_are_equal(V, dtype):
         check(x.to(dtype), scores, 4, torch.tensor([fin] * 2, dtype=torch.int32), eos=V - 1)
     if V == 3000:
         check(torch.where(torch.rand(72, 8, V, generator=g) < 0.5, -0.0, 0.0).to(dtype), torch.zeros(72, 8), 4)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("V", [60, 3000, 33000])
+def test_logits_that_a_score_swallows(V, dtype):
+    """Scores beside which logits are lost, as beams that do not count have them at a first step: their
+    continuations are equal, so the lowest tokens come first, not those of the largest logits."""
+    say("swallowed", V, dtype)
+    g = torch.Generator().manual_seed(V + 1)
+    x = normal(g, (2, 4, V), dtype, 3.0)
+    x[:, 0, 2:] = float("-inf")              # two live continuations, the others are of the beams after it
+    x[1, 1, :40] = float("-inf")
+    for far in (torch.finfo(F).min, -1e30, -2.0 ** 70):
+        scores = torch.full((2, 4), far)
+        scores[:, 0] = 0.0
+        check(x, scores, 8)
+        check(x, scores, 64)
+        fin = torch.tensor([[0, 0, 1, 0]] * 2, dtype=torch.int32)
+        check(x, scores, 50, fin, eos=V - 1)
+    # some of them lost: steps of 2^-12 at a score of 2^40
+    scores = torch.full((2, 4), -2.0 ** 40)
+    scores[:, 0] = 0.0
+    y = (x.float() * 2.0 ** -13).to(dtype)
+    y[x == float("-inf")] = float("-inf")
+    check(y, scores, 20)
+    # logits far below the sum's last bit, and most of them so
+    tiny = normal(g, (2, 3, V), F, 2.0 ** -80).to(BF if dtype == H16 else dtype)
+    check(tiny, torch.full((2, 3), -1.0), 16)
+    tiny[:, :, ::7] = 1.0
+    check(tiny, torch.full((2, 3), -1.0), 64)
+    # the last piece's and the first token's
+    tiny = torch.full((1, 2, V), -5.0, dtype=dtype)
+    tiny[0, :, V - 1], tiny[0, 1, V - 9], tiny[0, 0, 0] = 1e-7, 0.0, 1e-7
+    check(tiny, torch.tensor([[-2.0 ** 40, -2.0 ** 40]]), 3)
