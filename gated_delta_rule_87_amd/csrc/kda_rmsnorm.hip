@@ -105,18 +105,31 @@ __device__ __forceinline__ void load_param(const float* p, int i, int c, float n
 // ---- 8-bit outputs ------------------------------------------------------------------
 
 // A group's scale, and what its values are multiplied by, first with `up`: values whose scale is
-// tiny (and its reciprocal infinite) are brought nearer to 1 before.
+// tiny (and its reciprocal infinite) are brought nearer to 1 before. A scale below the normal numbers
+// is rounded to whole steps of 2^-149, at the worst to two thirds of what it should be: the quotients
+// then pass 448 by up to half, and are held there.
 struct Scale {
   float value, up, inv;
+  bool coarse;
   __device__ __forceinline__ explicit Scale(float most) {
     value = most / E4M3_MAX;
     if (value == 0.0f) value = 1.0f;
     up = most < 0x1p-100f ? 0x1p96f : 1.0f;
     inv = 1.0f / (value * up);
     if (up != 1.0f && value == 1.0f) up = inv = 1.0f;
+    coarse = value < 0x1p-126f;
+  }
+  template <int V>
+  __device__ __forceinline__ void divide(float* f) const {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = f[e] * up * inv;
+    if (coarse) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = f[e] > E4M3_MAX ? E4M3_MAX : f[e] < -E4M3_MAX ? -E4M3_MAX : f[e];   // (NaN stays)
+    }
   }
 };
-// rounded to nearest; the scale brings all finite values within what the format holds
+// rounded to nearest; finite values of a group over its scale are within what the format holds
 template <int V>
 __device__ __forceinline__ void store_e4m3(const float* f, void* p, size_t i, int c, bool whole) {
   uint8_t* a = static_cast<uint8_t*>(p) + i;
@@ -224,9 +237,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_rmsnorm_fwd_kernel(RmsParams
         const Scale sc(most[u]);
         if (m < p.M && lane == 0) p.scales[m] = sc.value;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) s[u][i][e] = s[u][i][e] * sc.up * sc.inv;
+        for (int i = 0; i < NV; ++i) sc.divide<VEC>(s[u][i]);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -237,8 +248,7 @@ __global__ __launch_bounds__(wg_of(LANES)) void kda_rmsnorm_fwd_kernel(RmsParams
           for (int e = 0; e < VEC; ++e) a = Most{}(a, fabsf(s[u][i][e]));
           const Scale sc(over_lanes<BLOCK / VEC>(a, Most{}));
           if (m < p.M && col % BLOCK == 0 && c[i] > 0) p.scales[m * blocks + col / BLOCK] = sc.value;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) s[u][i][e] = s[u][i][e] * sc.up * sc.inv;
+          sc.divide<VEC>(s[u][i]);
         }
         if (m >= p.M || c[i] <= 0) continue;
         const size_t at = (size_t)m * p.D + col;
@@ -326,8 +336,7 @@ __global__ __launch_bounds__(1024) void kda_rmsnorm_fwd_long_kernel(RmsParams p)
       if (GROUP != 0) {
         const Scale sc(most);
         if (GROUP == 1 && col % BLOCK == 0 && c > 0) p.scales[m * blocks + col / BLOCK] = sc.value;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s[e] = s[e] * sc.up * sc.inv;
+        sc.divide<VEC>(s);
       }
       if (c <= 0) return;
       if (GROUP == 0) {

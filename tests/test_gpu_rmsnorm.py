@@ -197,3 +197,28 @@ def test_refusals():
         kda.rmsnorm_fwd(x, None, -1.0, y)
     with pytest.raises(ValueError):
         kda.rmsnorm_bwd(x, x, None, None, y)
+
+
+@pytest.mark.parametrize("D", [64, 300, 2100, 20000])
+@pytest.mark.parametrize("per_row", [True, False])
+def test_8_bits_of_coarse_scales(D, per_row):
+    """Scales of a few steps of 2^-149: the quotient can pass 448 by up to half, and is held there."""
+    i = make(4, D, F, 8)
+    group = D if per_row else 128
+    for steps in (130, 180, 250, 400, 900, 2000):
+        wt = torch.full((D,), steps * 2.0 ** -149)
+        _, _, y = pl.rmsnorm(i["x"], None, wt, 0.0)
+        scales, y8 = blank((4, -(-D // group))), torch.empty(4, D, device=dev(), dtype=E8)
+        kda.rmsnorm_fwd(gpu(i["x"]), gpu(wt), 0.0, y8, scales=scales)
+        got, sc = y8.float().cpu().double(), scales.cpu().double()
+        for k in range(sc.shape[1]):
+            c = slice(k * group, min(D, (k + 1) * group))
+            v, s = y.v[:, c], sc[:, k, None]
+            # y is rounded to whole steps, its largest / 448 to a whole one too
+            assert bool(((s[:, 0] - v.abs().amax(1) / 448).abs() <= 2.0 ** -149).all()), (steps, k)
+            q = (v / s).clamp(-448, 448)
+            tol = 2.0 ** -149 / s + 1e-5 * q.abs()
+            tol = tol + torch.maximum((q.abs() + tol) * 2.0 ** -4, torch.tensor(2.0 ** -10, dtype=torch.float64))
+            assert bool(((got[:, c] - q).abs() <= tol).all()), (steps, k)
+            # t steps, t > 1/2, are rounded to 2 t at most: the largest quotient is not below 224
+            assert bool((got[:, c].abs().amax(1) >= 224).all()), (steps, k)
