@@ -554,6 +554,16 @@ __global__ __launch_bounds__(64, waves_of(S)) void kda_ssm_fwd_kernel(SsmParams 
   }
 }
 
+// 2^e h + r. A chunk's decay can be beyond fp32 (A > 0, or s < 0) where its product with h is not, or
+// where h is 0, as behind zeros of padding: then the exponent's whole part is applied to the product.
+__device__ __forceinline__ float passed_on(float e, float h, float r) {
+  if (e > 64.0f && e < INFINITY) {
+    const float n = __builtin_rintf(e);
+    return __builtin_ldexpf(fast_exp2(e - n) * h, n < 1024.0f ? (int)n : 1024) + r;
+  }
+  return fmaf(fast_exp2(e), h, r);
+}
+
 // maps[c] becomes the state that leaves chunk c (BACK: the gradient that leaves chunk c + 1 towards
 // its first token). 32 states of channels to a workgroup, 8 lanes each: a lane joins the maps of an
 // eighth of the chunks, takes the state that enters them from the lanes before it, and runs through
@@ -583,7 +593,7 @@ __global__ __launch_bounds__(256) void kda_ssm_pass_kernel(SsmParams p, SsmWs w,
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         if (c + k >= c1) break;
-        h = first || reset[k] ? r[k] : fmaf(fast_exp2(A * s[k]), h, r[k]);
+        h = first || reset[k] ? r[k] : passed_on(A * s[k], h, r[k]);
         first = false;
         put(c + k, h, s[k], reset[k] != 0);
       }
@@ -602,7 +612,7 @@ __global__ __launch_bounds__(256) void kda_ssm_pass_kernel(SsmParams p, SsmWs w,
   __syncthreads();
   float h = 0.0f;
   for (int k = 0; k < part; ++k)
-    if (k * each < count) h = k == 0 || s_reset[k] ? s_r[k][j] : fmaf(fast_exp2(A * s_s[k][j]), h, s_r[k][j]);
+    if (k * each < count) h = k == 0 || s_reset[k] ? s_r[k][j] : passed_on(A * s_s[k][j], h, s_r[k][j]);
   run(h, part == 0, [&](int c, float v, float, bool) {
     if (at < n) w.maps[chunk(c) * n + i] = v;
   });

@@ -565,7 +565,8 @@ int kda_conv_step(const void *x, const float *weight, const float *bias, void *y
  *
  *   x, dt, z, y, dy, dx, d_dt, d_z
  *                     [B, T, D] in `dtype`; T may be 0 (all tokens' tensors may then be NULL)
- *   A, dA             fp32 [D, E], 1 <= E <= 64; A is finite, A < 0 forgets
+ *   A, dA             fp32 [D, E], 1 <= E <= 64; A is finite, A < 0 forgets (s_t A[e] of a
+ *                     token is to stay below 88, where its exponential ends)
  *   Bm, Cm, dB, dC    [B, T, G, E] in `dtype`; G >= 1 divides D
  *   skip, dt_bias, d_skip, d_dt_bias
  *                     fp32 [D], or NULL; a gradient is given only where its input is

@@ -287,3 +287,70 @@ def test_refusals():
     with pytest.raises(ValueError):
         kda.ssm_bwd(j["x"], j["dt"], j["A"], j["B"], j["C"], j["dy"], blank((1, 8, 4)), y, blank(y.shape), blank((8, 4)),
                     blank(j["B"].shape), blank(j["B"].shape), d_D=blank((8,)))
+
+
+def grows(D=24, E=4, T=700, seed=12):
+    """Without softplus, s > 0: decays of channels with A > 0 grow by up to 1.8 a token, exp(115) over 64."""
+    i, n = make(1, T, D, E, 1, None, F, F, seed)
+    i["dt"] = i["dt"].abs() * 0.3 + 1.2
+    i["bias"], i["z"] = None, None
+    i["A"][::2] = -i["A"][::2] * 0.3
+    i["A"].clamp_(max=1.2)
+    i["h0"].zero_()
+    i["df"] = None
+    return i, n
+
+
+def both(i, n, grad=True):
+    j = {a: gpu(t) for a, t in i.items()}
+    y, fin, carry = forward(j, None, n, F, softplus=False)
+    return {"y": y, "final": fin, **(backward(j, None, n, carry, softplus=False) if grad else {})}
+
+
+def compare(got, want):
+    for name, t in got.items():
+        t = t.cpu()
+        assert bool(torch.isfinite(t).all()), name
+        pl.near(name, t.reshape(-1, *t.shape[2:]) if name in TOKENS else t, want[name])
+
+
+def test_growing_decays_of_states_that_are_zero():
+    """Padding with zeros in front: the state stays 0, whatever a chunk's decay is."""
+    T, first = 700, 660
+    i, n = grows()
+    i["x"][:, :first] = 0
+    got = both(i, n, grad=False)   # (a gradient would pass fp32 on its way to the first token)
+    assert bool((got["y"][:, :first] == 0).all())
+    got["y"] = got["y"][:, first:]
+    end = {a: t[:, first:] if a in ("x", "dt", "B", "C", "dy") else t for a, t in i.items()}
+    compare(got, plain(end, [(0, T - first)], softplus=False, grad=False))
+
+
+def test_growing_decays_of_gradients_that_are_zero():
+    """No gradient from the last tokens: it stays 0 towards the first ones."""
+    T, last = 700, 40
+    i, n = grows(seed=13)
+    i["x"].zero_()                 # (so that the states are 0)
+    i["dy"][:, last:] = 0
+    got = both(i, n)
+    for name in TOKENS:
+        if name in got:
+            assert bool((got[name][:, last:] == 0).all()), name
+            got[name] = got[name][:, :last]
+    begin = {a: t[:, :last] if a in ("x", "dt", "B", "C", "dy") else t for a, t in i.items()}
+    compare(got, plain(begin, [(0, last)], softplus=False))
+
+
+@pytest.mark.parametrize("T", [192, 1344])
+def test_growing_decays_of_states_that_are_small(T):
+    """A chunk's decay of exp(95) times a state, or a gradient, far below 1: the products are in range."""
+    i, n = grows(T=T, seed=14)
+    g = torch.Generator().manual_seed(3)
+    i["h0"], i["df"] = normal(g, i["h0"].shape), normal(g, i["h0"].shape)
+    i["A"][::2], i["A"][1::2] = 1.2, -0.1
+    # three blocks of 64 tokens with decays of about exp(-76), exp(95) and exp(-21)
+    step = torch.tensor([-0.9, 1.13, -0.25])[torch.arange(T) // 64 % 3]
+    i["dt"] = step[None, :, None] * (1.0 + 0.2 * torch.rand(i["dt"].shape, generator=g))
+    i["x"][0, 5:] = 0
+    i["dy"][0, :T - 5] = 0
+    compare(both(i, n), plain(i, [(0, T)], softplus=False))
