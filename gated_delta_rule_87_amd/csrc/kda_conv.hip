@@ -67,6 +67,22 @@ __device__ __forceinline__ void load_state_any(const void* p, int dtype, size_t 
   }
 }
 
+template <int DT, int V>
+__device__ __forceinline__ void store_any_f32(void* p, size_t i, const float* f) {
+  constexpr int M = V * elem_size(DT) > 16 ? 16 / elem_size(DT) : V;
+#pragma unroll
+  for (int j = 0; j < V; j += M) {
+    Pack<DT, M> q;
+    q.pack(f + j);
+    __builtin_memcpy(static_cast<uint8_t*>(p) + (i + j) * elem_size(DT), &q.r, M * elem_size(DT));
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_state_any(void* p, int dtype, size_t i, const float* f) {
+  if (dtype == FP32) store_any_f32<FP32, V>(p, i, f);
+  else if (dtype == BF16) store_any_f32<BF16, V>(p, i, f);
+}
+
 __device__ __forceinline__ Seqs seqs_of(const ConvParams& p) { return {p.cu, p.nseq, p.T, p.tokens}; }
 
 template <int W, int V>
@@ -292,8 +308,8 @@ __device__ __forceinline__ void initial_grads(const ConvParams& p, int block, in
         }
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      store_state<V>(p.dinit, p.dinit_dtype, ((size_t)n * (W - 1) + j) * p.D + d, out[j]);
+    for (int j = 0; j < W - 1; ++j)   // (4 channels of rows that are no whole 16 bytes: states begin anywhere there)
+      store_state_any<V>(p.dinit, p.dinit_dtype, ((size_t)n * (W - 1) + j) * p.D + d, out[j]);
   }
 }
 

@@ -188,3 +188,30 @@ def test_versions_and_refusals():
         kda.conv_fwd(x, w, None, y, initial_state=torch.zeros(1, 4, 8, device=dev()))
     with pytest.raises(ValueError):
         kda.conv_fwd(x, w, None, y, initial_state=torch.zeros(1, 3, 8, device=dev(), dtype=H16))
+
+
+@pytest.mark.parametrize("state", [F, BF], ids=str)
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("D", [4, 12, 20, 33])
+def test_states_that_begin_at_any_element(D, dtype, state):
+    """Where rows are no whole vectors of the token tensors, states may begin at any element (as layers
+    of a cache do): the same bits as from aligned ones."""
+    D += dtype == F and D % 4 == 0
+    say("conv states", D, dtype, state)
+    bounds = [0, 2, 2, 19, 60]
+    i, n = make(1, 60, D, 4, bounds, dtype, state, 3)
+    j, cu = {a: gpu(t) for a, t in i.items()}, cu_of(bounds)
+
+    def run(off):
+        def at(t=None):   # a copy, or an output, `off` elements into its memory
+            v = blank((n * 3 * D + 8,), state)[off:off + n * 3 * D].view(n, 3, D)
+            return v if t is None else v.copy_(t)
+        y, fin, d0, dx = blank(j["x"].shape, dtype), at(), at(), blank(j["x"].shape, dtype)
+        h0, df = at(j["h0"]), at(j["df"])
+        kda.conv_fwd(j["x"], j["w"], j["b"], y, initial_state=h0, final_state=fin, cu_seqlens=cu)
+        kda.conv_bwd(j["x"], j["w"], j["b"], j["dy"], dx, initial_state=h0, d_final=df, d_initial=d0, cu_seqlens=cu)
+        return y, fin, dx, d0
+    want = run(0)
+    assert not any(bool(torch.isnan(t).any()) for t in want)
+    for off in (1, 2, 3):
+        assert all(same(a, b) for a, b in zip(run(off), want)), off
