@@ -472,38 +472,40 @@ void by_dtype(int dt, F f) {
 // Elements of a lane: many, or few where the GPU would not be filled so.
 int per_lane(int64_t rows, int64_t V) { return rows * ((V + 256 * 32 - 1) / (256 * 32)) >= 512 ? 32 : 8; }
 
-size_t lay_out(BeamWs& w, uint8_t* at, int64_t rows, int64_t V, int64_t k) {
-  const int per = per_lane(rows, V);
-  w.size = 256 * per;
-  w.pieces = (int32_t)((V + w.size - 1) / w.size);
-  w.groups = 4;
-  while (w.groups < k) w.groups *= 2;
+size_t lay_out(BeamWs& w, uint8_t* at, int64_t items, int64_t k) {
   size_t used = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = at ? at + used : nullptr;
     used += (bytes + 255) / 256 * 256;
     return r;
   };
-  const size_t items = (size_t)rows * w.pieces;
-  w.best = reinterpret_cast<uint64_t*>(take(items * k * sizeof(uint64_t)));
-  w.sum = reinterpret_cast<double*>(take(items * sizeof(double)));
-  w.top = reinterpret_cast<float*>(take(items * sizeof(float)));
+  w.best = reinterpret_cast<uint64_t*>(take((size_t)items * k * sizeof(uint64_t)));
+  w.sum = reinterpret_cast<double*>(take((size_t)items * sizeof(double)));
+  w.top = reinterpret_cast<float*>(take((size_t)items * sizeof(float)));
   return used;
 }
 
 }  // namespace
 
+// Room for what any call of at most this size takes (few rows have four times as many pieces): a
+// workspace for the largest batch serves the smaller ones.
 size_t beam_workspace(int64_t N, int64_t W, int64_t V, int64_t k) {
+  const int64_t rows = N * W, many = rows * ((V + 256 * 32 - 1) / (256 * 32)), few = rows * ((V + 256 * 8 - 1) / (256 * 8));
+  const int64_t most_few = few < 4 * 511 ? few : 4 * 511;   // 8 elements a lane: less than 512 pieces of 32
   BeamWs w{};
-  return lay_out(w, nullptr, N * W, V, k);
+  return lay_out(w, nullptr, many > most_few ? many : most_few, k);
 }
 
 hipError_t launch_beam_select(const BeamParams& p, void* workspace, hipStream_t stream) {
   if (p.N == 0) return hipSuccess;
-  BeamWs w{};
   const int64_t rows = (int64_t)p.N * p.W;
-  lay_out(w, static_cast<uint8_t*>(workspace), rows, p.V, p.k);
+  BeamWs w{};
+  w.size = 256 * per_lane(rows, p.V);
+  w.pieces = (int32_t)(((int64_t)p.V + w.size - 1) / w.size);
+  w.groups = 4;
+  while (w.groups < p.k) w.groups *= 2;
   const int64_t items = rows * w.pieces;
+  lay_out(w, static_cast<uint8_t*>(workspace), items, p.k);
   const unsigned blocks = (unsigned)(items < 65536 ? items : 65536);
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;

@@ -155,6 +155,7 @@ struct SsmParams {
 struct SsmWs {
   int32_t tiles, per_group;   // workgroups across the channels, and across a group's
   int32_t len, chunks;        // tokens of a chunk
+  int32_t most;               // chunks that a call of at most as many tokens can have
   float* maps;                // [chunks - 1][D][E]
   float* sums;                // [chunks - 1][D] sum of s
   int32_t* resets;            // [chunks - 1] whether a sequence begins in the chunk

@@ -1048,6 +1048,7 @@ SsmWs shape_of(int64_t tokens, int64_t D, int64_t E, int64_t G, bool backward) {
   w.len = (int32_t)(len * BLK);
   w.chunks = (int32_t)((blocks + len - 1) / len);
   if (w.chunks < 1) w.chunks = 1;
+  w.most = (int32_t)(blocks < 1 ? 1 : blocks < want ? blocks : want);
   return w;
 }
 
@@ -1104,8 +1105,11 @@ bool ssm_fits(int64_t tokens, int64_t D, int64_t E, int64_t G) {
   return (int64_t)a.tiles * a.chunks < INT32_MAX / 256 && (int64_t)b.tiles * b.chunks < INT32_MAX / 256;
 }
 
+// Room for what any call of at most so many tokens takes (chunks are whole blocks: fewer tokens can
+// have more of them)
 size_t ssm_workspace(int64_t tokens, int64_t D, int64_t E, int64_t G, bool backward) {
   SsmWs w = shape_of(tokens, D, E, G, backward);
+  w.chunks = w.most;
   return lay_out(w, nullptr, tokens, D, E, G, backward);
 }
 

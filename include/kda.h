@@ -587,7 +587,7 @@ int kda_conv_step(const void *x, const float *weight, const float *bias, void *y
  *                     of their own that no timing changes
  *   workspace         caller-owned, kda_ssm_workspace_size(B, T, D, E, G, N, backward) bytes (N = 0
  *                     without cu_seqlens; backward: 0 or 1, the direction), 256-byte aligned;
- *                     contents need no initialisation and are clobbered
+ *                     contents need no initialisation and are clobbered. It serves fewer tokens too
  * Outputs do not overlap inputs, except as said. D is 1 to 2^20.
  *
  * kda_ssm_step: one token for each of N sequences, x, dt, z, y [N, D], Bm, Cm [N, G, E],
@@ -629,7 +629,8 @@ int kda_ssm_step(const void *x, const void *dt, const float *A, const void *Bm, 
  *                     k. 1 <= k <= 64.
  *   new_scores        fp32 [N, k]: their scores, rounded once; -infinity there. May be scores
  *                     where k = W.
- *   workspace         caller-owned, kda_beam_workspace_size(N, W, V, k) bytes, 256-byte aligned
+ *   workspace         caller-owned, kda_beam_workspace_size(N, W, V, k) bytes, 256-byte aligned.
+ *                     It serves smaller N, W, V and k too
  */
 size_t kda_beam_workspace_size(int64_t N, int64_t W, int64_t V, int64_t k);
 int kda_beam_select(const void *logits, int dtype, const float *scores, const int32_t *finished, int64_t eos,

@@ -148,3 +148,32 @@ def test_8_bit_output_of_the_norm_for_the_next_product():
     # half a step of 8 bits, 2^-4 of a value or 2^-10 of the scale, and of bf16
     assert bool(((a - b).abs() <= b.abs() * (2.0 ** -4 + 2.0 ** -7) + sc * 2.0 ** -10).all())
     assert not same(y, blank((1, 64, D), BF)) and pl.U == 2.0 ** -24
+
+
+def test_one_workspace_for_the_largest_call_serves_smaller_ones():
+    g = torch.Generator().manual_seed(5)
+    W, V, k = 8, 8192, 8
+    x, scores = gpu(normal(g, (64, W, V), BF, 3.0)), gpu(-torch.rand(64, W, generator=g))
+    ws = torch.full((kda.beam_workspace_size(64, W, V, k),), 255, dtype=torch.uint8, device=dev())
+    for N in (64, 63, 5, 1):
+        out = []
+        for w in (None, ws):
+            t, p, s = (torch.zeros(N, k, dtype=d, device=dev()) for d in (torch.int32, torch.int32, F))
+            kda.beam_select(x[:N], scores[:N], t, p, s, workspace=w)
+            out.append((t, p, s))
+        assert all(torch.equal(a, b) for a, b in zip(*out)), N
+    T, D, E = 17000, 64, 4
+    x, dt, dy, B, C = (gpu(normal(g, (1, T, d), BF)) for d in (D, D, D, E, E))
+    A = gpu(-torch.rand(D, E, generator=g))
+    wf, wb = (torch.full((kda.ssm_workspace_size(1, T, D, E, backward=b),), 255, dtype=torch.uint8, device=dev()) for b in (False, True))
+    for n in (T, 16384, 8256, 8192, 8000, 64, 1):
+        say("workspace", n)
+        i = [t[:, :n].contiguous() for t in (x, dt, dy)] + [t[:, :n].unsqueeze(2).contiguous() for t in (B, C)]
+        out = []
+        for f, b in ((None, None), (wf, wb)):
+            carry = blank(kda.ssm_carry_shape(1, n, D, E))
+            o = [blank(i[0].shape, BF), blank(i[0].shape, BF), blank(i[0].shape, BF), blank(A.shape), blank(i[3].shape, BF), blank(i[3].shape, BF)]
+            kda.ssm_fwd(i[0], i[1], A, i[3], i[4], o[0], carry=carry, workspace=f)
+            kda.ssm_bwd(i[0], i[1], A, i[3], i[4], i[2], carry, *o[1:], workspace=b)
+            out.append(o)
+        assert all(same(a, b) for a, b in zip(*out)), n

@@ -229,3 +229,26 @@ def test_wrappers_check_before_the_device():
         kda.cache_reorder(x, x, x, x)
     with pytest.raises(TypeError):
         kda.conv_step([1.0], None, None, None, None, None, None)
+
+
+def test_workspaces_serve_smaller_calls():
+    """Sizes do not fall where a call grows: what is kept for the largest batch or prompt is enough for
+    every smaller one."""
+    def grows(f, sizes):
+        got = [f(n) for n in sizes]
+        assert got == sorted(got), [(n, a, b) for n, a, b in zip(sizes[1:], got, got[1:]) if b < a][:3]
+    for W, V, k in ((8, 8192, 8), (1, 131072, 64), (64, 100, 3), (11, 586, 11), (4, 32003, 4)):
+        grows(lambda n: kda.beam_workspace_size(n, W, V, k), range(0, 700))
+    for N, V in ((1, 3000), (9, 60000), (300, 9000)):
+        grows(lambda w: kda.beam_workspace_size(N, w, V, 8), range(1, 65))
+    for N, W in ((1, 4), (8, 8), (70, 8)):
+        grows(lambda v: kda.beam_workspace_size(N, W, v, 8), range(1, 200000, 997))
+        grows(lambda k: kda.beam_workspace_size(N, W, 9001, k), range(1, 65))
+    tokens = [*range(0, 2000, 7), *range(2000, 60000, 61)]
+    for backward in (False, True):
+        for D, E, G in ((8192, 16, 1), (1024, 16, 1), (4096, 16, 4), (24, 8, 3), (130, 64, 1), (6, 2, 6)):
+            grows(lambda t: kda.ssm_workspace_size(1, t, D, E, G, 3, backward), tokens)
+            grows(lambda b: kda.ssm_workspace_size(b, 900, D, E, G, 0, backward), range(1, 70))
+    for D in (1, 3, 8, 100, 1024, 8192):
+        grows(lambda t: kda.conv_workspace_size(1, t, D, 4), tokens)
+        grows(lambda m: kda.rmsnorm_workspace_size(m, D), range(0, 3000, 13))
