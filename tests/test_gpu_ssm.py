@@ -354,3 +354,50 @@ def test_growing_decays_of_states_that_are_small(T):
     i["x"][0, 5:] = 0
     i["dy"][0, :T - 5] = 0
     compare(both(i, n), plain(i, [(0, T)], softplus=False))
+
+
+# chunks of several 64-token blocks in both directions: long packed batches, and wide ones (of narrow
+# groups), where each workgroup's share of the channels is small
+LONG = [(1, 17000, 16, 4, 1, None), (1, 17000, 16, 4, 1, [0, 5, 4000, 4000, 9000, 9001, 16999]), (2, 384, 1024, 4, 1024, None),
+        (1, 800, 1024, 3, 1024, [3, 70, 333, 700]), (1, 4200, 256, 4, 128, [0, 1500, 1500, 4111]), (1, 2100, 520, 9, 260, None)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=str)
+@pytest.mark.parametrize("B,T,D,E,G,bounds", LONG)
+def test_chunks_of_several_blocks(B, T, D, E, G, bounds, dtype):
+    say("ssm long", B, T, D, E, G, bounds, dtype)
+    i, n = make(B, T, D, E, G, bounds, dtype, F, 15)
+    i["A"][:, ::2] *= 0.01   # states that last over many chunks beside those that do not
+    sp = spans_of(bounds, B, T)
+    rows, cu = covered(sp, B * T), cu_of(bounds)
+    want = plain(i, sp)
+    j = {a: gpu(t) for a, t in i.items()}
+    y, fin, carry = forward(j, cu, n, F)
+    got = {"y": y, "final": fin, **backward(j, cu, n, carry)}
+    assert set(got) == set(want)
+    for name, t in got.items():
+        t = t.cpu()
+        if name in TOKENS:
+            t = t.reshape(-1, *t.shape[2:])
+            pl.near(name, t, want[name], rows)
+            untouched(name, t, rows)
+        else:
+            pl.near(name, t, want[name])
+    st, y2 = j["h0"].clone(), blank(y.shape, dtype)   # the final states over the initial ones
+    kda.ssm_fwd(j["x"], j["dt"], j["A"], j["B"], j["C"], y2, D=j["skip"], z=j["z"], dt_bias=j["bias"], initial_state=st, final_state=st,
+                cu_seqlens=cu)
+    assert same(y, y2) and same(fin, st)
+
+
+@pytest.mark.parametrize("B,T,D,E,G,bounds", LONG)
+def test_sums_over_chunks_of_several_blocks(B, T, D, E, G, bounds):
+    """d_D is the sum of dy x (without z): of whole numbers it is exact, and every token counts once."""
+    i, n = make(B, T, D, E, G, bounds, F, None, 16)
+    g = torch.Generator().manual_seed(17)
+    i["x"], i["dy"] = (torch.randint(-3, 4, (B, T, D), generator=g).float() for _ in range(2))
+    i["z"] = None
+    rows, cu = covered(spans_of(bounds, B, T), B * T), cu_of(bounds)
+    j = {a: gpu(t) for a, t in i.items()}
+    carry = forward(j, cu, n, None)[2]
+    got = backward(j, cu, n, carry)["dskip"].cpu()
+    assert torch.equal(got.double(), (i["x"] * i["dy"]).double().reshape(-1, D)[rows].sum(0))
