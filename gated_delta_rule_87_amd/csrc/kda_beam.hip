@@ -8,7 +8,8 @@
 // Their time goes to the exponentials and to the steps that a workgroup takes one after the other
 // (256 beams of 131072 bf16 logits: 54 us, of which reading is 13). Scores of different beams lie
 // close together and their order is the result, so sums and scores are 64 bits (an fp64 operation
-// takes twice an fp32 one's time here; the exponential of 18 of them is good to 1e-11).
+// takes twice an fp32 one's time here; the exponential of 18 of them is good to 1e-11, so beams
+// closer than that may change places).
 //
 // The best k are found by counting, not by sorting: the 256 lanes form k' >= k groups, each with
 // its best element, and the least of those k' is a threshold that at least k elements reach, about
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(256) void kda_beam_join_kernel(BeamParams p, BeamWs
   __syncthreads();
   // the pieces' best ones first, then their second ones: neighbouring lanes, and so all groups of a
   // threshold, have candidates of the same rank (in the order of the pieces, where a lane's group was
-  // the rank, the kernel took 31 us at 32 x 8 beams and not 14)
+  // the rank, the kernel took 31 us at 32 x 8 beams and not 11)
   const int lists = p.W * w.pieces, total = lists * p.k;
   auto score = [&](int b, float x) { return ordered((((double)x - s_top[b]) - s_log[b]) + s_score[b]); };
   uint64_t lost = 0;   // best score at the end of a list that may have left out others with it

@@ -3,17 +3,19 @@
 //
 //     u_t = bias + sum_j w[j] x_{t-W+1+j},   y_t = u_t or u_t sigmoid(u_t)
 //
-// Bound by memory: x is read and y written once (8192 tokens x 8192 channels bf16: 67 us, 4.0 TB/s;
+// Bound by memory: x is read and y written once (8192 tokens x 8192 channels bf16: 70 us, 3.9 TB/s;
 // backward, 26810 x 1024 with 32 sequences, 54 us). A lane takes 16 bytes of channels of a run of
 // consecutive tokens and keeps the last W - 1 inputs in registers, so a run costs W - 1 tokens
-// read twice (from the caches: its neighbours read them too). The next 8 tokens are loaded while
-// 8 are computed. A sequence's first token puts the initial state, or zeros, into those
-// registers.
+// read twice (from the caches: its neighbours read them too). Forward, the next 8 tokens are loaded
+// while 8 are computed, in runs of more than 8: a run is 32 tokens, or half and a quarter of that
+// where longer ones would leave less than 1024 workgroups (8 at 26810 x 1024: 38 us). A sequence's
+// first token puts the initial state, or zeros, into those registers.
 //
 // Backward, with du = dy SiLU'(u) recomputed from x: an input gets w[W-1-o] du_{t+o} from the
 // output o tokens after it, so a lane also keeps W - 1 unfinished sums, and reads W - 1 tokens
-// past its run. The weight's sums stay in registers over all of a lane's runs, are added up over
-// the workgroup, and a second kernel adds the workgroups' sums in a fixed order.
+// past its run; it loads 4 tokens, then computes them. The weight's sums stay in registers over all
+// of a lane's runs, are added up over the workgroup, and a second kernel adds the workgroups' sums in
+// a fixed order.
 //
 // States are written by workgroups of their own, a lane all of a sequence's state after it has read
 // all of it; where final_state is initial_state, in a launch after the one that reads it.

@@ -558,7 +558,7 @@ struct Shape {
 
 // f(shape) for the fewest lanes, and vectors of a lane, that hold a row; false: none does. Few
 // vectors leave registers for more rows at once.
-template <int DT, bool BWD, bool E, typename F>
+template <int DT, bool E, typename F>
 bool by_width_of(int32_t D, F f) {
   constexpr int V = vec_of<DT>(), LEAST = BLOCK / V;   // lanes that hold what has one scale
   if (D <= LEAST * V) f(Shape<E, LEAST, 1, 2>{});
@@ -576,9 +576,9 @@ bool by_width_of(int32_t D, F f) {
   }
   return true;
 }
-template <int DT, bool BWD, typename F>
+template <int DT, typename F>
 bool by_width(int32_t D, F f) {
-  return D % vec_of<DT>() == 0 ? by_width_of<DT, BWD, true>(D, f) : by_width_of<DT, BWD, false>(D, f);
+  return D % vec_of<DT>() == 0 ? by_width_of<DT, true>(D, f) : by_width_of<DT, false>(D, f);
 }
 template <typename F>
 void by_dtype(int dt, F f) {
@@ -590,7 +590,7 @@ unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : mos
 
 template <int DT, int GROUP>
 void forward(const RmsParams& p, hipStream_t stream) {
-  const bool done = by_width<DT, false>(p.D, [&](auto shape) {
+  const bool done = by_width<DT>(p.D, [&](auto shape) {
     using S = decltype(shape);
     constexpr int wg = wg_of(S::lanes), step = wg / S::lanes * S::rows;
     hipLaunchKernelGGL((kda_rmsnorm_fwd_kernel<DT, S::exact, S::lanes, S::nv, S::rows, GROUP>),
@@ -624,7 +624,7 @@ hipError_t launch_rmsnorm_bwd(const RmsParams& p, hipStream_t stream) {
   if (p.M > 0) {
     by_dtype(p.dtype, [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
-      const bool done = by_width<DT, true>(p.D, [&](auto shape) {
+      const bool done = by_width<DT>(p.D, [&](auto shape) {
         using S = decltype(shape);
         constexpr int wg = wg_of(S::lanes), step = wg / S::lanes * S::rows;
         parts = (int)at_most((p.M + step - 1) / step, parts < 256 * 1024 / wg ? parts : 256 * 1024 / wg);

@@ -369,10 +369,10 @@ __device__ __forceinline__ float quad_sums(const float (&v)[4], bool odd, bool h
   return (high ? b : a) + moved<0x4E>(high ? a : b);
 }
 
-// SUB tokens' rows of the table in shared memory, two of them in turn; one wave, so no barriers
-template <int S, int SUB>
+// ROWS tokens' rows of the table in shared memory, two of them in turn; one wave, so no barriers
+template <int S, int ROWS>
 struct Rows {
-  static constexpr int EP = 4 * S, N = SUB * 2 * EP / 4, K = (N + 63) / 64;   // 16-byte pieces, of a lane
+  static constexpr int EP = 4 * S, N = ROWS * 2 * EP / 4, K = (N + 63) / 64;   // 16-byte pieces, of a lane
   f32x4 r[K];
   __device__ __forceinline__ void load(const float* table, int32_t t, int32_t end, int lane) {
 #pragma unroll
@@ -627,7 +627,7 @@ __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmParams p, SsmWs w)
   float A[4];
   T.load4(p, p.A, 0, A);
   const float bias = p.dt_bias ? p.dt_bias[T.d] : 0.0f, skip = p.skip ? p.skip[T.d] : 0.0f;
-    for (int n = blockIdx.x / w.tiles; n < p.nseq; n += gridDim.x / w.tiles) {
+  for (int n = blockIdx.x / w.tiles; n < p.nseq; n += gridDim.x / w.tiles) {
     const int from = p.in_slots[n], to = p.out_slots[n];
     const size_t i = (size_t)n * p.D + T.d, bc = ((size_t)n * p.G + T.g) * p.E + T.e0;
     float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {}, c[4] = {}, x, dt, z = 0.0f, y = 0.0f;
@@ -1083,7 +1083,7 @@ void by_states(int S, F f) {
   else if (S == 8) f(integral_constant<int, 8>{});
   else f(integral_constant<int, 16>{});
 }
-template <int DT, typename F>
+template <typename F>
 void by_lanes(int lpc, F f) {
   if (lpc == 2) f(integral_constant<int, 2>{});
   else if (lpc == 4) f(integral_constant<int, 4>{});
@@ -1146,7 +1146,7 @@ hipError_t launch_ssm_step(const SsmParams& p, hipStream_t stream) {
   const int64_t most = 16384 / w.tiles + 1, rows = p.nseq < most ? p.nseq : most;
   by_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    by_lanes<DT>(lanes_of(p.E, false), [&](auto lpc) {
+    by_lanes(lanes_of(p.E, false), [&](auto lpc) {
       hipLaunchKernelGGL((kda_ssm_step_kernel<DT, decltype(lpc)::value>), dim3((unsigned)(rows * w.tiles)), dim3(256), 0, stream, p, w);
     });
   });
