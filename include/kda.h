@@ -486,7 +486,8 @@ int kda_layernorm_bwd(const void *dy, const void *x, const float *weight, const 
  *   y, y_dtype        [M, D] in `dtype`, or in KDA_E4M3 with scales
  *   scales, group     fp32 [M, ceil(D / group)] with KDA_E4M3, else NULL and 0: y holds what
  *                     the values are in units of their scale, the largest of the group's
- *                     |values| / 448, or 1 where that is 0. (A NaN in a group makes its scale
+ *                     |values| / 448, or 1 where that is 0. (Quotients by a scale that fp32
+ *                     holds in a few bits, below 1e-38, end at 448. A NaN in a group makes its scale
  *                     NaN; an infinity makes it infinite, and finite values 0 beside it.) A
  *                     group is 128 neighbouring
  *                     elements (the row's last one the rest), or the row: group is 128 or D.
@@ -588,7 +589,8 @@ int kda_conv_step(const void *x, const float *weight, const float *bias, void *y
  *   workspace         caller-owned, kda_ssm_workspace_size(B, T, D, E, G, N, backward) bytes (N = 0
  *                     without cu_seqlens; backward: 0 or 1, the direction), 256-byte aligned;
  *                     contents need no initialisation and are clobbered. It serves fewer tokens too
- * Outputs do not overlap inputs, except as said. D is 1 to 2^20.
+ * Outputs do not overlap inputs, except as said. D is 1 to 2^20. (64 channels of one group are
+ * taken at once: groups of fewer channels take as long as 64 would.)
  *
  * kda_ssm_step: one token for each of N sequences, x, dt, z, y [N, D], Bm, Cm [N, G, E],
  * states in the slots of a cache's layer [S, D, E] by the rules of kda_glr_step.
@@ -617,7 +619,9 @@ int kda_ssm_step(const void *x, const void *dt, const float *A, const void *Bm, 
  * kda_beam_select -- the k best continuations of every sequence's W beams. Continuation v of
  * beam b of sequence n has the score
  *     scores[n][b] + logits[n][b][v] - log(sum over v' of exp(logits[n][b][v']))
- * computed in 64 bits; the best come first, equal ones in the order of b, then v. A beam with
+ * computed in 64 bits (an exponential to 1e-11: beams whose scores are closer than that may
+ * change places); the best come first, equal ones (-0.0 and +0.0 among them, and logits that
+ * 64 bits of a score swallow) in the order of b, then v. A beam with
  * finished[n][b] != 0 has one continuation, v = eos, at its score as it is (its logits are
  * not read). Only finite scores count: a logit of -infinity is no continuation, and a beam
  * with a NaN or +infinite logit, or whose score is infinite or NaN, has none.
